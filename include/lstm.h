@@ -79,7 +79,7 @@ enum { LSTM_F32 = 0, LSTM_BF16 = 1, LSTM_F16 = 2 };
 enum {
   LSTM_OK = 0,
   LSTM_ERR_NULL = -1,        /* a required pointer is NULL */
-  LSTM_ERR_DIMS = -2,        /* T, B or I < 0, or H <= 0 */
+  LSTM_ERR_DIMS = -2,        /* T, B or I < 0, or H <= 0; a size, stride or count another call states */
   LSTM_ERR_DTYPE = -3,       /* dtype is not LSTM_F32 / LSTM_BF16 / LSTM_F16, or an unknown flag is set */
   LSTM_ERR_ALIGN = -4,       /* a tensor is not aligned to its element size, or the workspace to 256 B */
   LSTM_ERR_WORKSPACE = -5,   /* workspace_bytes < lstm_query() */
@@ -271,6 +271,7 @@ int lstm_check_workspace(void* workspace, size_t workspace_bytes, void* stream);
  *   3 dW product (with its split-K sum and the final db sum)   4 dx product
  *   5 direction copies (LSTM_BIDIRECTIONAL: y joined, dy split)
  *   6 state copies of the T = 0 / B = 0 cases
+ *   7 embedding   8 cross attention   9 log probabilities
  * lstm_timing_enable(1) also resets the totals.  lstm_timing_read() waits for
  * the recorded events and returns the total milliseconds and the launch
  * count of one kind.  Not thread-safe; timing adds a few microseconds per
@@ -322,6 +323,90 @@ int lstm_stack_bwd(const lstm_shape* shape, int64_t layers, int64_t chunks, cons
                    const void* dcT, const void* x, const void* W, const void* h0, const void* c0, const void* y,
                    void* workspace, size_t workspace_bytes, void* dx, void* dW, void* db, void* dh0, void* dc0,
                    void* stream);
+
+/* ---- Sequence-to-sequence operators --------------------------------------
+ * What stands around the LSTM layers in an encoder-decoder model: tokens to
+ * x (lstm_embed_*), the decoder's attention over the encoder's states
+ * (lstm_attend_*), and logits to log probabilities (lstm_logprob_*).  The
+ * conventions are those of the layer calls: the caller owns every buffer,
+ * launches are asynchronous on `stream`, outputs are overwritten, argument
+ * checks come before any launch, one storage type per call with fp32 sums,
+ * repeated calls give the same bits.  A dimension of 0 is a valid call. */
+
+/* Type of token ids. */
+enum { LSTM_I32 = 0, LSTM_I64 = 1 };
+
+/* Embedding of N tokens by a table of V rows of D values (row strides in
+ * elements, >= D):
+ *   out[n][:]    = scale * table[ids[n]][:]     (an id outside [0, V): zeros)
+ *   dtable[v][:] = scale * sum over { n : ids[n] = v } of dout[n][:]
+ * dtable is written whole (rows of no token are zeros); the row `padding`
+ * (-1: none) is read like any other and takes no gradient, nor does an id
+ * outside [0, V).  The sum of a row runs over n in a fixed order in fp32 and
+ * is rounded once.  N, V < 2^26, D <= 2^20.  With [T][B] ids, out is
+ * the x [T][B][I = D] of lstm_fwd_train() and dout its dx. */
+typedef struct {
+  int64_t N, V, D;
+  int64_t ld_table; /* elements between rows of table, and of dtable */
+  int64_t ld_out;   /* elements between rows of out, and of dout */
+  int64_t padding;
+  float scale;
+  int32_t dtype;    /* LSTM_F32 / BF16 / F16 */
+  int32_t id_type;  /* LSTM_I32 / I64 */
+} lstm_embed_shape;
+
+/* Workspace of lstm_embed_bwd (256-byte aligned, opaque, no state between
+ * calls). */
+int lstm_embed_query(const lstm_embed_shape* shape, size_t* workspace_bytes);
+int lstm_embed_fwd(const lstm_embed_shape* shape, const void* ids, const void* table, void* out, void* stream);
+int lstm_embed_bwd(const lstm_embed_shape* shape, const void* ids, const void* dout, void* workspace,
+                   size_t workspace_bytes, void* dtable, void* stream);
+
+/* Log probabilities of N rows of V logits (row stride ld >= V), z = scale *
+ * logit with scale > 0 (an inverse temperature):
+ *   lse[n]     = log sum_v exp z[n][v]
+ *   logp[n]    = z[n][targets[n]] - lse[n]     (a target outside [0, V): 0)
+ *   entropy[n] = -sum_v p log p, p = exp(z - lse)   (0 where p = 0)
+ *   top_ids[n][k], top_logp[n][k], k < top: the largest logits in descending
+ *     order, equal ones by the lower id, and their z - lse
+ * and, with the cotangents dlogp, dentropy [N], dtop [N][top] (each may be
+ * NULL = zero), the logits' gradient (row stride ld_grad >= V)
+ *   dlogits[n][v] = scale * ( [v = target] dlogp + sum_k [v = top_ids[k]] dtop[k]
+ *                    - p_v (dlogp + sum_k dtop[k])
+ *                    - dentropy p_v (log p_v + entropy) )
+ * (a target outside [0, V) has no dlogp).  logits and dlogits have the
+ * storage type; lse, logp, entropy, top_logp and the cotangents are fp32;
+ * targets and top_ids have id_type.  Logits of -inf are banned tokens: p =
+ * 0, no gradient.  A row of nothing but -inf has lse = logp = top_logp =
+ * -inf (logp of a target outside [0, V) stays 0), entropy 0 and no gradient.
+ * A NaN or +inf in a row makes its sums NaN.  0 <= top <= LSTM_MAX_TOP,
+ * top <= V; N < 2^24, V < 2^30, and N V < 2^37. */
+#define LSTM_MAX_TOP 32
+typedef struct {
+  int64_t N, V;
+  int64_t ld, ld_grad;
+  float scale;
+  int32_t top;
+  int32_t dtype;
+  int32_t id_type;
+} lstm_logprob_shape;
+
+/* record [N][2]: required; receives a reference m near the row's largest
+ * logit (-inf: a row of nothing but -inf) and log sum_v exp(scale (x_v - m)),
+ * which log p = scale (x - m) - that sum needs where lse = scale m + that sum
+ * has been rounded.  lse, logp (needs targets), entropy: each optional (NULL =
+ * not computed); top > 0 needs top_logp and top_ids.  Workspace:
+ * lstm_logprob_query() bytes, 256-byte aligned (may be 0: workspace NULL). */
+int lstm_logprob_query(const lstm_logprob_shape* shape, size_t* workspace_bytes);
+int lstm_logprob_fwd(const lstm_logprob_shape* shape, const void* logits, const void* targets, void* workspace,
+                     size_t workspace_bytes, float* record, float* lse, float* logp, float* entropy, float* top_logp,
+                     void* top_ids, void* stream);
+/* record, entropy (needed with dentropy), top_ids (needed with dtop) as the
+ * forward wrote them; targets needed with dlogp.  dlogits may be logits
+ * itself (ld = ld_grad). */
+int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const void* targets, const float* record,
+                     const float* entropy, const void* top_ids, const float* dlogp, const float* dentropy,
+                     const float* dtop, void* dlogits, void* stream);
 
 /* The floor under a recurrence step, for measurement: runs the forward
  * recurrence's per-step exchange alone -- the step flags of the batch group,

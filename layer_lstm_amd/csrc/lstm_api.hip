@@ -23,7 +23,7 @@ static int g_fail_step = -1, g_misplace = 0;
 constexpr int kMaxDevices = 64;
 static bool g_spread_only[kMaxDevices];
 
-static int device_cus(int* cus, int* devp = nullptr) {
+int device_cus(int* cus, int* devp) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return LSTM_ERR_DEVICE;
   if (devp) *devp = dev;
@@ -245,7 +245,7 @@ static int status_of(hipError_t e) {
 static bool misaligned(const void* ptr, int esize) { return ptr && ((uintptr_t)ptr % (uintptr_t)esize) != 0; }
 
 // ---- per-kernel event timing (lstm_timing_enable / lstm_timing_read) ----
-enum { kKinds = 7 };
+enum { kKinds = 10 };
 struct Pending { int kind; hipEvent_t a, b; };
 static bool g_timing_on = false;
 static std::vector<Pending> g_pending;
@@ -344,7 +344,7 @@ const char* lstm_status_string(int status) {
   switch (status) {
     case LSTM_OK: return "ok";
     case LSTM_ERR_NULL: return "a required pointer is NULL";
-    case LSTM_ERR_DIMS: return "invalid dimensions (T, B, I < 0 or H <= 0)";
+    case LSTM_ERR_DIMS: return "invalid dimensions (T, B, I < 0 or H <= 0, or a size, stride or count outside its range)";
     case LSTM_ERR_DTYPE: return "unsupported dtype, unknown flag or invalid flag combination";
     case LSTM_ERR_ALIGN: return "misaligned pointer";
     case LSTM_ERR_WORKSPACE: return "workspace too small";

@@ -27,6 +27,8 @@ GATES_IJFO = 2  # lstm_shape.flags: W/b/dW/db row blocks in the gate order i, g,
 TWO_BIAS = 4  # lstm_shape.flags: b and db are [2][4H] (b_ih, b_hh)
 BIDIRECTIONAL = 8  # lstm_shape.flags: both directions of time, outputs side by side
 GATE_I, GATE_F, GATE_G, GATE_O = 0, 1, 2, 3
+I32, I64 = 0, 1  # id_type of token ids
+MAX_TOP = 32  # LSTM_MAX_TOP
 F32, BF16, F16 = 0, 1, 2
 OK = 0
 STATUS = {0: "OK", -1: "ERR_NULL", -2: "ERR_DIMS", -3: "ERR_DTYPE", -4: "ERR_ALIGN",
@@ -40,10 +42,11 @@ SCRATCH_BYTES = 64 << 20  # LSTM_SCRATCH_BYTES
 EXPORTS = ("lstm_abi_version", "lstm_status_string", "lstm_query", "lstm_query_plan", "lstm_fwd_train",
            "lstm_fwd_train_scratch", "lstm_bwd", "lstm_check_workspace", "lstm_timing_enable", "lstm_timing_read",
            "lstm_stamps_set", "lstm_probe_exchange", "lstm_probe_mfma_stage", "lstm_debug_inject", "lstm_stack_query",
-           "lstm_stack_fwd_train", "lstm_stack_bwd")
+           "lstm_stack_fwd_train", "lstm_stack_bwd", "lstm_embed_query", "lstm_embed_fwd", "lstm_embed_bwd",
+           "lstm_logprob_query", "lstm_logprob_fwd", "lstm_logprob_bwd")
 STAMP_WGS, STAMP_POINTS = 8, 6
 KERNEL_KINDS = ("input_projection", "forward_recurrence", "backward_recurrence", "dW_product",
-                "dx_product", "direction_copy", "state_copy")
+                "dx_product", "direction_copy", "state_copy", "embedding", "cross_attention", "log_probability")
 
 
 class Shape(ctypes.Structure):
@@ -56,6 +59,16 @@ class PlanInfo(ctypes.Structure):
                                                "grid", "waves", "xcd_local", "fwd_valu", "bwd_valu",
                                                "inproj_tiles_per_wg", "directions_concurrent", "fwd_tagged")] + \
                [("reserved", ctypes.c_int32 * 4)]
+
+
+class EmbedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("N", "V", "D", "ld_table", "ld_out", "padding")] + \
+               [("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("id_type", ctypes.c_int32)]
+
+
+class LogprobShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("N", "V", "ld", "ld_grad")] + \
+               [("scale", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("top", "dtype", "id_type")]
 
 
 _P = ctypes.c_void_p
@@ -93,6 +106,14 @@ _lib.lstm_stack_fwd_train.argtypes = [ctypes.POINTER(Shape), ctypes.c_int64, cty
 _lib.lstm_stack_bwd.restype = ctypes.c_int
 _lib.lstm_stack_bwd.argtypes = [ctypes.POINTER(Shape), ctypes.c_int64, ctypes.c_int64] + [_P] * 8 + \
     [_P, ctypes.c_size_t] + [_P] * 5 + [_P]
+for _n, _a in (("lstm_embed_query", [ctypes.POINTER(EmbedShape), ctypes.POINTER(ctypes.c_size_t)]),
+               ("lstm_embed_fwd", [ctypes.POINTER(EmbedShape)] + [_P] * 4),
+               ("lstm_embed_bwd", [ctypes.POINTER(EmbedShape)] + [_P] * 3 + [ctypes.c_size_t] + [_P] * 2),
+               ("lstm_logprob_query", [ctypes.POINTER(LogprobShape), ctypes.POINTER(ctypes.c_size_t)]),
+               ("lstm_logprob_fwd", [ctypes.POINTER(LogprobShape)] + [_P] * 3 + [ctypes.c_size_t] + [_P] * 7),
+               ("lstm_logprob_bwd", [ctypes.POINTER(LogprobShape)] + [_P] * 10)):
+    getattr(_lib, _n).restype = ctypes.c_int
+    getattr(_lib, _n).argtypes = _a
 _lib.lstm_debug_inject.restype = ctypes.c_int
 _lib.lstm_debug_inject.argtypes = [ctypes.c_int, ctypes.c_int64]
 _lib.lstm_stamps_set.restype = ctypes.c_int
@@ -355,3 +376,124 @@ class Stack:
         rc = check_workspace(self.workspace, stream)
         if rc != OK:
             raise LstmError(rc, "lstm_check_workspace")
+
+
+# --- sequence-to-sequence operators -------------------------------------------
+def _workspace(fn, name, shape, device):
+    n = ctypes.c_size_t(0)
+    rc = fn(ctypes.byref(shape), ctypes.byref(n))
+    if rc != OK:
+        raise LstmError(rc, name)
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class Embedding:
+    """The embedding of N tokens by a [V, D] table (lstm_embed_*), with its
+    workspace and output buffers on the current device.  `ids`: N tokens,
+    int32 or int64, of any shape, contiguous; the rows of `table` and `dout`
+    may be strided (D contiguous).  `padding`: an id whose row takes no
+    gradient."""
+
+    def __init__(self, N, V, D, dtype=F32, scale=1.0, padding=None, device="cuda"):
+        self.N, self.V, self.D, self.dtype, self.device = N, V, D, dtype, device
+        self.shape = EmbedShape(N, V, D, D, D, -1 if padding is None else int(padding), float(scale), int(dtype), I64)
+        self.workspace = _workspace(_lib.lstm_embed_query, "lstm_embed_query", self.shape, device)
+        self.tdtype = torch_dtype(dtype)
+        self.out = self.dtable = None
+
+    def _ids(self, ids):
+        _need(ids.numel() == self.N and ids.is_contiguous(), f"ids: {self.N} contiguous tokens")
+        _need(ids.dtype in (torch.int64, torch.int32), "ids: int32 or int64")
+        self.shape.id_type = I64 if ids.dtype == torch.int64 else I32
+        return ids
+
+    def forward(self, ids, table, stream=None):
+        """out [*ids.shape, D] = scale * table[ids]."""
+        self._ids(ids)
+        _need(table.dtype == self.tdtype and table.shape == (self.V, self.D) and (self.D <= 1 or table.stride(1) == 1),
+              f"table: [{self.V}, {self.D}] of {self.tdtype}, rows contiguous")
+        if self.out is None or self.out.shape[:-1] != ids.shape:
+            self.out = torch.empty((*ids.shape, self.D), dtype=self.tdtype, device=self.device)
+        self.shape.ld_table, self.shape.ld_out = max(table.stride(0), self.D), self.D
+        rc = _lib.lstm_embed_fwd(ctypes.byref(self.shape), _ptr(ids), _ptr(table), _ptr(self.out), _stream(stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_embed_fwd")
+        return self.out
+
+    def backward(self, ids, dout, stream=None):
+        """dtable [V, D] of dout [*ids.shape, D]."""
+        self._ids(ids)
+        _need(dout.dtype == self.tdtype and dout.shape == (*ids.shape, self.D),
+              f"dout: {[*ids.shape, self.D]} of {self.tdtype}")
+        rows = dout if dout.dim() == 2 else dout.view(self.N, self.D)
+        _need(self.D <= 1 or rows.stride(1) == 1, "dout: rows contiguous")
+        if self.dtable is None:
+            self.dtable = torch.empty((self.V, self.D), dtype=self.tdtype, device=self.device)
+        self.shape.ld_table, self.shape.ld_out = self.D, max(rows.stride(0), self.D)
+        rc = _lib.lstm_embed_bwd(ctypes.byref(self.shape), _ptr(ids), _ptr(rows), _ptr(self.workspace),
+                                 self.workspace.numel(), _ptr(self.dtable), _stream(stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_embed_bwd")
+        return self.dtable
+
+
+class LogProb:
+    """Log probabilities of given tokens under N rows of V logits, entropies
+    and the `top` best alternatives (lstm_logprob_*), with workspace and
+    output buffers on the current device.  logits [N, V] (rows may be
+    strided), targets [N] int32 or int64."""
+
+    def __init__(self, N, V, dtype=F32, top=0, scale=1.0, device="cuda"):
+        self.N, self.V, self.top, self.dtype, self.device = N, V, int(top), dtype, device
+        self.shape = LogprobShape(N, V, V, V, float(scale), int(top), int(dtype), I64)
+        self.workspace = _workspace(_lib.lstm_logprob_query, "lstm_logprob_query", self.shape, device)
+        self.tdtype = torch_dtype(dtype)
+        self.record = torch.empty((N, 2), dtype=torch.float32, device=device)
+        self.lse, self.logp, self.entropy = (torch.empty(N, dtype=torch.float32, device=device) for _ in range(3))
+        self.top_logp = torch.empty((N, self.top), dtype=torch.float32, device=device)
+        self.top_ids = self.dlogits = None
+
+    def _rows(self, logits, targets):
+        _need(logits.dtype == self.tdtype and logits.shape == (self.N, self.V) and
+              (self.V <= 1 or logits.stride(1) == 1), f"logits: [{self.N}, {self.V}] of {self.tdtype}, rows contiguous")
+        _need(targets.shape == (self.N,) and targets.is_contiguous() and targets.dtype in (torch.int64, torch.int32),
+              f"targets: [{self.N}] int32 or int64, contiguous")
+        self.shape.id_type = I64 if targets.dtype == torch.int64 else I32
+        self.shape.ld = max(logits.stride(0), self.V)
+
+    def forward(self, logits, targets, stream=None):
+        """logp [N], entropy [N] and, with alternatives, top_logp and top_ids [N, top] (ids of targets' type)."""
+        self._rows(logits, targets)
+        if self.top_ids is None or self.top_ids.dtype != targets.dtype:
+            self.top_ids = torch.empty((self.N, self.top), dtype=targets.dtype, device=self.device)
+        rc = _lib.lstm_logprob_fwd(ctypes.byref(self.shape), _ptr(logits), _ptr(targets), _ptr(self.workspace),
+                                   self.workspace.numel(), _ptr(self.record), _ptr(self.lse), _ptr(self.logp),
+                                   _ptr(self.entropy), _ptr(self.top_logp), _ptr(self.top_ids), _stream(stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_logprob_fwd")
+        if not self.top:
+            return self.logp, self.entropy
+        return self.logp, self.entropy, self.top_logp, self.top_ids
+
+    def backward(self, logits, targets, dlogp=None, dentropy=None, dtop=None, stream=None):
+        """dlogits [N, V] after a forward on the same logits and targets; cotangents fp32, contiguous, None = zero."""
+        self._rows(logits, targets)
+        for name, g, shape in (("dlogp", dlogp, (self.N,)), ("dentropy", dentropy, (self.N,)),
+                               ("dtop", dtop, (self.N, self.top))):
+            _need(g is None or (g.dtype == torch.float32 and g.shape == shape and g.is_contiguous()),
+                  f"{name}: {list(shape)} of float32, contiguous")
+        _need(self.N == 0 or dtop is None or not self.top or self.top_ids is not None and
+              self.top_ids.dtype == targets.dtype, "backward follows a forward on the same targets")
+        if self.dlogits is None:
+            self.dlogits = torch.empty((self.N, self.V), dtype=self.tdtype, device=self.device)
+        rc = _lib.lstm_logprob_bwd(ctypes.byref(self.shape), _ptr(logits), _ptr(targets), _ptr(self.record),
+                                   _ptr(self.entropy), _ptr(self.top_ids), _ptr(dlogp), _ptr(dentropy),
+                                   _ptr(dtop) if self.top else None, _ptr(self.dlogits), _stream(stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_logprob_bwd")
+        return self.dlogits
