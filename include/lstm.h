@@ -362,6 +362,47 @@ int lstm_embed_fwd(const lstm_embed_shape* shape, const void* ids, const void* t
 int lstm_embed_bwd(const lstm_embed_shape* shape, const void* ids, const void* dout, void* workspace,
                    size_t workspace_bytes, void* dtable, void* stream);
 
+/* Cross attention of Tq queries to the Tk states of an encoder, for each of B
+ * sequences and Hq query heads, Hq / Hk of them sharing a key head (query
+ * head h reads key head h / (Hq / Hk)):
+ *   s = scale q . k over the valid keys,  p = softmax(s),  o = sum p v,
+ *   lse = log sum exp s
+ *   q, o, dout, dq: element (t, b, h, d), t < Tq, h < Hq, at t*stride.t +
+ *     b*stride.b + h*stride.h + d;  k, v, dk, dv: t < Tk, h < Hk; strides in
+ *     elements, >= 0, those of o, dq, dk, dv without overlap.  The dense time-
+ *     major [T][B][H][D] of the LSTM calls is {B*H*D, H*D, D}.
+ *   lse [B][Hq][Tq] fp32
+ * Valid keys of sequence b: t < k_length[b] (int32 [B], NULL = all; not
+ * clamped, see seq_length above) and key_mask[b*mask_b + t] != 0 (bytes [B]
+ * [Tk], NULL = all).  Rows of k and v that are not valid are not used: they
+ * may hold anything, infinities and NaN included.  A query with no valid key
+ * has o = 0, lse = -inf and no gradient; dk and dv of such keys are zeros.
+ * p enters sum p v rounded to the storage type, ds the products of dq and dk
+ * (the operands of the matrix cores); scores, sums and statistics are fp32.
+ * Any D in [1, 256], scale > 0; rows of whole aligned 16-byte chunks (t
+ * stride included) are the fast case. */
+typedef struct {
+  int64_t t, b, h;
+} lstm_stride;
+typedef struct {
+  int64_t Tq, Tk, B, Hq, Hk, D;
+  lstm_stride q, k, v, o;
+  lstm_stride dout, dq, dk, dv; /* lstm_attend_bwd only */
+  int64_t mask_b;               /* bytes between the sequences of key_mask */
+  float scale;
+  int32_t dtype;
+} lstm_attend_shape;
+
+/* Workspaces of the two calls (256-byte aligned, opaque, no state between
+ * calls; 0 bytes: NULL). */
+int lstm_attend_query(const lstm_attend_shape* shape, size_t* fwd_bytes, size_t* bwd_bytes);
+int lstm_attend_fwd(const lstm_attend_shape* shape, const void* q, const void* k, const void* v, const void* k_length,
+                    const void* key_mask, void* workspace, size_t workspace_bytes, void* o, float* lse, void* stream);
+/* o and lse as the forward wrote them.  dq, dk and dv are written whole. */
+int lstm_attend_bwd(const lstm_attend_shape* shape, const void* dout, const void* q, const void* k, const void* v,
+                    const void* k_length, const void* key_mask, const void* o, const float* lse, void* workspace,
+                    size_t workspace_bytes, void* dq, void* dk, void* dv, void* stream);
+
 /* Log probabilities of N rows of V logits (row stride ld >= V), z = scale *
  * logit with scale > 0 (an inverse temperature):
  *   lse[n]     = log sum_v exp z[n][v]

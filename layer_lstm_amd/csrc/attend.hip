@@ -1,0 +1,352 @@
+// attend.hip -- cross attention forward (gfx950).
+//
+//   s = scale q . k over the valid keys,  p = exp(s - lse),  o = sum p v
+//
+// A wave holds 32 query rows (attend_common.hpp) as one operand in registers
+// and walks over tiles of keys in LDS: S^T = K Q^T leaves row r of the tile's
+// scores down one lane's registers (and those of lane ^ 32), so the softmax
+// statistics are sums over a lane's own registers, and the rounded p are the
+// second operand of O^T += V^T P^T as they stand; neither S nor P touches
+// memory.  Scores are kept in powers of two, y = s log2 e - m, against a
+// reference m that moves only when a score passes it by more than kMaxLag
+// (2^kMaxLag times the largest p is no loss of precision in floating point);
+// most tiles rescale nothing.
+//
+// Two kernels.  attend_fwd_kernel: four waves of 32 rows share each tile of
+// keys, double-buffered, one barrier a tile.  attend_step_kernel: for few
+// rows (one token of each sequence): every wave walks over its own keys with
+// its own double buffer and no barrier, the keys split over the waves and
+// over `splits` work-groups, joined at the end -- there the keys' and values'
+// bytes are the bound.
+#include "attend_common.hpp"
+
+namespace lstm {
+
+constexpr float kMaxLag = 8.f;
+
+// One tile of 32 KT keys for a wave's 32 rows.
+template <typename T, int DP, int KT>
+__device__ __forceinline__ void attend_tile(const char* kt, const char* vt, uint64_t bits, const u32x4_t* q, f32x16_t* o,
+                                            float& m, float& l, float c2, int lane) {
+  using TL = Tile<T, DP>;
+  f32x16_t s[KT];
+#pragma unroll
+  for (int t = 0; t < KT; ++t) {
+    s[t] = zero16();
+#pragma unroll
+    for (int kb = 0; kb < TL::KB; ++kb) s[t] = Mm<T>::mac(TL::row_frag(kt, 32 * t, kb, lane), q[kb], s[t]);
+  }
+  constexpr uint64_t kAll = KT == 2 ? ~(uint64_t)0 : 0xffffffffull;
+  if ((bits & kAll) != kAll) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const uint32_t mine = (uint32_t)(bits >> (32 * t)) >> (4 * (lane >> 5));
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!((mine >> reg_row(i, 0)) & 1)) s[t][i] = -INFINITY;
+    }
+  }
+  float top = s[0][0];
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+  top = fmaxf(top, other_half(top)) * c2;
+  if (__ballot(top > m + kMaxLag)) {
+    const float to = fmaxf(m, top), by = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+    m = to;
+    l *= by;
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[dt][i] *= by;
+  }
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c2, -ref));
+      l += s[t][i];
+    }
+#pragma unroll
+  for (int t = 0; t < KT; ++t)
+#pragma unroll
+    for (int pb = 0; pb < TL::PB; ++pb) {
+      const u32x4_t p = TL::reg_frag(s[t], pb);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt)
+        o[dt] = Mm<T>::mac(TL::col_frag(vt, 32 * t + TL::KR * pb, dt, lane), p, o[dt]);
+    }
+}
+
+// Keys per tile of the shared kernel: two double-buffered tiles within 128 KB.
+template <typename T, int DP> constexpr int fwd_keys() { return 4 * 64 * Tile<T, DP>::C * 16 <= 128 * 1024 ? 64 : 32; }
+
+template <typename T, int DP, bool DMA>
+__global__ void __launch_bounds__(256, DP * sizeof(T) > 512 ? 1 : 2) attend_fwd_kernel(AttendArgs a) {
+  using TL = Tile<T, DP>;
+  constexpr int NK = fwd_keys<T, DP>(), TB = NK * TL::C * 16;
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // K, V tiles, twice
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int grp, tile;
+  if (!group_of(a, blockIdx.x, &grp, &tile)) return;
+  const int b = grp / a.Hk, hk = grp - b * a.Hk;
+  const int end = keys_of(a, b);
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_b : nullptr;
+  const uint32_t r = (uint32_t)tile * 128 + w * 32 + (lane & 31);
+  const bool ok = r < a.M;
+  const uint32_t t = r / a.G, h = hk * a.G + (r - t * a.G);
+
+  u32x4_t q[TL::KB];
+  load_row_frags<T, DP>((const T*)a.q + t * a.qs.t + b * a.qs.b + h * a.qs.h, a.D, a.whole & kWholeQ, ok, lane, q);
+  Loader<T, DP, NK, 4, DMA> lk, lv;
+  lk.init((const T*)a.k + b * a.ks.b + hk * a.ks.h, a.ks.t, a.D, a.whole & kWholeK, mask, w, lane);
+  lv.init((const T*)a.v + b * a.vs.b + hk * a.vs.h, a.vs.t, a.D, a.whole & kWholeV, mask, w, lane);
+
+  f32x16_t o[DP / 32];
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt) o[dt] = zero16();
+  float m = -INFINITY, l = 0.f;
+  const float c2 = a.scale * kLog2e;
+  const int n = (end + NK - 1) / NK;
+  if (n > 0) {
+    lk.load(0, end, lds);
+    lv.load(0, end, lds + TB);
+  }
+  uint64_t bits = key_bits(mask, 0, end, lane);
+  for (int i = 0; i < n; ++i) {
+    wait_vmem();
+    __syncthreads();
+    char* cur = lds + (i & 1) * 2 * TB;
+    char* nxt = lds + (~i & 1) * 2 * TB;
+    const uint64_t now = bits;
+    if (i + 1 < n) {
+      lk.load((i + 1) * NK, end, nxt);
+      lv.load((i + 1) * NK, end, nxt + TB);
+      bits = key_bits(mask, (i + 1) * NK, end, lane);
+    }
+    attend_tile<T, DP, NK / 32>(cur, cur + TB, now, q, o, m, l, c2, lane);
+  }
+  l += other_half(l);
+  if (!ok) return;
+  const float by = l == 0.f ? 0.f : 1.f / l;
+  store_col<T, DP>((T*)a.out + t * a.os.t + b * a.os.b + h * a.os.h, o, by, a.D, a.whole & kWholeO, lane);
+  if (lane < 32) a.lse[((int64_t)b * a.Hq + h) * a.Tq + t] = kLn2 * (m + __builtin_amdgcn_logf(l));
+}
+
+// ---------------------------------------------------------------------------
+// Few rows.  Waves of a work-group: as many as hold their two stages of a K
+// and a V tile of 32 keys in 128 KB.
+template <typename T, int DP> constexpr int step_waves() {
+  return Tile<T, DP>::kBytes32 * 4 * 4 <= 128 * 1024 ? 4 : Tile<T, DP>::kBytes32 * 4 * 2 <= 128 * 1024 ? 2 : 1;
+}
+
+template <typename T, int DP, bool DMA>
+__global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_step_kernel(AttendArgs a) {
+  using TL = Tile<T, DP>;
+  constexpr int NW = step_waves<T, DP>(), TB = TL::kBytes32;
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // per wave: K, V tiles, twice
+  __shared__ float wm[NW][32], wl[NW][32];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int grp, tile;
+  if (!group_of(a, blockIdx.x, &grp, &tile)) return;
+  const int rt = tile / a.splits, sp = tile - rt * a.splits;
+  const int b = grp / a.Hk, hk = grp - b * a.Hk;
+  const int end = keys_of(a, b);
+  const uint8_t* mask = a.mask ? a.mask + b * a.mask_b : nullptr;
+  const uint32_t r = (uint32_t)rt * 32 + (lane & 31);
+  const bool ok = r < a.M;
+  const uint32_t t = r / a.G, h = hk * a.G + (r - t * a.G);
+
+  u32x4_t q[TL::KB];
+  load_row_frags<T, DP>((const T*)a.q + t * a.qs.t + b * a.qs.b + h * a.qs.h, a.D, a.whole & kWholeQ, ok, lane, q);
+  Loader<T, DP, 32, 1, DMA> lk, lv;
+  lk.init((const T*)a.k + b * a.ks.b + hk * a.ks.h, a.ks.t, a.D, a.whole & kWholeK, mask, 0, lane);
+  lv.init((const T*)a.v + b * a.vs.b + hk * a.vs.h, a.vs.t, a.D, a.whole & kWholeV, mask, 0, lane);
+  char* mine = lds + w * 4 * TB;
+
+  f32x16_t o[DP / 32];
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt) o[dt] = zero16();
+  float m = -INFINITY, l = 0.f;
+  const float c2 = a.scale * kLog2e;
+  // this sequence's tiles in equal shares; the waves take theirs in turn
+  const int all = (end + 31) / 32, each = (all + a.splits - 1) / a.splits;
+  const int first = sp * each + w, last = (sp + 1) * each < all ? (sp + 1) * each : all;
+  uint64_t bits = 0;
+  if (first < last) {
+    lk.load(first * 32, end, mine);
+    lv.load(first * 32, end, mine + TB);
+    bits = key_bits(mask, first * 32, end, lane);
+  }
+  int stage = 0;
+  for (int i = first; i < last; i += NW) {
+    char* cur = mine + stage * 2 * TB;
+    char* nxt = mine + (stage ^ 1) * 2 * TB;
+    const uint64_t now = bits;
+    if (i + NW < last) {
+      bits = key_bits(mask, (i + NW) * 32, end, lane);
+      // the other stage was read by the products of the tile before
+      __builtin_amdgcn_s_waitcnt(kLgkm0);
+      lk.load((i + NW) * 32, end, nxt);
+      lv.load((i + NW) * 32, end, nxt + TB);
+      // all but the loads just issued (63 at most can be told apart)
+      constexpr int kNew = 2 * Loader<T, DP, 32, 1, DMA>::kLoads;
+      if constexpr (DMA && kNew <= 63) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kNew));
+      else wait_vmem();
+    } else {
+      wait_vmem();
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    attend_tile<T, DP, 1>(cur, cur + TB, now, q, o, m, l, c2, lane);
+    stage ^= 1;
+  }
+  l += other_half(l);
+  // the waves' parts on one reference: column r of wave w at its own stages
+  float* mo = (float*)mine;  // [DP][32]
+  __syncthreads();
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mo[(32 * dt + reg_row(i, lane)) * 32 + (lane & 31)] = o[dt][i];
+  if (lane < 32) {
+    wm[w][lane] = m;
+    wl[w][lane] = l;
+  }
+  __syncthreads();
+  float top = -INFINITY, sum = 0.f, by[NW];
+#pragma unroll
+  for (int k = 0; k < NW; ++k) top = fmaxf(top, wm[k][lane & 31]);
+  const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    by[k] = __builtin_amdgcn_exp2f(wm[k][lane & 31] - ref);
+    sum += wl[k][lane & 31] * by[k];
+  }
+  if (!ok) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t unit = ((int64_t)grp * (a.tiles / a.splits) + rt) * a.splits + sp;
+  T* out = (T*)a.out + t * a.os.t + b * a.os.b + h * a.os.h;
+  float* part = a.part + (unit * 32 + (lane & 31)) * a.D;
+  for (int d = 2 * w + (lane >> 5); d < a.D; d += 2 * NW) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) v += ((const float*)(lds + k * 4 * TB))[d * 32 + (lane & 31)] * by[k];
+    if (a.splits == 1) out[d] = Elem<T>::from_f(as_f32(v * inv));
+    else part[d] = v;
+  }
+  if (w == 0 && lane < 32) {
+    if (a.splits == 1) {
+      a.lse[((int64_t)b * a.Hq + h) * a.Tq + t] = kLn2 * (top + __builtin_amdgcn_logf(sum));
+    } else {
+      a.part_ml[2 * (unit * 32 + lane)] = top;
+      a.part_ml[2 * (unit * 32 + lane) + 1] = sum;
+    }
+  }
+}
+
+// A wave per row: the parts of its keys.
+template <typename T>
+__global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int row_tiles) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t n = (int64_t)a.B * a.Hk * a.M;
+  if (i >= n) return;
+  const int64_t grp = i / a.M;
+  const uint32_t r = (uint32_t)(i - grp * a.M), t = r / a.G;
+  const int b = (int)(grp / a.Hk);
+  const uint32_t h = (uint32_t)(grp - (int64_t)b * a.Hk) * a.G + (r - t * a.G);
+  const int64_t unit = ((grp * row_tiles + r / 32) * a.splits) * 32 + (r & 31);  // + 32 per part
+  float top = -INFINITY;
+  for (int k = 0; k < a.splits; ++k) top = fmaxf(top, a.part_ml[2 * (unit + 32 * k)]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  for (int k = 0; k < a.splits; ++k)
+    sum += a.part_ml[2 * (unit + 32 * k) + 1] * __builtin_amdgcn_exp2f(a.part_ml[2 * (unit + 32 * k)] - ref);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* out = (T*)a.out + t * a.os.t + b * a.os.b + h * a.os.h;
+  for (int d = lane; d < a.D; d += 64) {
+    float v = 0.f;
+    for (int k = 0; k < a.splits; ++k)
+      v += a.part[(unit + 32 * k) * a.D + d] * __builtin_amdgcn_exp2f(a.part_ml[2 * (unit + 32 * k)] - ref);
+    out[d] = Elem<T>::from_f(as_f32(v * inv));
+  }
+  if (lane == 0) a.lse[((int64_t)b * a.Hq + h) * a.Tq + t] = kLn2 * (top + __builtin_amdgcn_logf(sum));
+}
+
+// ---------------------------------------------------------------------------
+void make_attend_plan(const lstm_attend_shape& s, int cus, AttendPlan* p) {
+  p->dtype = s.dtype;
+  const int dps[6] = {32, 64, 96, 128, 192, 256};
+  p->DP = 256;
+  for (int i = 5; i >= 0; --i)
+    if (s.D <= dps[i]) p->DP = dps[i];
+  const int64_t e = s.dtype == LSTM_F32 ? 4 : 2, G = s.Hk > 0 ? s.Hq / s.Hk : 1, M = s.Tq * G, groups = s.B * s.Hk;
+  p->row_tiles32 = (int)((M + 31) / 32);
+  // the shared kernel where its work-groups fill at least half the device
+  p->step = M <= 32 || groups * ((M + 127) / 128) < cus / 2;
+  p->splits = 1;
+  if (p->step && groups > 0 && M > 0) {
+    // two work-groups a compute unit, each wave at least two tiles of keys
+    const int64_t units = groups * p->row_tiles32, per = 32 * p->DP * e * 16 <= 128 * 1024 ? 4 : 2;
+    int64_t n = 2 * (int64_t)cus / units;
+    const int64_t most = s.Tk / (32 * per * 2);
+    if (n > most) n = most;
+    if (n > 64) n = 64;
+    if (n < 1) n = 1;
+    p->splits = (int)n;
+  }
+  size_t off = 0;
+  p->off_part = p->off_ml = p->off_delta = 0;
+  if (p->splits > 1) {
+    const size_t rows = (size_t)groups * p->row_tiles32 * p->splits * 32;
+    p->off_part = off; off += align256_seq(rows * (size_t)s.D * 4);
+    p->off_ml = off; off += align256_seq(rows * 8);
+  }
+  p->total_fwd = off;
+  p->total_bwd = align256_seq((size_t)s.B * s.Hq * s.Tq * 4);
+}
+
+template <typename T, int DP, bool DMA>
+static hipError_t attend_fwd_t(const AttendPlan& p, const AttendArgs& a0, hipStream_t s) {
+  AttendArgs a = a0;
+  constexpr int C = Tile<T, DP>::C;
+  if (p.step) {
+    constexpr int NW = step_waves<T, DP>();
+    const size_t lds = (size_t)NW * 4 * Tile<T, DP>::kBytes32;
+    a.tiles = p.row_tiles32 * p.splits;
+    const unsigned grid = attend_grid(&a);
+    const hipError_t e = allow_lds((const void*)attend_step_kernel<T, DP, DMA>, lds);
+    if (e != hipSuccess) return e;
+    attend_step_kernel<T, DP, DMA><<<grid, 64 * NW, lds, s>>>(a);
+    if (p.splits > 1) {
+      const int64_t rows = (int64_t)a.B * a.Hk * a.M;
+      attend_join_kernel<T><<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(a, p.row_tiles32);
+    }
+  } else {
+    const size_t lds = (size_t)4 * fwd_keys<T, DP>() * C * 16;
+    a.tiles = (int)((a.M + 127) / 128);
+    const unsigned grid = attend_grid(&a);
+    const hipError_t e = allow_lds((const void*)attend_fwd_kernel<T, DP, DMA>, lds);
+    if (e != hipSuccess) return e;
+    attend_fwd_kernel<T, DP, DMA><<<grid, 256, lds, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_attend_fwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s) {
+  if (a.B == 0 || a.M == 0) return hipSuccess;
+  Timed tm(8, s);
+#define ATTEND_DP(T, N) \
+  if (p.DP == N) return p.dma ? attend_fwd_t<T, N, true>(p, a, s) : attend_fwd_t<T, N, false>(p, a, s)
+#define ATTEND_T(T) \
+  ATTEND_DP(T, 32); ATTEND_DP(T, 64); ATTEND_DP(T, 96); ATTEND_DP(T, 128); ATTEND_DP(T, 192); ATTEND_DP(T, 256)
+  if (p.dtype == LSTM_F32) { ATTEND_T(float); }
+  if (p.dtype == LSTM_BF16) { ATTEND_T(bf16_t); }
+  if (p.dtype == LSTM_F16) { ATTEND_T(f16_t); }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace lstm

@@ -1,5 +1,6 @@
 // seq_api.hip -- the extern "C" entry points of the sequence-to-sequence
 // operators (include/lstm.h): argument checks, then the launches.
+#include "attend_common.hpp"
 #include "internal.hpp"
 #include "seq_internal.hpp"
 
@@ -42,6 +43,74 @@ static int logprob_plan(const lstm_logprob_shape* s, LogprobPlan* p) {
   if (rc != LSTM_OK) return rc;
   make_logprob_plan(*s, cus, p);
   return LSTM_OK;
+}
+
+// A tensor of [T][B][H] rows of D values whose rows do not overlap.
+static bool disjoint(const lstm_stride& s, int64_t T, int64_t B, int64_t H, int64_t D) {
+  if (T == 0 || B == 0 || H == 0) return true;
+  int64_t st[3] = {s.t, s.b, s.h}, n[3] = {T, B, H}, cover = D;
+  for (int i = 0; i < 3; ++i) {
+    int k = -1;
+    for (int j = 0; j < 3; ++j)
+      if (n[j] > 1 && (k < 0 || st[j] < st[k])) k = j;
+    if (k < 0) return true;
+    if (st[k] < cover) return false;
+    cover += st[k] * (n[k] - 1);
+    n[k] = 1;
+  }
+  return true;
+}
+static bool strides_ok(const lstm_stride& s) {
+  const int64_t far = (int64_t)1 << 36;
+  return s.t >= 0 && s.b >= 0 && s.h >= 0 && s.t < far && s.b < far && s.h < far;
+}
+// whole aligned 16-byte chunks in every row
+static bool whole_rows(const void* p, const lstm_stride& s, int64_t D, int64_t e) {
+  return aligned16(p) && (D * e) % 16 == 0 && (s.t * e) % 16 == 0 && (s.b * e) % 16 == 0 && (s.h * e) % 16 == 0;
+}
+// rows a tile of which can be loaded through one descriptor
+static bool dma_rows(const void* p, const lstm_stride& s, int64_t D, int64_t e) {
+  return whole_rows(p, s, D, e) && s.t >= D && s.t * e < ((int64_t)1 << 31) / 64;
+}
+
+static int attend_plan(const lstm_attend_shape* s, bool bwd, AttendPlan* p) {
+  if (!s) return LSTM_ERR_NULL;
+  if (s->Tq < 0 || s->Tk < 0 || s->B < 0 || s->Hq < 0 || s->Hk < 0 || s->D < 1 || (s->Hk == 0) != (s->Hq == 0) ||
+      (s->Hk > 0 && s->Hq % s->Hk != 0) || !(s->scale > 0.f) || s->scale > 3.0e38f || s->mask_b < 0 ||
+      !strides_ok(s->q) || !strides_ok(s->k) || !strides_ok(s->v) || !strides_ok(s->o) ||
+      !disjoint(s->o, s->Tq, s->B, s->Hq, s->D))
+    return LSTM_ERR_DIMS;
+  if (bwd && (!strides_ok(s->dout) || !strides_ok(s->dq) || !strides_ok(s->dk) || !strides_ok(s->dv) ||
+              !disjoint(s->dq, s->Tq, s->B, s->Hq, s->D) || !disjoint(s->dk, s->Tk, s->B, s->Hk, s->D) ||
+              !disjoint(s->dv, s->Tk, s->B, s->Hk, s->D)))
+    return LSTM_ERR_DIMS;
+  if (!dtype_ok(s->dtype)) return LSTM_ERR_DTYPE;
+  const int64_t big = (int64_t)1 << 26, wide = (int64_t)1 << 20;
+  if (s->D > 256 || s->Tq >= big || s->Tk >= big || s->B >= wide || s->Hq >= wide || s->mask_b >= ((int64_t)1 << 36))
+    return LSTM_ERR_UNSUPPORTED;
+  const int64_t G = s->Hk > 0 ? s->Hq / s->Hk : 1, M = s->Tq * G, groups = s->B * s->Hk + 8;
+  // work-groups of any launch stay below 2^24
+  if (M >= ((int64_t)1 << 30) || groups >= ((int64_t)1 << 23) || groups * ((M + 31) / 32 + 64) >= ((int64_t)1 << 24) ||
+      groups * ((s->Tk + 127) / 128) >= ((int64_t)1 << 24))
+    return LSTM_ERR_UNSUPPORTED;
+  int cus = 0;
+  const int rc = device_cus(&cus);
+  if (rc != LSTM_OK) return rc;
+  make_attend_plan(*s, cus, p);
+  return LSTM_OK;
+}
+
+static AttendArgs attend_args(const lstm_attend_shape& s) {
+  AttendArgs a = {};
+  a.qs = s.q; a.ks = s.k; a.vs = s.v; a.os = s.o; a.gs = s.dout; a.dqs = s.dq; a.dks = s.dk; a.dvs = s.dv;
+  a.mask_b = s.mask_b;
+  a.Tq = (int)s.Tq; a.Tk = (int)s.Tk; a.B = (int)s.B; a.Hq = (int)s.Hq; a.Hk = (int)s.Hk;
+  a.G = s.Hk > 0 ? (int)(s.Hq / s.Hk) : 1;
+  a.D = (int)s.D;
+  a.M = (uint32_t)(s.Tq * a.G);
+  if (s.Hk == 0) a.M = 0;
+  a.scale = s.scale;
+  return a;
 }
 
 }  // namespace lstm
@@ -128,6 +197,71 @@ int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const 
   if (dlogits == logits && p.ld != p.ldg) return LSTM_ERR_DIMS;
   return status(launch_logprob_bwd(p, logits, targets, record, entropy, top_ids, dlogp, dentropy, dtop, dlogits,
                                    (hipStream_t)stream));
+}
+
+int lstm_attend_query(const lstm_attend_shape* shape, size_t* fwd_bytes, size_t* bwd_bytes) {
+  if (!fwd_bytes || !bwd_bytes) return LSTM_ERR_NULL;
+  AttendPlan p;
+  const int rc = attend_plan(shape, false, &p);
+  if (rc != LSTM_OK) return rc;
+  *fwd_bytes = p.total_fwd;
+  *bwd_bytes = p.total_bwd;
+  return LSTM_OK;
+}
+
+int lstm_attend_fwd(const lstm_attend_shape* shape, const void* q, const void* k, const void* v, const void* k_length,
+                    const void* key_mask, void* workspace, size_t workspace_bytes, void* o, float* lse, void* stream) {
+  AttendPlan p;
+  const int rc = attend_plan(shape, false, &p);
+  if (rc != LSTM_OK) return rc;
+  AttendArgs a = attend_args(*shape);
+  const bool any = a.M > 0 && a.B > 0;
+  if (any && (!q || !o || !lse || (a.Tk > 0 && (!k || !v)) || (p.total_fwd > 0 && !workspace))) return LSTM_ERR_NULL;
+  const int64_t e = esize_of(p.dtype);
+  if (off_size(q, e) || off_size(k, e) || off_size(v, e) || off_size(o, e) || off_size(lse, 4) ||
+      off_size(k_length, 4) || ((uintptr_t)workspace & 255u))
+    return LSTM_ERR_ALIGN;
+  if (workspace_bytes < p.total_fwd) return LSTM_ERR_WORKSPACE;
+  a.q = q; a.k = k; a.v = v; a.out = o; a.lse = lse;
+  a.len = (const int32_t*)k_length;
+  a.mask = (const uint8_t*)key_mask;
+  a.splits = p.splits;
+  a.part = (float*)((char*)workspace + p.off_part);
+  a.part_ml = (float*)((char*)workspace + p.off_ml);
+  const int64_t D = shape->D;
+  a.whole = (whole_rows(q, a.qs, D, e) ? kWholeQ : 0) | (whole_rows(k, a.ks, D, e) ? kWholeK : 0) |
+            (whole_rows(v, a.vs, D, e) ? kWholeV : 0) | (whole_rows(o, a.os, D, e) ? kWholeO : 0);
+  p.dma = dma_rows(k, a.ks, D, e) && dma_rows(v, a.vs, D, e);
+  return status(launch_attend_fwd(p, a, (hipStream_t)stream));
+}
+
+int lstm_attend_bwd(const lstm_attend_shape* shape, const void* dout, const void* q, const void* k, const void* v,
+                    const void* k_length, const void* key_mask, const void* o, const float* lse, void* workspace,
+                    size_t workspace_bytes, void* dq, void* dk, void* dv, void* stream) {
+  AttendPlan p;
+  const int rc = attend_plan(shape, true, &p);
+  if (rc != LSTM_OK) return rc;
+  AttendArgs a = attend_args(*shape);
+  const bool rows = a.M > 0 && a.B > 0, keys = a.Tk > 0 && a.B > 0 && a.Hk > 0;
+  if ((rows && (!dout || !q || !o || !lse || !dq || !workspace)) || (keys && (!k || !v || !dk || !dv)))
+    return LSTM_ERR_NULL;
+  const int64_t e = esize_of(p.dtype);
+  if (off_size(dout, e) || off_size(q, e) || off_size(k, e) || off_size(v, e) || off_size(o, e) || off_size(lse, 4) ||
+      off_size(k_length, 4) || off_size(dq, e) || off_size(dk, e) || off_size(dv, e) || ((uintptr_t)workspace & 255u))
+    return LSTM_ERR_ALIGN;
+  if (workspace_bytes < p.total_bwd) return LSTM_ERR_WORKSPACE;
+  a.q = q; a.k = k; a.v = v; a.o = o; a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;
+  a.lse = const_cast<float*>(lse);
+  a.delta = (float*)workspace;
+  a.len = (const int32_t*)k_length;
+  a.mask = (const uint8_t*)key_mask;
+  const int64_t D = shape->D;
+  a.whole = (whole_rows(q, a.qs, D, e) ? kWholeQ : 0) | (whole_rows(k, a.ks, D, e) ? kWholeK : 0) |
+            (whole_rows(v, a.vs, D, e) ? kWholeV : 0) | (whole_rows(o, a.os, D, e) ? kWholeO : 0) |
+            (whole_rows(dout, a.gs, D, e) ? kWholeG : 0) | (whole_rows(dq, a.dqs, D, e) ? kWholeDq : 0) |
+            (whole_rows(dk, a.dks, D, e) ? kWholeDk : 0) | (whole_rows(dv, a.dvs, D, e) ? kWholeDv : 0);
+  p.dma = dma_rows(q, a.qs, D, e) && dma_rows(k, a.ks, D, e) && dma_rows(v, a.vs, D, e) && dma_rows(dout, a.gs, D, e);
+  return status(launch_attend_bwd(p, a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -43,7 +43,7 @@ EXPORTS = ("lstm_abi_version", "lstm_status_string", "lstm_query", "lstm_query_p
            "lstm_fwd_train_scratch", "lstm_bwd", "lstm_check_workspace", "lstm_timing_enable", "lstm_timing_read",
            "lstm_stamps_set", "lstm_probe_exchange", "lstm_probe_mfma_stage", "lstm_debug_inject", "lstm_stack_query",
            "lstm_stack_fwd_train", "lstm_stack_bwd", "lstm_embed_query", "lstm_embed_fwd", "lstm_embed_bwd",
-           "lstm_logprob_query", "lstm_logprob_fwd", "lstm_logprob_bwd")
+           "lstm_attend_query", "lstm_attend_fwd", "lstm_attend_bwd", "lstm_logprob_query", "lstm_logprob_fwd", "lstm_logprob_bwd")
 STAMP_WGS, STAMP_POINTS = 8, 6
 KERNEL_KINDS = ("input_projection", "forward_recurrence", "backward_recurrence", "dW_product",
                 "dx_product", "direction_copy", "state_copy", "embedding", "cross_attention", "log_probability")
@@ -69,6 +69,16 @@ class EmbedShape(ctypes.Structure):
 class LogprobShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("N", "V", "ld", "ld_grad")] + \
                [("scale", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("top", "dtype", "id_type")]
+
+
+class Stride(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("t", "b", "h")]
+
+
+class AttendShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("Tq", "Tk", "B", "Hq", "Hk", "D")] + \
+               [(n, Stride) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")] + \
+               [("mask_b", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -109,6 +119,9 @@ _lib.lstm_stack_bwd.argtypes = [ctypes.POINTER(Shape), ctypes.c_int64, ctypes.c_
 for _n, _a in (("lstm_embed_query", [ctypes.POINTER(EmbedShape), ctypes.POINTER(ctypes.c_size_t)]),
                ("lstm_embed_fwd", [ctypes.POINTER(EmbedShape)] + [_P] * 4),
                ("lstm_embed_bwd", [ctypes.POINTER(EmbedShape)] + [_P] * 3 + [ctypes.c_size_t] + [_P] * 2),
+               ("lstm_attend_query", [ctypes.POINTER(AttendShape)] + [ctypes.POINTER(ctypes.c_size_t)] * 2),
+               ("lstm_attend_fwd", [ctypes.POINTER(AttendShape)] + [_P] * 6 + [ctypes.c_size_t] + [_P] * 3),
+               ("lstm_attend_bwd", [ctypes.POINTER(AttendShape)] + [_P] * 9 + [ctypes.c_size_t] + [_P] * 4),
                ("lstm_logprob_query", [ctypes.POINTER(LogprobShape), ctypes.POINTER(ctypes.c_size_t)]),
                ("lstm_logprob_fwd", [ctypes.POINTER(LogprobShape)] + [_P] * 3 + [ctypes.c_size_t] + [_P] * 7),
                ("lstm_logprob_bwd", [ctypes.POINTER(LogprobShape)] + [_P] * 10)):
@@ -440,6 +453,73 @@ class Embedding:
         if rc != OK:
             raise LstmError(rc, "lstm_embed_bwd")
         return self.dtable
+
+
+class Attention:
+    """Cross attention of Tq queries to Tk states of an encoder
+    (lstm_attend_*), with its workspace and output buffers on the current
+    device.  q [Tq, B, Hq, D], k and v [Tk, B, Hk, D] (any strides >= 0, D
+    contiguous; an expanded k or v gets the gradient of its expanded form);
+    k_length: int32 [B] valid keys of each sequence; key_mask: bool or uint8
+    [B, Tk], zero = not a key.  o, dq, dk, dv are dense, lse fp32 [B, Hq,
+    Tq]."""
+
+    def __init__(self, Tq, Tk, B, Hq, Hk, D, dtype=F32, scale=None, device="cuda"):
+        self.Tq, self.Tk, self.B, self.Hq, self.Hk, self.D, self.dtype, self.device = Tq, Tk, B, Hq, Hk, D, dtype, device
+        dense_q, dense_k = Stride(B * Hq * D, Hq * D, D), Stride(B * Hk * D, Hk * D, D)
+        self.shape = AttendShape(Tq, Tk, B, Hq, Hk, D, dense_q, dense_k, dense_k, dense_q, dense_q, dense_q, dense_k,
+                                 dense_k, Tk, float(max(D, 1) ** -0.5 if scale is None else scale), int(dtype))
+        nf, nb = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        rc = _lib.lstm_attend_query(ctypes.byref(self.shape), ctypes.byref(nf), ctypes.byref(nb))
+        if rc != OK:
+            raise LstmError(rc, "lstm_attend_query")
+        self.ws_bytes = max(nf.value, nb.value)
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.tdtype = torch_dtype(dtype)
+        self.o = torch.empty((Tq, B, Hq, D), dtype=self.tdtype, device=device)
+        self.lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=device)
+        self.dq = self.dk = self.dv = None
+
+    def _strides(self, name, x, T, H):
+        _need(x.dtype == self.tdtype and x.shape == (T, self.B, H, self.D) and (self.D == 1 or x.stride(3) == 1),
+              f"{name}: {[T, self.B, H, self.D]} of {self.tdtype}, last dimension contiguous")
+        s = getattr(self.shape, name)
+        s.t, s.b, s.h = x.stride(0), x.stride(1), x.stride(2)
+
+    def _inputs(self, q, k, v, k_length, key_mask):
+        self._strides("q", q, self.Tq, self.Hq)
+        self._strides("k", k, self.Tk, self.Hk)
+        self._strides("v", v, self.Tk, self.Hk)
+        _need(k_length is None or (k_length.dtype == torch.int32 and k_length.shape == (self.B,) and
+                                   k_length.is_contiguous()), f"k_length: int32 [{self.B}], contiguous")
+        if key_mask is not None:
+            _need(key_mask.dtype in (torch.bool, torch.uint8) and key_mask.shape == (self.B, self.Tk) and
+                  (self.Tk <= 1 or key_mask.stride(1) == 1), f"key_mask: bool or uint8 {[self.B, self.Tk]}, rows contiguous")
+            self.shape.mask_b = key_mask.stride(0)
+
+    def forward(self, q, k, v, k_length=None, key_mask=None, stream=None):
+        """o [Tq, B, Hq, D] and lse [B, Hq, Tq]."""
+        self._inputs(q, k, v, k_length, key_mask)
+        rc = _lib.lstm_attend_fwd(ctypes.byref(self.shape), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length), _ptr(key_mask),
+                                  _ptr(self.workspace), self.ws_bytes, _ptr(self.o), _ptr(self.lse), _stream(stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_attend_fwd")
+        return self.o, self.lse
+
+    def backward(self, dout, q, k, v, k_length=None, key_mask=None, stream=None):
+        """dq, dk, dv after a forward on the same inputs."""
+        self._inputs(q, k, v, k_length, key_mask)
+        self._strides("dout", dout, self.Tq, self.Hq)
+        if self.dq is None:
+            self.dq = torch.empty((self.Tq, self.B, self.Hq, self.D), dtype=self.tdtype, device=self.device)
+            self.dk, self.dv = (torch.empty((self.Tk, self.B, self.Hk, self.D), dtype=self.tdtype, device=self.device)
+                                for _ in range(2))
+        rc = _lib.lstm_attend_bwd(ctypes.byref(self.shape), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length),
+                                  _ptr(key_mask), _ptr(self.o), _ptr(self.lse), _ptr(self.workspace), self.ws_bytes,
+                                  _ptr(self.dq), _ptr(self.dk), _ptr(self.dv), _stream(stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_attend_bwd")
+        return self.dq, self.dk, self.dv
 
 
 class LogProb:

@@ -53,3 +53,41 @@ def test_logprob_shapes(lstm, change, code):
     assert L.lstm_logprob_fwd(ctypes.byref(s), None, None, None, 0, *([None] * 6), None) == code
     assert L.lstm_logprob_bwd(ctypes.byref(s), *([None] * 9), None) == code
     assert L.lstm_logprob_query(None, ctypes.byref(n)) == L.lstm_logprob_query(ctypes.byref(s), None) == -1
+
+
+def attend_shape(lstm):
+    q, k = lstm.Stride(2 * 4 * 16, 4 * 16, 16), lstm.Stride(2 * 2 * 16, 2 * 16, 16)
+    return lstm.AttendShape(3, 5, 2, 4, 2, 16, q, k, k, q, q, q, k, k, 5, 0.25, 0)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(Tq=-1), -2), (dict(Tk=-1), -2), (dict(B=-1), -2), (dict(Hq=3), -2), (dict(Hk=3), -2), (dict(Hk=0), -2),
+    (dict(Hq=0), -2), (dict(D=0), -2), (dict(scale=0.0), -2), (dict(scale=float("nan")), -2), (dict(mask_b=-1), -2),
+    (dict(dtype=3), -3), (dict(D=257, Tq=1, Tk=1, B=1, Hq=1, Hk=1), -6), (dict(Tk=1 << 26), -6), (dict(Tq=1 << 25), -6)])
+def test_attend_shapes(lstm, change, code):
+    s = attend_shape(lstm)
+    for k, v in change.items():
+        setattr(s, k, v)
+    a, b = ctypes.c_size_t(77), ctypes.c_size_t(77)
+    L = lstm.lib()
+    assert L.lstm_attend_query(ctypes.byref(s), ctypes.byref(a), ctypes.byref(b)) == code
+    assert a.value == b.value == 77
+    assert L.lstm_attend_fwd(ctypes.byref(s), *([None] * 6), 0, None, None, None) == code
+    assert L.lstm_attend_bwd(ctypes.byref(s), *([None] * 9), 0, None, None, None, None) == code
+    assert L.lstm_attend_query(None, ctypes.byref(a), ctypes.byref(b)) == -1
+    assert L.lstm_attend_query(ctypes.byref(s), None, ctypes.byref(b)) == -1
+
+
+@pytest.mark.parametrize("name,field,value", [
+    ("q", "t", -1), ("k", "b", -1), ("v", "h", 1 << 36), ("o", "h", 8), ("o", "t", 0)])
+def test_attend_strides(lstm, name, field, value):
+    """A stride out of range, or an output whose rows overlap; inputs may overlap."""
+    s = attend_shape(lstm)
+    setattr(getattr(s, name), field, value)
+    a, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert lstm.lib().lstm_attend_query(ctypes.byref(s), ctypes.byref(a), ctypes.byref(b)) == -2
+    s = attend_shape(lstm)
+    s.k.b = s.v.t = 0
+    assert lstm.lib().lstm_attend_query(ctypes.byref(s), ctypes.byref(a), ctypes.byref(b)) in (0, -10)  # -10: no GPU
+    s.dk.b = 0
+    assert lstm.lib().lstm_attend_bwd(ctypes.byref(s), *([None] * 9), 0, None, None, None, None) == -2
