@@ -18,8 +18,21 @@ namespace lstm {
 // p is carried 2^32 times larger through the products and their sums, and the
 // factor goes with `scale` when the sums are stored, so that the gradients of
 // the smallest p survive as far as the type reaches.  (fp16 would overflow.)
-template <typename T> constexpr float kCarry = std::is_same<T, f16_t>::value ? 0.f : 32.f;
-template <typename T> constexpr float kUncarry = std::is_same<T, f16_t>::value ? 1.f : 2.3283064365386963e-10f;
+// In bf16 the factor is in the exponent, y + 32, whose rounding (2^-19 of p)
+// is far below the storage type's; in fp32 it would be the largest error of
+// all, so there the factor is multiplied on, and the exponent of a small p is
+// raised by 64 first.
+template <typename T> constexpr float kCarry = std::is_same<T, f16_t>::value ? 1.f : 4294967296.f;
+template <typename T> constexpr float kInExponent = std::is_same<T, bf16_t>::value ? 32.f : 0.f;
+template <typename T>
+__device__ __forceinline__ float exp_carried(float y) {
+  if constexpr (std::is_same<T, float>::value) {
+    const bool low = y < -64.f;
+    return __builtin_amdgcn_exp2f(low ? y + 64.f : y) * (low ? kCarry<T> * 0x1p-64f : kCarry<T>);
+  } else {
+    return __builtin_amdgcn_exp2f(y);
+  }
+}
 
 template <typename T, int DP> constexpr int dq_keys() { return 4 * 64 * Tile<T, DP>::C * 16 <= 64 * 1024 ? 64 : 32; }
 
@@ -63,7 +76,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
   float lse2 = INFINITY;  // no row, or a row without keys: p = 0
   if (ok) {
     const float v = a.lse[li];
-    if (v != -INFINITY) lse2 = v * kLog2e - kCarry<T>;
+    if (v != -INFINITY) lse2 = v * kLog2e - kInExponent<T>;
     if (lane < 32) a.delta[li] = delta;
   }
   Loader<T, DP, NK, 4, DMA> lk, lv;
@@ -107,7 +120,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
       // the factor `scale` of ds goes to the end
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        s[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - delta);
+        s[j] = exp_carried<T>(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - delta);
 #pragma unroll
       for (int pb = 0; pb < TL::PB; ++pb) {
         const u32x4_t ds = TL::reg_frag(s, pb);
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
     }
   }
   if (ok)
-    store_col<T, DP>((T*)a.dq + t * a.dqs.t + b * a.dqs.b + h * a.dqs.h, dq, a.scale * kUncarry<T>, a.D, a.whole & kWholeDq, lane);
+    store_col<T, DP>((T*)a.dq + t * a.dqs.t + b * a.dqs.b + h * a.dqs.h, dq, a.scale / kCarry<T>, a.D, a.whole & kWholeDq, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
         if (t < a.Tq) {
           const int64_t li = ((int64_t)b * a.Hq + hk * a.G + hd) * a.Tq + t;
           const float x = a.lse[li];
-          if (x != -INFINITY) st_l = x * kLog2e - kCarry<T>;
+          if (x != -INFINITY) st_l = x * kLog2e - kInExponent<T>;
           st_d = a.delta[li];
         }
       }
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
       for (int j = 0; j < 4; ++j) {
         const f32x4_t L = *(const f32x4_t*)&stat[buf][0][reg_row(4 * j, lane)];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * j + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * j + e], c2, -L[e]));
+        for (int e = 0; e < 4; ++e) s[4 * j + e] = exp_carried<T>(__builtin_fmaf(s[4 * j + e], c2, -L[e]));
       }
       if (DV) {
 #pragma unroll
@@ -232,9 +245,9 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
 #pragma unroll
     for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = zero16();
   }
-  if (DK) store_col<T, DP>((T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h, dk, a.scale * kUncarry<T>,
+  if (DK) store_col<T, DP>((T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h, dk, a.scale / kCarry<T>,
                    a.D, a.whole & kWholeDk, lane);
-  if (DV) store_col<T, DP>((T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h, dv, kUncarry<T>, a.D, a.whole & kWholeDv, lane);
+  if (DV) store_col<T, DP>((T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h, dv, 1.f / kCarry<T>, a.D, a.whole & kWholeDv, lane);
 }
 
 // ---------------------------------------------------------------------------
