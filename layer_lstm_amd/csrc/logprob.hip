@@ -16,8 +16,9 @@
 // The alternatives are kept as a list sorted across the lanes of a wave: a
 // 64-bit key per lane, the logit in an order-preserving form above the
 // complement of its id, so that no two keys are equal and a tie goes to the
-// lower id.  A vector whose largest logit does not reach the list's entry
-// `top` is passed over with one comparison.
+// lower id.  Logits that reach the list's entry `top` are appended to a buffer
+// in LDS, and a full buffer is merged into the list by counting, for every
+// key, the keys above it.
 #include <type_traits>
 
 #include "internal.hpp"
@@ -25,18 +26,19 @@
 
 namespace lstm {
 
-constexpr int kLpThreads = 256, kLpWaves = 4;
+constexpr int kLpThreads = 256;
+constexpr int kLpVecs = 4;      // 16-byte vectors a lane of the forward takes at a time
 constexpr int kMaxParts = 64;   // a row's parts are joined by the lanes of one wave
 constexpr float kSlack = 16.f;  // how far (in powers of two) a logit may pass the reference
 
 void make_logprob_plan(const lstm_logprob_shape& s, int cus, LogprobPlan* p) {
   p->N = s.N; p->V = s.V; p->ld = s.ld; p->ldg = s.ld_grad;
   p->scale = s.scale; p->top = s.top; p->dtype = s.dtype; p->id64 = s.id_type == LSTM_I64;
-  // a work-group per row; rows too few for four work-groups a compute unit
-  // are split, down to one vector per thread
-  const int64_t step = (int64_t)kLpThreads * (s.dtype == LSTM_F32 ? 4 : 8);
+  // a wave per row; rows too few for eight waves a compute unit are split,
+  // down to one round of a wave's loads
+  const int64_t step = (int64_t)64 * kLpVecs * (s.dtype == LSTM_F32 ? 4 : 8);
   int64_t parts = 1;
-  if (s.N > 0 && s.N < 4 * (int64_t)cus) parts = 4 * (int64_t)cus / s.N;
+  if (s.N > 0 && s.N < 8 * (int64_t)cus) parts = 8 * (int64_t)cus / s.N;
   if (parts > kMaxParts) parts = kMaxParts;
   int64_t steps = (s.V + step - 1) / step;  // of a row
   if (steps < 1) steps = 1;
@@ -61,56 +63,139 @@ __device__ __forceinline__ float from_order(uint32_t o) {
   return __uint_as_float(o ^ ((o & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
+// Reductions over a wave in registers: inside rows of 16 lanes by row_shr,
+// then across the rows by row_bcast, the result in lane 63 (in a fixed order).
+template <class Op>
+__device__ __forceinline__ float wave_reduce(float v, float none, Op op) {
+  auto from = [&](auto ctl, auto rows) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+        (int)__float_as_uint(none), (int)__float_as_uint(v), decltype(ctl)::value, decltype(rows)::value, 0xf, false));
+  };
+  using std::integral_constant;
+  v = op(v, from(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{}));  // row_shr:1
+  v = op(v, from(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{}));  // row_shr:2
+  v = op(v, from(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{}));  // row_shr:4
+  v = op(v, from(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{}));  // row_shr:8
+  v = op(v, from(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{}));  // row_bcast:15 into rows 1, 3
+  v = op(v, from(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{}));  // row_bcast:31 into rows 2, 3
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  return wave_reduce(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return wave_reduce(v, 0.f, [](float a, float b) { return a + b; });
 }
 
-// Sums against a reference, moved to another reference.
+// Sums against a reference m: s = sum 2^y, t = sum 2^y y.  y is one fused
+// multiply-add, x c2 - m2 with m2 = m c2 rounded; the rounding of m2 is put
+// back when the sums are read (lg).  Where m c2 might overflow (a row of the
+// type's lowest value) y = (x - m) c2 and m2 = 0.
 struct RowSums {
   float m, s, t;  // m = -inf: nothing but -inf so far (s = t = 0, or NaN)
-  __device__ __forceinline__ float ref() const { return m == -INFINITY ? 0.f : m; }
+  __device__ __forceinline__ bool huge(float c2) const { return !(fabsf(m * c2) < 1e37f); }
+  __device__ __forceinline__ float m2(float c2) const { return huge(c2) ? 0.f : m * c2; }
   __device__ __forceinline__ void move(float to, float c2) {
     if (m != -INFINITY && to != m) {
-      const float d = (to - m) * c2, r = __builtin_amdgcn_exp2f(-d);
+      RowSums n = {to, 0.f, 0.f};
+      const float d = !huge(c2) && !n.huge(c2) ? n.m2(c2) - m2(c2) : (to - m) * c2;
+      const float r = __builtin_amdgcn_exp2f(-d);
       t = r == 0.f ? s * 0.f : (t - d * s) * r;
       s *= r;
     }
     m = to;
   }
+  // log2 sum exp(scale (x - m)), and what has to go off y
+  __device__ __forceinline__ float lost(float c2) const { return huge(c2) ? 0.f : __builtin_fmaf(m, c2, -m2(c2)); }
 };
 
-// The list: lane i holds the i-th largest key so far (0: none).
+// The largest threshold that at least `top` of the wave's values reach, on the
+// grid of the upper kGridBits bits (0: fewer than `top` values).  Values are
+// order_of() of one logit per lane, 0 for none.
+constexpr int kGridBits = 16;
+__device__ __forceinline__ uint32_t wave_threshold(uint32_t v, int top) {
+  uint32_t at = 0;
+#pragma unroll
+  for (int b = 31; b >= 32 - kGridBits; --b) {
+    const uint32_t to = at | (1u << b);
+    if (__popcll(__ballot(v >= to)) >= top) at = to;
+  }
+  return at;
+}
+
+// The value of f whose bit alone is set (registers cannot be indexed).
+template <int C>
+__device__ __forceinline__ float pick(const float* f, uint32_t bit) {
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) v |= __float_as_uint(f[i]) & (uint32_t)__builtin_amdgcn_sbfe((int)bit, i, 1);
+  return __uint_as_float(v);
+}
+
+// What a wave's list needs in LDS: the keys appended since the last merge,
+// and the merged keys in order.
+struct TopLds {
+  uint64_t cand[128], sorted[LSTM_MAX_TOP];
+};
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The list: lane i < top holds the i-th largest key so far (0: none).  A key
+// has to pass `least`: the list's last, or a floor that `top` logits of the
+// wave are known to reach (which keeps the first logits of a row from being
+// appended one and all).
 struct TopList {
-  uint32_t hi, lo;    // this lane's key
-  uint32_t thi, tlo;  // key `top` - 1, which a key has to pass
-  float tval;         // its logit
-  bool full;
-  __device__ __forceinline__ void clear() { hi = lo = thi = tlo = 0; tval = -INFINITY; full = false; }
-  // true in the lanes whose vector may hold a key to insert
-  __device__ __forceinline__ bool wants(float vmax) const { return !full || vmax >= tval; }
-  __device__ __forceinline__ void insert(uint32_t chi, uint32_t clo, int top, int lane) {
-    uint64_t cand = __ballot(chi > thi || (chi == thi && clo > tlo));
-    while (cand) {
-      const int l = __builtin_ctzll(cand);
-      const uint32_t a = __builtin_amdgcn_readlane(chi, l), b = __builtin_amdgcn_readlane(clo, l);
-      const int at = __popcll(__ballot(hi > a || (hi == a && lo > b)));
-      const uint32_t shi = __shfl_up(hi, 1), slo = __shfl_up(lo, 1);
-      hi = lane < at ? hi : lane == at ? a : shi;
-      lo = lane < at ? lo : lane == at ? b : slo;
-      thi = __builtin_amdgcn_readlane(hi, top - 1);
-      tlo = __builtin_amdgcn_readlane(lo, top - 1);
-      cand &= ~((uint64_t)2 << l) + 1;  // the lanes after l
-      cand &= __ballot(chi > thi || (chi == thi && clo > tlo));
+  uint64_t key, least;
+  float tval;  // the logit of `least` (no number where everything may pass)
+  int count;   // appended keys
+  __device__ __forceinline__ void clear() { key = least = 0; tval = -NAN; count = 0; }
+  __device__ __forceinline__ void set_floor(uint32_t order) {
+    if (order > 0) {
+      least = ((uint64_t)order << 32) - 1;
+      tval = from_order(order);
     }
-    full = thi != 0 || tlo != 0;
-    tval = from_order(thi);
+  }
+  // true where x may be a key to append
+  __device__ __forceinline__ bool wants(float x) const { return !(x < tval); }
+  // one key of every lane (0: none), and a merge as soon as it can raise the
+  // list's last key; `more`: further keys follow at once
+  __device__ __forceinline__ void append(TopLds* lds, uint64_t k, bool more, int top, int lane) {
+    const uint64_t in = __ballot(k > least);
+    if (k > least) lds->cand[count + __popcll(in & (((uint64_t)1 << lane) - 1))] = k;
+    count += __popcll(in);
+    if (count > 64 || (!more && count >= top)) merge(lds, top, lane);
+  }
+  // appended keys into the list, 64 - top at a time
+  __device__ __forceinline__ void merge(TopLds* lds, int top, int lane) {
+    wave_sync();
+    while (count > 0) {
+      const int m = count < 64 - top ? count : 64 - top;
+      count -= m;
+      uint64_t k = lane < top ? key : 0;
+      if (lane >= top && lane < top + m) k = lds->cand[count + lane - top];
+      int rank = 0;
+      for (int i = 0; i < top + m; i += 4) {
+#pragma unroll
+        for (int j = i; j < i + 4; ++j) {  // lanes past the last hold no key
+          const uint64_t o = ((uint64_t)__builtin_amdgcn_readlane((uint32_t)(k >> 32), j) << 32) |
+                             (uint32_t)__builtin_amdgcn_readlane((uint32_t)k, j);
+          rank += o > k;
+        }
+      }
+      if (lane < top) lds->sorted[lane] = 0;
+      wave_sync();
+      if (k != 0 && rank < top) lds->sorted[rank] = k;
+      wave_sync();
+      key = lane < top ? lds->sorted[lane] : 0;
+      const uint64_t last = ((uint64_t)__builtin_amdgcn_readlane((uint32_t)(key >> 32), top - 1) << 32) |
+                            (uint32_t)__builtin_amdgcn_readlane((uint32_t)key, top - 1);
+      if (last > least) {
+        least = last;
+        tval = from_order((uint32_t)(last >> 32));
+      }
+    }
   }
 };
 
@@ -129,144 +214,165 @@ __device__ __forceinline__ float log_prob(float x, float scale, float m, float l
   return m == -INFINITY ? -INFINITY : (x - m) * scale - ls;
 }
 
-// A row's results from its sums; called by every thread of the group that
-// writes them, `key` the sorted list.
+// The target's logit, which lane 32 of the wave that writes a row reads
+// ahead (`real`: the row has one).
+struct Target {
+  float x;
+  bool real;
+};
 template <typename T>
-__device__ __forceinline__ void finish_row(const LogprobOut& o, int64_t n, const T* row, const void* targets, int64_t V,
-                                           float scale, int top, RowSums r, const uint64_t* key, int tid) {
-  const float l2 = log2f(r.s), ls = kLn2 * l2;
+__device__ __forceinline__ Target read_target(const LogprobOut& o, int64_t n, const T* row, const void* targets,
+                                              int64_t V, int tid) {
+  Target t = {0.f, false};
+  if (tid == 32 && o.logp) {
+    const int64_t id = id_at(targets, n, o.id64);
+    t.real = id >= 0 && id < V;
+    if (t.real) t.x = Elem<T>::load(row + id);
+  }
+  return t;
+}
+
+// A row's results from its sums, by one wave; lane i holds key i of the list.
+__device__ __forceinline__ void finish_row(const LogprobOut& o, int64_t n, Target target, float scale, int top,
+                                           RowSums r, uint64_t key, int tid) {
+  const float l2 = log2f(r.s), ls = kLn2 * (l2 - r.lost(scale * kLog2e));
   if (tid == 0) {
     o.record[2 * n] = r.m;
     o.record[2 * n + 1] = ls;
     if (o.lse) o.lse[n] = r.m * scale + ls;
     if (o.entropy) o.entropy[n] = r.m == -INFINITY && r.s == 0.f ? 0.f : kLn2 * (l2 - r.t / r.s);
   }
-  if (tid == 32 && o.logp) {
-    const int64_t id = id_at(targets, n, o.id64);
-    o.logp[n] = id >= 0 && id < V ? log_prob(Elem<T>::load(row + id), scale, r.m, ls) : 0.f;
-  }
+  if (tid == 32 && o.logp) o.logp[n] = target.real ? log_prob(target.x, scale, r.m, ls) : 0.f;
   if (tid < top) {
-    const uint64_t k = key[tid];
-    const uint32_t id = ~(uint32_t)k;
-    o.top_logp[n * top + tid] = log_prob(from_order((uint32_t)(k >> 32)), scale, r.m, ls);
+    const uint32_t id = ~(uint32_t)key;
+    o.top_logp[n * top + tid] = log_prob(from_order((uint32_t)(key >> 32)), scale, r.m, ls);
     if (o.id64) ((int64_t*)o.top_ids)[n * top + tid] = id;
     else ((int32_t*)o.top_ids)[n * top + tid] = (int32_t)id;
   }
 }
 
-// A work-group per (row, part).
+// A wave per (row, part): the fixed work (joins of sums and lists, threshold)
+// is paid once per wave and covered by the row's hundred and more logits per
+// lane.  (2049 rows of 10007 fp16 logits with 5 alternatives: 19 us; with a
+// work-group of four waves per row and its joins in LDS 25 us; 16 rows of
+// 131072 fp32 with 8, in 64 parts a row: 7 us and 4 for the join, with
+// work-groups 11 and 4.)  The arithmetic, about ten vector instructions a
+// logit with the exponential counting four, is as long as the memory for
+// 16-bit logits: 16384 rows of 32768 bf16 take 195-230 us, 4.7-5.5 TB/s.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits, const void* targets, int64_t V,
-                                                                 int64_t ld, float scale, int top, int parts,
+__global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits, const void* targets, int64_t N,
+                                                                 int64_t V, int64_t ld, float scale, int top, int parts,
                                                                  int64_t part, LogprobOut out, uint64_t* wkey,
                                                                  f32x4_t* wsum) {
   constexpr int E = vec_of<T>();
-  constexpr int U = 4;  // vectors a thread has in flight
-  __shared__ RowSums sums[kLpWaves];
-  __shared__ uint64_t keys[kLpWaves * LSTM_MAX_TOP], best[LSTM_MAX_TOP];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t n = blockIdx.x / parts;
-  const int pt = (int)(blockIdx.x - n * parts);
+  constexpr int U = kLpVecs;
+  __shared__ TopLds tops[TOP ? 4 : 1];
+  TopLds* lds = tops + (TOP ? threadIdx.x >> 6 : 0);
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n = parts == 1 ? unit : unit / parts;
+  if (n >= N) return;
+  const int pt = (int)(unit - n * parts);
   const T* row = logits + n * ld;
   const int64_t lo = (int64_t)pt * part, hi = lo + part < V ? lo + part : V;
   const float c2 = scale * kLog2e, slack = kSlack / c2;
+  Target target = {0.f, false};
+  if (parts == 1) target = read_target<T>(out, n, row, targets, V, lane);
 
   RowSums r = {-INFINITY, 0.f, 0.f};
   TopList list;
   list.clear();
-  // C logits of this lane at ids id0 .. (valid: the lane has any)
-  auto take = [&](const float* f, auto C, int64_t id0, bool valid) {
+  // C logits of this lane, E at a time 64 E apart, the first at id0 of the
+  // part (count: past its end, where -inf stands for them)
+  const uint32_t count = (uint32_t)(hi - lo);
+  auto take = [&](float* f, auto C, uint32_t id0) {
     constexpr int c = decltype(C)::value;
     float vm = f[0];
 #pragma unroll
     for (int j = 1; j < c; ++j) vm = fmaxf(vm, f[j]);
-    if (__ballot(vm > r.m + slack || (vm > r.m && r.m == -INFINITY))) {
-      const float to = wave_max(vm);
-      r.move(to, c2);
+    if (__ballot(vm > r.m + slack || (vm > r.m && r.m == -INFINITY))) r.move(fmaxf(wave_max(vm), r.m), c2);
+    if (TOP && __ballot(list.wants(vm))) {
+      // each lane's candidates as bits, then one of every lane at a time
+      // (mostly there is one in all)
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < c; ++j) bits |= list.wants(f[j]) ? 1u << j : 0u;
+      while (__ballot(bits != 0)) {
+        const int j = bits ? __builtin_ctz(bits) : 0;
+        const uint32_t id = id0 + (j / E) * (64 * E) + j % E;
+        const bool in = bits != 0 && id < count;
+        const uint64_t key = ((uint64_t)order_of(pick<c>(f, bits & -bits)) << 32) | ~((uint32_t)lo + id);
+        bits &= bits - 1;
+        list.append(lds, in ? key : 0, __ballot(bits != 0) != 0, top, lane);
+      }
     }
-    const float m = r.ref();
+    const bool huge = r.huge(c2) && r.m != -INFINITY;
+    if (huge) {
+#pragma unroll
+      for (int j = 0; j < c; ++j) f[j] -= r.m;
+    }
+    const float m2 = huge || r.m == -INFINITY ? 0.f : r.m * c2;
 #pragma unroll
     for (int j = 0; j < c; ++j) {
-      const float y = (f[j] - m) * c2, e = __builtin_amdgcn_exp2f(y);
+      const float y = __builtin_fmaf(f[j], c2, -m2), e = __builtin_amdgcn_exp2f(y);
       r.s += e;
       r.t += e * fmaxf(y, -1000.f);  // e = 0 there
     }
-    if (TOP && __ballot(valid && list.wants(vm))) {
-#pragma unroll
-      for (int j = 0; j < c; ++j)
-        list.insert(valid ? order_of(f[j]) : 0, valid ? ~(uint32_t)(id0 + j) : 0, top, lane);
-    }
   };
   using One = std::integral_constant<int, 1>;
-  using Vec = std::integral_constant<int, E>;
+  using Take = std::integral_constant<int, U * E>;
 
   // the part's logits up to the first 16-byte border, and past the last
-  const int64_t off = (int64_t)(((uintptr_t)(row + lo) & 15u) / sizeof(T));
-  int64_t head = off ? E - off : 0;
-  if (head > hi - lo) head = hi - lo;
-  const int64_t nv = (hi - lo - head) / E, tail0 = lo + head + nv * E;
-  if (w == 0 && (head > 0 || tail0 < hi)) {
-    const bool is_head = lane < head, is_tail = lane >= 32 && tail0 + lane - 32 < hi;
-    const int64_t id = is_head ? lo + lane : tail0 + lane - 32;
-    float f[1] = {-INFINITY};
-    if (is_head || is_tail) f[0] = Elem<T>::load(row + id);
-    take(f, One{}, id, is_head || is_tail);
-  }
+  const uint32_t off = (uint32_t)(((uintptr_t)(row + lo) & 15u) / sizeof(T));
+  uint32_t head = off ? E - off : 0;
+  if (head > count) head = count;
+  const uint32_t nv = (count - head) / E, tail0 = head + nv * E;
   const u32x4_t* body = (const u32x4_t*)(row + lo + head);
-  for (int64_t v0 = 0; v0 < nv; v0 += (int64_t)kLpThreads * U) {
-    u32x4_t raw[U];
+  u32x4_t raw[U], none;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    none[j] = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, f16_t>::value ? 0xfc00fc00u : 0xff80ff80u;  // -inf
+  auto fetch = [&](uint32_t v0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t v = v0 + u * kLpThreads + tid;
+      const uint32_t v = v0 + u * 64 + lane;
+      raw[u] = none;
       if (v < nv) raw[u] = body[v];
     }
+  };
+  fetch(0);
+  const bool is_head = lane < (int)head, is_tail = lane >= 32 && tail0 + lane - 32 < count;
+  float edge[1] = {-INFINITY};
+  const uint32_t edge_id = is_head ? lane : is_tail ? tail0 + lane - 32 : count;
+  if (is_head || is_tail) edge[0] = Elem<T>::load(row + lo + edge_id);
+  if (TOP) {
+    float vm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t v = v0 + u * kLpThreads + tid;
-      if (v0 + u * kLpThreads + w * 64 >= nv) break;  // no lane of the wave
       float f[E];
-      if (v < nv) {
-        unpack<T>(raw[u], f);
-      } else {
+      unpack<T>(raw[u], f);
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] = -INFINITY;
-      }
-      take(f, Vec{}, lo + head + v * E, v < nv);
+      for (int j = 0; j < E; ++j) vm = fmaxf(vm, f[j]);
     }
+    list.set_floor(wave_threshold(lane < (int)nv ? order_of(vm) : 0, top));
   }
-  // the waves' sums on one reference, their lists as one
+  if (head > 0 || tail0 < count) take(edge, One{}, edge_id);
+#pragma unroll 1
+  for (uint32_t v0 = 0; v0 < nv; v0 += 64 * U) {  // one copy of its long body: the next loads run beside it
+    float f[U * E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) unpack<T>(raw[u], f + u * E);
+    if (v0 + 64 * U < nv) fetch(v0 + 64 * U);
+    take(f, Take{}, head + (v0 + lane) * E);
+  }
+  if (TOP) list.merge(lds, top, lane);
   r.s = wave_sum(r.s);
   r.t = wave_sum(r.t);
-  if (lane == 0) sums[w] = r;
-  if (TOP) {
-    if (lane < top) keys[w * top + lane] = ((uint64_t)list.hi << 32) | list.lo;
-    if (tid < top) best[tid] = 0;
-  }
-  __syncthreads();
-  RowSums a = sums[0];
-#pragma unroll
-  for (int k = 1; k < kLpWaves; ++k) {
-    RowSums b = sums[k];
-    const float to = fmaxf(a.m, b.m);
-    a.move(to, c2);
-    b.move(to, c2);
-    a.s += b.s;
-    a.t += b.t;
-  }
-  if (TOP) {
-    if (tid < kLpWaves * top) {
-      const uint64_t k = keys[tid];
-      int rank = 0;
-      for (int i = 0; i < kLpWaves * top; ++i) rank += keys[i] > k;
-      if (k != 0 && rank < top) best[rank] = k;
-    }
-    __syncthreads();
-  }
   if (parts == 1) {
-    finish_row<T>(out, n, row, targets, V, scale, TOP ? top : 0, a, best, tid);
+    finish_row(out, n, target, scale, TOP ? top : 0, r, list.key, lane);
   } else {
-    if (tid == 0) wsum[blockIdx.x] = f32x4_t{a.m, a.s, a.t, 0.f};
-    if (TOP && tid < top) wkey[(int64_t)blockIdx.x * top + tid] = best[tid];
+    if (lane == 0) wsum[unit] = f32x4_t{r.m, r.s, r.t, 0.f};
+    if (TOP && lane < top) wkey[unit * top + lane] = list.key;
   }
 }
 
@@ -276,10 +382,10 @@ template <typename T>
 __global__ void __launch_bounds__(64) logprob_join_kernel(const T* logits, const void* targets, int64_t V, int64_t ld,
                                                           float scale, int top, int parts, LogprobOut out,
                                                           const uint64_t* wkey, const f32x4_t* wsum) {
-  __shared__ uint64_t best[LSTM_MAX_TOP];
   const int lane = threadIdx.x;
   const int64_t n = blockIdx.x;
   const float c2 = scale * kLog2e;
+  const Target target = read_target<T>(out, n, logits + n * ld, targets, V, lane);
   RowSums r = {-INFINITY, 0.f, 0.f};
   if (lane < parts) {
     const f32x4_t q = wsum[n * parts + lane];
@@ -288,24 +394,23 @@ __global__ void __launch_bounds__(64) logprob_join_kernel(const T* logits, const
   r.move(wave_max(r.m), c2);
   r.s = wave_sum(r.s);
   r.t = wave_sum(r.t);
-  const uint64_t* mine = wkey + (n * parts + lane) * top;
-  int at = 0;
-  uint64_t head = lane < parts && top > 0 ? mine[0] : 0;
-  for (int k = 0; k < top; ++k) {
-    uint64_t big = head;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor((unsigned long long)big, o);
-      big = other > big ? other : big;
+  __shared__ TopLds lds;
+  TopList list;
+  list.clear();
+  if (top > 0) {
+    // the lists' largest keys bound the key `top` of all from below
+    const uint64_t* mine = wkey + (n * parts + lane) * top;
+    uint64_t key = lane < parts ? mine[0] : 0;
+    list.set_floor(wave_threshold((uint32_t)(key >> 32), top));
+    for (int k = 0; k < top; ++k) {
+      if (!__ballot(key > list.least)) break;  // the lists descend
+      const uint64_t now = key;
+      key = k + 1 < top && lane < parts ? mine[k + 1] : 0;
+      list.append(&lds, now, k + 1 < top, top, lane);
     }
-    if (lane == 0) best[k] = big;
-    if (head == big && big != 0) {
-      ++at;
-      head = at < top ? mine[at] : 0;
-    }
+    list.merge(&lds, top, lane);
   }
-  __syncthreads();
-  finish_row<T>(out, n, logits + n * ld, targets, V, scale, top, r, best, lane);
+  finish_row(out, n, target, scale, top, r, list.key, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -416,13 +521,13 @@ static hipError_t logprob_fwd_t(const LogprobPlan& p, const void* logits, const 
                                 const LogprobOut& o, hipStream_t s) {
   uint64_t* wkey = (uint64_t*)(ws + p.off_key);
   f32x4_t* wsum = (f32x4_t*)(ws + p.off_sum);
-  const unsigned grid = (unsigned)(p.N * p.parts);
+  const unsigned grid = (unsigned)((p.N * p.parts + 3) / 4);
   if (p.top > 0)
-    logprob_fwd_kernel<T, true><<<grid, kLpThreads, 0, s>>>((const T*)logits, targets, p.V, p.ld, p.scale, p.top,
-                                                            p.parts, p.part, o, wkey, wsum);
+    logprob_fwd_kernel<T, true><<<grid, kLpThreads, 0, s>>>((const T*)logits, targets, p.N, p.V, p.ld, p.scale,
+                                                            p.top, p.parts, p.part, o, wkey, wsum);
   else
-    logprob_fwd_kernel<T, false><<<grid, kLpThreads, 0, s>>>((const T*)logits, targets, p.V, p.ld, p.scale, 0, p.parts,
-                                                             p.part, o, wkey, wsum);
+    logprob_fwd_kernel<T, false><<<grid, kLpThreads, 0, s>>>((const T*)logits, targets, p.N, p.V, p.ld, p.scale, 0,
+                                                             p.parts, p.part, o, wkey, wsum);
   if (p.parts > 1)
     logprob_join_kernel<T><<<(unsigned)p.N, 64, 0, s>>>((const T*)logits, targets, p.V, p.ld, p.scale, p.top, p.parts,
                                                         o, wkey, wsum);
