@@ -160,14 +160,14 @@ def test_refusals(lstm):
     L, s = lstm.lib(), m.shape
     s.ld_table = s.ld_out = 8
     out = torch.full((9, 8), 7.0, device="cuda")
-    ws = m.workspace
     P = lambda t: t.data_ptr()  # noqa: E731
     assert L.lstm_embed_fwd(ctypes.byref(s), None, P(table), P(out), None) == -1
     assert L.lstm_embed_fwd(ctypes.byref(s), P(ids), P(table) + 2, P(out), None) == -4
     assert L.lstm_embed_fwd(ctypes.byref(s), P(ids) + 4, P(table), P(out), None) == -4
-    assert L.lstm_embed_bwd(ctypes.byref(s), P(ids), P(table), P(ws), ws.numel() - 1, P(out), None) == -5
-    assert L.lstm_embed_bwd(ctypes.byref(s), P(ids), P(table), P(ws) + 8, ws.numel(), P(out), None) == -4
-    assert L.lstm_embed_bwd(ctypes.byref(s), P(ids), P(table), None, ws.numel(), P(out), None) == -1
+    many = lstm.Embedding(5000, 9, 8, lstm.F32)  # enough tokens to need a workspace
+    ws, ids5, rows5 = many.workspace, torch.zeros(5000, dtype=torch.int64, device="cuda"), torch.zeros(5000, 8, device="cuda")
+    bwd = lambda w, n: L.lstm_embed_bwd(ctypes.byref(many.shape), P(ids5), P(rows5), w, n, P(out), None)  # noqa: E731
+    assert bwd(P(ws), ws.numel() - 1) == -5 and bwd(P(ws) + 8, ws.numel()) == -4 and bwd(None, ws.numel()) == -1
     s.ld_out = 7
     assert L.lstm_embed_fwd(ctypes.byref(s), P(ids), P(table), P(out), None) == -2
     s.ld_out, s.id_type = 8, 5
