@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblstm.so")
 SOURCES = ["lstm_api.hip", "gemm.hip", "recurrent.hip", "recurrent_vec.hip", "recurrent_bwd.hip", "exchange_probe.hip",
            "stack_api.hip", "mfma_probe.hip", "seq_api.hip", "embed.hip", "logprob.hip",
-           "attend.hip", "attend_bwd.hip"]
+           "attend.hip", "attend_bwd_f32.hip", "attend_bwd_bf16.hip", "attend_bwd_f16.hip"]
 ARCH = "gfx950"
 
 

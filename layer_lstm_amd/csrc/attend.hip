@@ -136,17 +136,13 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 512 ? 1 : 2) attend_fwd_
 }
 
 // ---------------------------------------------------------------------------
-// Few rows.  Waves of a work-group: as many as hold their two stages of a K
-// and a V tile of 32 keys in 128 KB.
-template <typename T, int DP> constexpr int step_waves() {
-  return Tile<T, DP>::kBytes32 * 4 * 4 <= 128 * 1024 ? 4 : Tile<T, DP>::kBytes32 * 4 * 2 <= 128 * 1024 ? 2 : 1;
-}
-
+// Few rows (step_waves in attend_common.hpp): the keys' tiles dealt to the
+// waves, the waves' parts joined in LDS.
 template <typename T, int DP, bool DMA>
 __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_step_kernel(AttendArgs a) {
   using TL = Tile<T, DP>;
   constexpr int NW = step_waves<T, DP>(), TB = TL::kBytes32;
-  extern __shared__ __attribute__((aligned(16))) char lds[];  // per wave: K, V tiles, twice
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // per wave: K, V tile
   __shared__ float wm[NW][32], wl[NW][32];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int grp, tile;
@@ -164,7 +160,7 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_step_ker
   Loader<T, DP, 32, 1, DMA> lk, lv;
   lk.init((const T*)a.k + b * a.ks.b + hk * a.ks.h, a.ks.t, a.D, a.whole & kWholeK, mask, 0, lane);
   lv.init((const T*)a.v + b * a.vs.b + hk * a.vs.h, a.vs.t, a.D, a.whole & kWholeV, mask, 0, lane);
-  char* mine = lds + w * 4 * TB;
+  char* mine = lds + w * 2 * TB;
 
   f32x16_t o[DP / 32];
 #pragma unroll
@@ -180,28 +176,18 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_step_ker
     lv.load(first * 32, end, mine + TB);
     bits = key_bits(mask, first * 32, end, lane);
   }
-  int stage = 0;
   for (int i = first; i < last; i += NW) {
-    char* cur = mine + stage * 2 * TB;
-    char* nxt = mine + (stage ^ 1) * 2 * TB;
     const uint64_t now = bits;
-    if (i + NW < last) {
-      bits = key_bits(mask, (i + NW) * 32, end, lane);
-      // the other stage was read by the products of the tile before
-      __builtin_amdgcn_s_waitcnt(kLgkm0);
-      lk.load((i + NW) * 32, end, nxt);
-      lv.load((i + NW) * 32, end, nxt + TB);
-      // all but the loads just issued (63 at most can be told apart)
-      constexpr int kNew = 2 * Loader<T, DP, 32, 1, DMA>::kLoads;
-      if constexpr (DMA && kNew <= 63) __builtin_amdgcn_s_waitcnt(vmcnt_imm(kNew));
-      else wait_vmem();
-    } else {
-      wait_vmem();
-    }
+    wait_vmem();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    attend_tile<T, DP, 1>(cur, cur + TB, now, q, o, m, l, c2, lane);
-    stage ^= 1;
+    attend_tile<T, DP, 1>(mine, mine + TB, now, q, o, m, l, c2, lane);
+    if (i + NW < last) {
+      __builtin_amdgcn_s_waitcnt(kLgkm0);  // every fragment of this tile is read
+      lk.load((i + NW) * 32, end, mine);
+      lv.load((i + NW) * 32, end, mine + TB);
+      bits = key_bits(mask, (i + NW) * 32, end, lane);
+    }
   }
   l += other_half(l);
   // the waves' parts on one reference: column r of wave w at its own stages
@@ -233,7 +219,7 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_step_ker
   for (int d = 2 * w + (lane >> 5); d < a.D; d += 2 * NW) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) v += ((const float*)(lds + k * 4 * TB))[d * 32 + (lane & 31)] * by[k];
+    for (int k = 0; k < NW; ++k) v += ((const float*)(lds + k * 2 * TB))[d * 32 + (lane & 31)] * by[k];
     if (a.splits == 1) out[d] = Elem<T>::from_f(as_f32(v * inv));
     else part[d] = v;
   }
@@ -259,19 +245,34 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendArgs a, int row_
   const int b = (int)(grp / a.Hk);
   const uint32_t h = (uint32_t)(grp - (int64_t)b * a.Hk) * a.G + (r - t * a.G);
   const int64_t unit = ((grp * row_tiles + r / 32) * a.splits) * 32 + (r & 31);  // + 32 per part
-  float top = -INFINITY;
-  for (int k = 0; k < a.splits; ++k) top = fmaxf(top, a.part_ml[2 * (unit + 32 * k)]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  for (int k = 0; k < a.splits; ++k)
-    sum += a.part_ml[2 * (unit + 32 * k) + 1] * __builtin_amdgcn_exp2f(a.part_ml[2 * (unit + 32 * k)] - ref);
+  // lane k: part k's statistics (at most 64 parts)
+  float m = -INFINITY, l = 0.f;
+  if (lane < a.splits) {
+    m = a.part_ml[2 * (unit + 32 * lane)];
+    l = a.part_ml[2 * (unit + 32 * lane) + 1];
+  }
+  float top = m;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+  const float by = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.f : top));
+  float sum = l * by;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   T* out = (T*)a.out + t * a.os.t + b * a.os.b + h * a.os.h;
-  for (int d = lane; d < a.D; d += 64) {
+  for (int d0 = 0; d0 < a.D; d0 += 64) {
+    const int d = d0 + lane;
+    const float* from = a.part + unit * a.D + (d < a.D ? d : 0);
     float v = 0.f;
-    for (int k = 0; k < a.splits; ++k)
-      v += a.part[(unit + 32 * k) * a.D + d] * __builtin_amdgcn_exp2f(a.part_ml[2 * (unit + 32 * k)] - ref);
-    out[d] = Elem<T>::from_f(as_f32(v * inv));
+    for (int k0 = 0; k0 < a.splits; k0 += 8) {  // eight loads in flight
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = k0 + k < a.splits ? from[(int64_t)32 * (k0 + k) * a.D] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v += x[k] * __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(by), (k0 + k) & 63));
+    }
+    if (d < a.D) out[d] = Elem<T>::from_f(as_f32(v * inv));
   }
   if (lane == 0) a.lse[((int64_t)b * a.Hq + h) * a.Tq + t] = kLn2 * (top + __builtin_amdgcn_logf(sum));
 }
@@ -287,13 +288,19 @@ void make_attend_plan(const lstm_attend_shape& s, int cus, AttendPlan* p) {
   p->row_tiles32 = (int)((M + 31) / 32);
   // the shared kernel where its work-groups fill at least half the device
   p->step = M <= 32 || groups * ((M + 127) / 128) < cus / 2;
+  p->few_rows = p->step;
+  p->few_keys = groups * ((s.Tk + 127) / 128) < cus / 2;
   p->splits = 1;
   if (p->step && groups > 0 && M > 0) {
-    // two work-groups a compute unit, each wave at least two tiles of keys
-    const int64_t units = groups * p->row_tiles32, per = 32 * p->DP * e * 16 <= 128 * 1024 ? 4 : 2;
-    int64_t n = 2 * (int64_t)cus / units;
-    const int64_t most = s.Tk / (32 * per * 2);
-    if (n > most) n = most;
+    // fill the device, or, with long keys, twice that, which evens out
+    // sequences of different lengths; never less than two tiles a wave (the
+    // join costs a launch)
+    const int64_t units = groups * p->row_tiles32, tile = 2 * 32 * p->DP * e;
+    const int64_t waves = step_waves_of(tile), keys = 32 * waves;
+    const int64_t fill = (cus * (waves * tile <= 80 * 1024 ? 2 : 1) + units - 1) / units;
+    int64_t n = s.Tk / (8 * keys) < 2 * fill ? s.Tk / (8 * keys) : 2 * fill;
+    if (n < fill) n = fill;
+    if (n > s.Tk / (2 * keys)) n = s.Tk / (2 * keys);
     if (n > 64) n = 64;
     if (n < 1) n = 1;
     p->splits = (int)n;
@@ -315,7 +322,7 @@ static hipError_t attend_fwd_t(const AttendPlan& p, const AttendArgs& a0, hipStr
   constexpr int C = Tile<T, DP>::C;
   if (p.step) {
     constexpr int NW = step_waves<T, DP>();
-    const size_t lds = (size_t)NW * 4 * Tile<T, DP>::kBytes32;
+    const size_t lds = (size_t)NW * 2 * Tile<T, DP>::kBytes32;
     a.tiles = p.row_tiles32 * p.splits;
     const unsigned grid = attend_grid(&a);
     const hipError_t e = allow_lds((const void*)attend_step_kernel<T, DP, DMA>, lds);
@@ -336,17 +343,37 @@ static hipError_t attend_fwd_t(const AttendPlan& p, const AttendArgs& a0, hipStr
   return hipGetLastError();
 }
 
+template <typename T>
+static hipError_t attend_fwd_dp(const AttendPlan& p, const AttendArgs& a, hipStream_t s) {
+  if (p.dma) {
+    switch (p.DP) {
+      case 32: return attend_fwd_t<T, 32, true>(p, a, s);
+      case 64: return attend_fwd_t<T, 64, true>(p, a, s);
+      case 96: return attend_fwd_t<T, 96, true>(p, a, s);
+      case 128: return attend_fwd_t<T, 128, true>(p, a, s);
+      case 192: return attend_fwd_t<T, 192, true>(p, a, s);
+      default: return attend_fwd_t<T, 256, true>(p, a, s);
+    }
+  }
+  // rows that go through registers: fewer sizes
+  return p.DP <= 64 ? attend_fwd_t<T, 64, false>(p, a, s)
+         : p.DP <= 128 ? attend_fwd_t<T, 128, false>(p, a, s) : attend_fwd_t<T, 256, false>(p, a, s);
+}
+
 hipError_t launch_attend_fwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s) {
   if (a.B == 0 || a.M == 0) return hipSuccess;
   Timed tm(8, s);
-#define ATTEND_DP(T, N) \
-  if (p.DP == N) return p.dma ? attend_fwd_t<T, N, true>(p, a, s) : attend_fwd_t<T, N, false>(p, a, s)
-#define ATTEND_T(T) \
-  ATTEND_DP(T, 32); ATTEND_DP(T, 64); ATTEND_DP(T, 96); ATTEND_DP(T, 128); ATTEND_DP(T, 192); ATTEND_DP(T, 256)
-  if (p.dtype == LSTM_F32) { ATTEND_T(float); }
-  if (p.dtype == LSTM_BF16) { ATTEND_T(bf16_t); }
-  if (p.dtype == LSTM_F16) { ATTEND_T(f16_t); }
-  return hipErrorInvalidValue;
+  if (p.dtype == LSTM_F32) return attend_fwd_dp<float>(p, a, s);
+  if (p.dtype == LSTM_BF16) return attend_fwd_dp<bf16_t>(p, a, s);
+  return attend_fwd_dp<f16_t>(p, a, s);
+}
+
+hipError_t launch_attend_bwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s) {
+  if (a.B == 0) return hipSuccess;
+  Timed tm(8, s);
+  if (p.dtype == LSTM_F32) return launch_attend_bwd_f32(p, a, s);
+  if (p.dtype == LSTM_BF16) return launch_attend_bwd_bf16(p, a, s);
+  return launch_attend_bwd_f16(p, a, s);
 }
 
 }  // namespace lstm

@@ -268,6 +268,38 @@ struct Loader {
   }
 };
 
+// The kernels for few rows or keys give every wave of a work-group its own
+// tiles of the axis they sum over: as many waves (up to 8) as hold the two
+// tiles of 32 rows they read in 128 KB; their loads overlap each other's
+// products, and their sums are joined in LDS.
+constexpr int step_waves_of(int64_t two_tiles) {
+  return 128 * 1024 / two_tiles >= 8 ? 8 : 128 * 1024 / two_tiles >= 4 ? 4 : 2;
+}
+template <typename T, int DP> constexpr int step_waves() { return step_waves_of(2 * Tile<T, DP>::kBytes32); }
+
+// Sum over the waves of their products' registers (column lane % 32), each in
+// its own part (two tiles) of LDS; `f(d, v)` takes the sums of column
+// lane % 32, whose rows d are dealt to the waves and the halves of a wave.
+// Every wave has read its tiles when it calls this.
+template <typename T, int DP, class F>
+__device__ __forceinline__ void join_waves(const f32x16_t* acc, char* lds, int D, int w, int lane, F f) {
+  constexpr int NW = step_waves<T, DP>(), kPart = 2 * Tile<T, DP>::kBytes32;
+  static_assert(DP * 32 * 4 <= kPart, "a wave's registers fit its part");
+  float* mine = (float*)(lds + w * kPart);  // [DP][32]
+  __syncthreads();
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine[(32 * dt + reg_row(i, lane)) * 32 + (lane & 31)] = acc[dt][i];
+  __syncthreads();
+  for (int d = 2 * w + (lane >> 5); d < D; d += 2 * NW) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) v += ((const float*)(lds + k * kPart))[d * 32 + (lane & 31)];
+    f(d, v);
+  }
+}
+
 // 16-byte operands along d of one row in registers (zeros where !ok).
 template <typename T, int DP>
 __device__ __forceinline__ void load_row_frags(const T* row, int D, bool whole, bool ok, int lane, u32x4_t* f) {

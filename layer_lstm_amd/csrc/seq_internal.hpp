@@ -100,18 +100,22 @@ hipError_t launch_logprob_bwd(const LogprobPlan& p, const void* logits, const vo
                               const float* entropy, const void* top_ids, const float* dlogp, const float* dentropy,
                               const float* dtop, void* dlogits, hipStream_t s);
 
-// ---- attend.hip, attend_bwd.hip ----
+// ---- attend.hip, attend_bwd.hpp ----
 struct AttendArgs;
 struct AttendPlan {
   int dtype, DP;    // DP: the head size the kernels run with
   int dma;          // rows are whole aligned 16-byte chunks that do not overlap
   int step;         // forward by attend_step_kernel,
   int splits;       //   the keys of a row tile split over this many work-groups
+  int few_rows, few_keys;  // backward: dq, dk and dv by the kernels that split the sums over waves
   int row_tiles32;  // tiles of 32 rows per (sequence, key head)
   size_t off_part, off_ml, off_delta, total_fwd, total_bwd;
 };
 void make_attend_plan(const lstm_attend_shape& s, int cus, AttendPlan* p);
 hipError_t launch_attend_fwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s);
 hipError_t launch_attend_bwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s);
+hipError_t launch_attend_bwd_f32(const AttendPlan& p, const AttendArgs& a, hipStream_t s);
+hipError_t launch_attend_bwd_bf16(const AttendPlan& p, const AttendArgs& a, hipStream_t s);
+hipError_t launch_attend_bwd_f16(const AttendPlan& p, const AttendArgs& a, hipStream_t s);
 
 }  // namespace lstm
