@@ -325,7 +325,7 @@ static hipError_t attend_fwd_t(const AttendPlan& p, const AttendArgs& a0, hipStr
     const size_t lds = (size_t)NW * 2 * Tile<T, DP>::kBytes32;
     a.tiles = p.row_tiles32 * p.splits;
     const unsigned grid = attend_grid(&a);
-    const hipError_t e = allow_lds((const void*)attend_step_kernel<T, DP, DMA>, lds);
+    const hipError_t e = allow_lds<attend_step_kernel<T, DP, DMA>>(lds);
     if (e != hipSuccess) return e;
     attend_step_kernel<T, DP, DMA><<<grid, 64 * NW, lds, s>>>(a);
     if (p.splits > 1) {
@@ -336,7 +336,7 @@ static hipError_t attend_fwd_t(const AttendPlan& p, const AttendArgs& a0, hipStr
     const size_t lds = (size_t)4 * fwd_keys<T, DP>() * C * 16;
     a.tiles = (int)((a.M + 127) / 128);
     const unsigned grid = attend_grid(&a);
-    const hipError_t e = allow_lds((const void*)attend_fwd_kernel<T, DP, DMA>, lds);
+    const hipError_t e = allow_lds<attend_fwd_kernel<T, DP, DMA>>(lds);
     if (e != hipSuccess) return e;
     attend_fwd_kernel<T, DP, DMA><<<grid, 256, lds, s>>>(a);
   }

@@ -399,9 +399,8 @@ static hipError_t attend_dkv_t(const AttendPlan& p, AttendArgs a, hipStream_t s)
   const size_t lds = (few ? 2 * step_waves<T, DP>() : 4) * (size_t)Tile<T, DP>::kBytes32;
   a.tiles = few ? (a.Tk + 31) / 32 : (a.Tk + 127) / 128;
   const unsigned grid = attend_grid(&a);
-  const void* kernel = few ? (const void*)attend_dkv_few_kernel<T, DP, DMA, DV, DK>
-                           : (const void*)attend_dkv_kernel<T, DP, DMA, DV, DK>;
-  const hipError_t e = allow_lds(kernel, lds);
+  const hipError_t e = few ? allow_lds<attend_dkv_few_kernel<T, DP, DMA, DV, DK>>(lds)
+                           : allow_lds<attend_dkv_kernel<T, DP, DMA, DV, DK>>(lds);
   if (e != hipSuccess) return e;
   if (few)
     attend_dkv_few_kernel<T, DP, DMA, DV, DK><<<grid, 64 * step_waves<T, DP>(), lds, s>>>(a);
@@ -419,8 +418,8 @@ static hipError_t attend_bwd_t(const AttendPlan& p, const AttendArgs& a0, hipStr
                            : (size_t)4 * dq_keys<T, DP>() * Tile<T, DP>::C * 16;
     a.tiles = few ? p.row_tiles32 : (int)((a.M + 127) / 128);
     const unsigned grid = attend_grid(&a);
-    const hipError_t e = allow_lds(few ? (const void*)attend_dq_few_kernel<T, DP, DMA>
-                                       : (const void*)attend_dq_kernel<T, DP, DMA>, lds);
+    const hipError_t e =
+        few ? allow_lds<attend_dq_few_kernel<T, DP, DMA>>(lds) : allow_lds<attend_dq_kernel<T, DP, DMA>>(lds);
     if (e != hipSuccess) return e;
     if (few)
       attend_dq_few_kernel<T, DP, DMA><<<grid, 64 * step_waves<T, DP>(), lds, s>>>(a);

@@ -20,6 +20,8 @@
 // storage type, in fp32 not at all): a k index may be permuted as long as
 // both operands agree, and col_frag reads the rows in that order.
 #pragma once
+#include <atomic>
+
 #include "internal.hpp"
 #include "seq_internal.hpp"
 
@@ -188,10 +190,20 @@ static inline unsigned attend_grid(AttendArgs* a) {
   a->spread = !(n % 8 == 0 || n >= 64);
   return (a->spread ? n : (n + 7) / 8 * 8) * (unsigned)a->tiles;
 }
-// Dynamic LDS past 64 KB has to be asked for.
-static inline hipError_t allow_lds(const void* kernel, size_t bytes) {
-  return bytes > 64 * 1024 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-                           : hipSuccess;
+// Dynamic LDS past 64 KB has to be asked for, once per kernel (the static
+// is the instance's own) and device.
+template <auto Kernel>
+static inline hipError_t allow_lds(size_t bytes) {
+  if (bytes <= 64 * 1024) return hipSuccess;
+  static std::atomic<uint64_t> asked{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (bit && (asked.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+  e = hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == hipSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Valid keys of a sequence: below its length (and not masked).

@@ -189,10 +189,17 @@ def _ptr(t):
     return t.data_ptr() if t.numel() > 0 else None
 
 
+# The current stream's handle without a Stream object built for it (3 us a
+# call, which is a third of a small operator's).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def fwd_train(shape, x, W, b, h0, c0, y, hT, cT, workspace, ws_bytes=None, stream=None, check=True,
@@ -392,17 +399,15 @@ class Stack:
 
 
 # --- sequence-to-sequence operators -------------------------------------------
+_ID_TYPES = {torch.int64: I64, torch.int32: I32}
+
+
 def _workspace(fn, name, shape, device):
     n = ctypes.c_size_t(0)
     rc = fn(ctypes.byref(shape), ctypes.byref(n))
     if rc != OK:
         raise LstmError(rc, name)
     return torch.empty(n.value, dtype=torch.uint8, device=device)
-
-
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
 
 
 class Embedding:
@@ -415,25 +420,25 @@ class Embedding:
     def __init__(self, N, V, D, dtype=F32, scale=1.0, padding=None, device="cuda"):
         self.N, self.V, self.D, self.dtype, self.device = N, V, D, dtype, device
         self.shape = EmbedShape(N, V, D, D, D, -1 if padding is None else int(padding), float(scale), int(dtype), I64)
+        self._ref = ctypes.byref(self.shape)
         self.workspace = _workspace(_lib.lstm_embed_query, "lstm_embed_query", self.shape, device)
         self.tdtype = torch_dtype(dtype)
         self.out = self.dtable = None
 
     def _ids(self, ids):
-        _need(ids.numel() == self.N and ids.is_contiguous(), f"ids: {self.N} contiguous tokens")
-        _need(ids.dtype in (torch.int64, torch.int32), "ids: int32 or int64")
-        self.shape.id_type = I64 if ids.dtype == torch.int64 else I32
-        return ids
+        if ids.numel() != self.N or not ids.is_contiguous() or ids.dtype not in _ID_TYPES:
+            raise ValueError(f"ids: {self.N} contiguous tokens, int32 or int64")
+        self.shape.id_type = _ID_TYPES[ids.dtype]
 
     def forward(self, ids, table, stream=None):
         """out [*ids.shape, D] = scale * table[ids]."""
         self._ids(ids)
-        _need(table.dtype == self.tdtype and table.shape == (self.V, self.D) and (self.D <= 1 or table.stride(1) == 1),
-              f"table: [{self.V}, {self.D}] of {self.tdtype}, rows contiguous")
+        if table.dtype != self.tdtype or table.shape != (self.V, self.D) or (self.D > 1 and table.stride(1) != 1):
+            raise ValueError(f"table: [{self.V}, {self.D}] of {self.tdtype}, rows contiguous")
         if self.out is None or self.out.shape[:-1] != ids.shape:
             self.out = torch.empty((*ids.shape, self.D), dtype=self.tdtype, device=self.device)
         self.shape.ld_table, self.shape.ld_out = max(table.stride(0), self.D), self.D
-        rc = _lib.lstm_embed_fwd(ctypes.byref(self.shape), _ptr(ids), _ptr(table), _ptr(self.out), _stream(stream))
+        rc = _lib.lstm_embed_fwd(self._ref, _ptr(ids), _ptr(table), _ptr(self.out), _stream(stream))
         if rc != OK:
             raise LstmError(rc, "lstm_embed_fwd")
         return self.out
@@ -441,15 +446,16 @@ class Embedding:
     def backward(self, ids, dout, stream=None):
         """dtable [V, D] of dout [*ids.shape, D]."""
         self._ids(ids)
-        _need(dout.dtype == self.tdtype and dout.shape == (*ids.shape, self.D),
-              f"dout: {[*ids.shape, self.D]} of {self.tdtype}")
+        if dout.dtype != self.tdtype or dout.shape != (*ids.shape, self.D):
+            raise ValueError(f"dout: {[*ids.shape, self.D]} of {self.tdtype}")
         rows = dout if dout.dim() == 2 else dout.view(self.N, self.D)
-        _need(self.D <= 1 or rows.stride(1) == 1, "dout: rows contiguous")
+        if self.D > 1 and rows.stride(1) != 1:
+            raise ValueError("dout: rows contiguous")
         if self.dtable is None:
             self.dtable = torch.empty((self.V, self.D), dtype=self.tdtype, device=self.device)
         self.shape.ld_table, self.shape.ld_out = self.D, max(rows.stride(0), self.D)
-        rc = _lib.lstm_embed_bwd(ctypes.byref(self.shape), _ptr(ids), _ptr(rows), _ptr(self.workspace),
-                                 self.workspace.numel(), _ptr(self.dtable), _stream(stream))
+        rc = _lib.lstm_embed_bwd(self._ref, _ptr(ids), _ptr(rows), _ptr(self.workspace), self.workspace.numel(),
+                                 _ptr(self.dtable), _stream(stream))
         if rc != OK:
             raise LstmError(rc, "lstm_embed_bwd")
         return self.dtable
@@ -473,6 +479,7 @@ class Attention:
         rc = _lib.lstm_attend_query(ctypes.byref(self.shape), ctypes.byref(nf), ctypes.byref(nb))
         if rc != OK:
             raise LstmError(rc, "lstm_attend_query")
+        self._ref = ctypes.byref(self.shape)
         self.ws_bytes = max(nf.value, nb.value)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.tdtype = torch_dtype(dtype)
@@ -480,27 +487,28 @@ class Attention:
         self.lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=device)
         self.dq = self.dk = self.dv = None
 
-    def _strides(self, name, x, T, H):
-        _need(x.dtype == self.tdtype and x.shape == (T, self.B, H, self.D) and (self.D == 1 or x.stride(3) == 1),
-              f"{name}: {[T, self.B, H, self.D]} of {self.tdtype}, last dimension contiguous")
-        s = getattr(self.shape, name)
-        s.t, s.b, s.h = x.stride(0), x.stride(1), x.stride(2)
+    def _strides(self, name, s, x, T, H):
+        if x.dtype != self.tdtype or x.shape != (T, self.B, H, self.D) or (self.D > 1 and x.stride(3) != 1):
+            raise ValueError(f"{name}: {[T, self.B, H, self.D]} of {self.tdtype}, last dimension contiguous")
+        s.t, s.b, s.h = x.stride()[:3]
 
     def _inputs(self, q, k, v, k_length, key_mask):
-        self._strides("q", q, self.Tq, self.Hq)
-        self._strides("k", k, self.Tk, self.Hk)
-        self._strides("v", v, self.Tk, self.Hk)
-        _need(k_length is None or (k_length.dtype == torch.int32 and k_length.shape == (self.B,) and
-                                   k_length.is_contiguous()), f"k_length: int32 [{self.B}], contiguous")
+        self._strides("q", self.shape.q, q, self.Tq, self.Hq)
+        self._strides("k", self.shape.k, k, self.Tk, self.Hk)
+        self._strides("v", self.shape.v, v, self.Tk, self.Hk)
+        if k_length is not None and (k_length.dtype != torch.int32 or k_length.shape != (self.B,) or
+                                     not k_length.is_contiguous()):
+            raise ValueError(f"k_length: int32 [{self.B}], contiguous")
         if key_mask is not None:
-            _need(key_mask.dtype in (torch.bool, torch.uint8) and key_mask.shape == (self.B, self.Tk) and
-                  (self.Tk <= 1 or key_mask.stride(1) == 1), f"key_mask: bool or uint8 {[self.B, self.Tk]}, rows contiguous")
+            if key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (self.B, self.Tk) or \
+                    (self.Tk > 1 and key_mask.stride(1) != 1):
+                raise ValueError(f"key_mask: bool or uint8 {[self.B, self.Tk]}, rows contiguous")
             self.shape.mask_b = key_mask.stride(0)
 
     def forward(self, q, k, v, k_length=None, key_mask=None, stream=None):
         """o [Tq, B, Hq, D] and lse [B, Hq, Tq]."""
         self._inputs(q, k, v, k_length, key_mask)
-        rc = _lib.lstm_attend_fwd(ctypes.byref(self.shape), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length), _ptr(key_mask),
+        rc = _lib.lstm_attend_fwd(self._ref, _ptr(q), _ptr(k), _ptr(v), _ptr(k_length), _ptr(key_mask),
                                   _ptr(self.workspace), self.ws_bytes, _ptr(self.o), _ptr(self.lse), _stream(stream))
         if rc != OK:
             raise LstmError(rc, "lstm_attend_fwd")
@@ -509,12 +517,12 @@ class Attention:
     def backward(self, dout, q, k, v, k_length=None, key_mask=None, stream=None):
         """dq, dk, dv after a forward on the same inputs."""
         self._inputs(q, k, v, k_length, key_mask)
-        self._strides("dout", dout, self.Tq, self.Hq)
+        self._strides("dout", self.shape.dout, dout, self.Tq, self.Hq)
         if self.dq is None:
             self.dq = torch.empty((self.Tq, self.B, self.Hq, self.D), dtype=self.tdtype, device=self.device)
             self.dk, self.dv = (torch.empty((self.Tk, self.B, self.Hk, self.D), dtype=self.tdtype, device=self.device)
                                 for _ in range(2))
-        rc = _lib.lstm_attend_bwd(ctypes.byref(self.shape), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length),
+        rc = _lib.lstm_attend_bwd(self._ref, _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length),
                                   _ptr(key_mask), _ptr(self.o), _ptr(self.lse), _ptr(self.workspace), self.ws_bytes,
                                   _ptr(self.dq), _ptr(self.dk), _ptr(self.dv), _stream(stream))
         if rc != OK:
@@ -531,6 +539,7 @@ class LogProb:
     def __init__(self, N, V, dtype=F32, top=0, scale=1.0, device="cuda"):
         self.N, self.V, self.top, self.dtype, self.device = N, V, int(top), dtype, device
         self.shape = LogprobShape(N, V, V, V, float(scale), int(top), int(dtype), I64)
+        self._ref = ctypes.byref(self.shape)
         self.workspace = _workspace(_lib.lstm_logprob_query, "lstm_logprob_query", self.shape, device)
         self.tdtype = torch_dtype(dtype)
         self.record = torch.empty((N, 2), dtype=torch.float32, device=device)
@@ -539,11 +548,11 @@ class LogProb:
         self.top_ids = self.dlogits = None
 
     def _rows(self, logits, targets):
-        _need(logits.dtype == self.tdtype and logits.shape == (self.N, self.V) and
-              (self.V <= 1 or logits.stride(1) == 1), f"logits: [{self.N}, {self.V}] of {self.tdtype}, rows contiguous")
-        _need(targets.shape == (self.N,) and targets.is_contiguous() and targets.dtype in (torch.int64, torch.int32),
-              f"targets: [{self.N}] int32 or int64, contiguous")
-        self.shape.id_type = I64 if targets.dtype == torch.int64 else I32
+        if logits.dtype != self.tdtype or logits.shape != (self.N, self.V) or (self.V > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits: [{self.N}, {self.V}] of {self.tdtype}, rows contiguous")
+        if targets.shape != (self.N,) or not targets.is_contiguous() or targets.dtype not in _ID_TYPES:
+            raise ValueError(f"targets: [{self.N}] int32 or int64, contiguous")
+        self.shape.id_type = _ID_TYPES[targets.dtype]
         self.shape.ld = max(logits.stride(0), self.V)
 
     def forward(self, logits, targets, stream=None):
@@ -551,7 +560,7 @@ class LogProb:
         self._rows(logits, targets)
         if self.top_ids is None or self.top_ids.dtype != targets.dtype:
             self.top_ids = torch.empty((self.N, self.top), dtype=targets.dtype, device=self.device)
-        rc = _lib.lstm_logprob_fwd(ctypes.byref(self.shape), _ptr(logits), _ptr(targets), _ptr(self.workspace),
+        rc = _lib.lstm_logprob_fwd(self._ref, _ptr(logits), _ptr(targets), _ptr(self.workspace),
                                    self.workspace.numel(), _ptr(self.record), _ptr(self.lse), _ptr(self.logp),
                                    _ptr(self.entropy), _ptr(self.top_logp), _ptr(self.top_ids), _stream(stream))
         if rc != OK:
@@ -565,13 +574,13 @@ class LogProb:
         self._rows(logits, targets)
         for name, g, shape in (("dlogp", dlogp, (self.N,)), ("dentropy", dentropy, (self.N,)),
                                ("dtop", dtop, (self.N, self.top))):
-            _need(g is None or (g.dtype == torch.float32 and g.shape == shape and g.is_contiguous()),
-                  f"{name}: {list(shape)} of float32, contiguous")
-        _need(self.N == 0 or dtop is None or not self.top or self.top_ids is not None and
-              self.top_ids.dtype == targets.dtype, "backward follows a forward on the same targets")
+            if g is not None and (g.dtype != torch.float32 or g.shape != shape or not g.is_contiguous()):
+                raise ValueError(f"{name}: {list(shape)} of float32, contiguous")
+        if dtop is not None and self.top and (self.top_ids is None or self.top_ids.dtype != targets.dtype):
+            raise ValueError("backward follows a forward on the same targets")
         if self.dlogits is None:
             self.dlogits = torch.empty((self.N, self.V), dtype=self.tdtype, device=self.device)
-        rc = _lib.lstm_logprob_bwd(ctypes.byref(self.shape), _ptr(logits), _ptr(targets), _ptr(self.record),
+        rc = _lib.lstm_logprob_bwd(self._ref, _ptr(logits), _ptr(targets), _ptr(self.record),
                                    _ptr(self.entropy), _ptr(self.top_ids), _ptr(dlogp), _ptr(dentropy),
                                    _ptr(dtop) if self.top else None, _ptr(self.dlogits), _stream(stream))
         if rc != OK:
