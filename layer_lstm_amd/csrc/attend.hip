@@ -23,6 +23,7 @@
 namespace lstm {
 
 constexpr float kMaxLag = 8.f;
+constexpr int kAheadRows = 8, kAheadCols = 4;  // fragments read ahead of their products
 
 // One tile of 32 KT keys for a wave's 32 rows.
 template <typename T, int DP, int KT>
@@ -31,11 +32,17 @@ __device__ __forceinline__ void attend_tile(const char* kt, const char* vt, uint
   using TL = Tile<T, DP>;
   f32x16_t s[KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t) {
-    s[t] = zero16();
-#pragma unroll
-    for (int kb = 0; kb < TL::KB; ++kb) s[t] = Mm<T>::mac(TL::row_frag(kt, 32 * t, kb, lane), q[kb], s[t]);
-  }
+  for (int t = 0; t < KT; ++t) s[t] = zero16();
+  // fragment f of the keys: subtile f / KB, k-block f % KB; of the values:
+  // k-block f / (DP / 32) of the rows, d-tile f % (DP / 32)
+  constexpr int NDT = DP / 32;
+  Ahead<KT * TL::KB, kAheadRows> ak;
+  Ahead<KT * TL::PB * NDT, kAheadCols> av;
+  auto read_k = [&](int f) { return TL::row_frag(kt, 32 * (f / TL::KB), f % TL::KB, lane); };
+  auto read_v = [&](int f) { return TL::col_frag(vt, TL::KR * (f / NDT), f % NDT, lane); };
+  ak.start(read_k);
+  ak.run(read_k, [&](int f, u32x4_t a) { s[f / TL::KB] = Mm<T>::mac(a, q[f % TL::KB], s[f / TL::KB]); });
+  av.start(read_v);
   constexpr uint64_t kAll = KT == 2 ? ~(uint64_t)0 : 0xffffffffull;
   if ((bits & kAll) != kAll) {
 #pragma unroll
@@ -69,15 +76,10 @@ __device__ __forceinline__ void attend_tile(const char* kt, const char* vt, uint
       s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c2, -ref));
       l += s[t][i];
     }
+  u32x4_t p[KT * TL::PB];
 #pragma unroll
-  for (int t = 0; t < KT; ++t)
-#pragma unroll
-    for (int pb = 0; pb < TL::PB; ++pb) {
-      const u32x4_t p = TL::reg_frag(s[t], pb);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt)
-        o[dt] = Mm<T>::mac(TL::col_frag(vt, 32 * t + TL::KR * pb, dt, lane), p, o[dt]);
-    }
+  for (int i = 0; i < KT * TL::PB; ++i) p[i] = TL::reg_frag(s[i / TL::PB], i % TL::PB);
+  av.run(read_v, [&](int f, u32x4_t a) { o[f % NDT] = Mm<T>::mac(a, p[f / NDT], o[f % NDT]); });
 }
 
 // Keys per tile of the shared kernel: two double-buffered tiles within 128 KB.
@@ -306,14 +308,14 @@ void make_attend_plan(const lstm_attend_shape& s, int cus, AttendPlan* p) {
     p->splits = (int)n;
   }
   size_t off = 0;
-  p->off_part = p->off_ml = p->off_delta = 0;
+  p->off_part = p->off_ml = 0;
   if (p->splits > 1) {
     const size_t rows = (size_t)groups * p->row_tiles32 * p->splits * 32;
     p->off_part = off; off += align256_seq(rows * (size_t)s.D * 4);
     p->off_ml = off; off += align256_seq(rows * 8);
   }
   p->total_fwd = off;
-  p->total_bwd = align256_seq((size_t)s.B * s.Hq * s.Tq * 4);
+  p->total_bwd = align256_seq((size_t)s.B * s.Hq * s.Tq * 8);
 }
 
 template <typename T, int DP, bool DMA>

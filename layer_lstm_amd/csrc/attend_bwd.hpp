@@ -44,7 +44,7 @@ struct QueryRow {
   float lse2, delta;
   uint32_t t, h;
   bool ok;
-  // r of the pair's M rows; also writes its delta
+  // r of the pair's M rows; `write`: its statistics go to memory for dk and dv
   __device__ __forceinline__ void load(const AttendArgs& a, int b, int hk, uint32_t r, bool write, int lane) {
     ok = r < a.M;
     t = r / a.G;
@@ -71,17 +71,24 @@ struct QueryRow {
       const int64_t li = ((int64_t)b * a.Hq + h) * a.Tq + t;
       const float v = a.lse[li];
       if (v != -INFINITY) lse2 = v * kLog2e - kInExponent<T>;
-      if (write && lane < 32) a.delta[li] = delta;
+      if (write && lane < 32) *(float2*)(a.stats + 2 * li) = make_float2(lse2, delta);
     }
   }
   // adds 32 keys' terms to dq (the factor `scale` of ds goes to the end)
   __device__ __forceinline__ void tile(const char* kt, const char* vt, uint32_t bits, f32x16_t* dq, float c2,
                                        int lane) const {
     f32x16_t s = zero16(), dp = zero16();
-#pragma unroll
-    for (int kb = 0; kb < TL::KB; ++kb) s = Mm<T>::mac(TL::row_frag(kt, 0, kb, lane), q[kb], s);
-#pragma unroll
-    for (int kb = 0; kb < TL::KB; ++kb) dp = Mm<T>::mac(TL::row_frag(vt, 0, kb, lane), g[kb], dp);
+    constexpr int NDT = DP / 32;
+    Ahead<2 * TL::KB, 8> rows;  // keys, then values
+    Ahead<TL::PB * NDT, 4> cols;
+    auto read_row = [&](int f) { return TL::row_frag(f < TL::KB ? kt : vt, 0, f % TL::KB, lane); };
+    auto read_col = [&](int f) { return TL::col_frag(kt, TL::KR * (f / NDT), f % NDT, lane); };
+    rows.start(read_row);
+    rows.run(read_row, [&](int f, u32x4_t x) {
+      if (f < TL::KB) s = Mm<T>::mac(x, q[f % TL::KB], s);
+      else dp = Mm<T>::mac(x, g[f % TL::KB], dp);
+    });
+    cols.start(read_col);
     if (bits != 0xffffffffu) {
       const uint32_t mine = bits >> (4 * (lane >> 5));
 #pragma unroll
@@ -90,12 +97,10 @@ struct QueryRow {
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) s[j] = exp_carried<T>(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - delta);
+    u32x4_t ds[TL::PB];
 #pragma unroll
-    for (int pb = 0; pb < TL::PB; ++pb) {
-      const u32x4_t ds = TL::reg_frag(s, pb);
-#pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = Mm<T>::mac(TL::col_frag(kt, TL::KR * pb, dt, lane), ds, dq[dt]);
-    }
+    for (int pb = 0; pb < TL::PB; ++pb) ds[pb] = TL::reg_frag(s, pb);
+    cols.run(read_col, [&](int f, u32x4_t x) { dq[f % NDT] = Mm<T>::mac(x, ds[f / NDT], dq[f % NDT]); });
   }
 };
 
@@ -196,159 +201,217 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dq_few_k
 }
 
 // ---------------------------------------------------------------------------
-// What a key (column lane % 32) keeps in registers.  DV, DK: which of the two
-// gradients (both, where a wave has the registers).
-template <typename T, int DP, bool DV, bool DK>
-struct Key {
+// What 32 NS keys (subtile n: column lane % 32) keep in registers.  DV, DK:
+// which of the two gradients (both, where a wave has the registers).
+template <typename T, int DP, int NS, bool DV, bool DK>
+struct Keys {
   using TL = Tile<T, DP>;
-  u32x4_t k[TL::KB], v[DK ? TL::KB : 1];
-  f32x16_t dk[DK ? DP / 32 : 1], dv[DV ? DP / 32 : 1];
+  // 16-bit rows of 128 values leave registers for fewer
+  static constexpr bool kTight = sizeof(T) == 2 && DP == 128;
+  static constexpr int kAheadRows = kTight ? 4 : 8, kAheadCols = kTight ? 2 : 4;
+  u32x4_t k[NS][TL::KB], v[NS][DK ? TL::KB : 1];
+  f32x16_t dk[NS][DK ? DP / 32 : 1], dv[NS][DV ? DP / 32 : 1];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int dt = 0; dt < (DK ? DP / 32 : 1); ++dt) dk[dt] = zero16();
+    for (int n = 0; n < NS; ++n) {
 #pragma unroll
-    for (int dt = 0; dt < (DV ? DP / 32 : 1); ++dt) dv[dt] = zero16();
+      for (int dt = 0; dt < (DK ? DP / 32 : 1); ++dt) dk[n][dt] = zero16();
+#pragma unroll
+      for (int dt = 0; dt < (DV ? DP / 32 : 1); ++dt) dv[n][dt] = zero16();
+    }
   }
-  __device__ __forceinline__ void load(const AttendArgs& a, int b, int hk, int key, bool ok, int lane) {
-    load_row_frags<T, DP>((const T*)a.k + key * a.ks.t + b * a.ks.b + hk * a.ks.h, a.D, a.whole & kWholeK, ok, lane, k);
+  __device__ __forceinline__ void load(const AttendArgs& a, int b, int hk, int n, int key, bool ok, int lane) {
+    load_row_frags<T, DP>((const T*)a.k + key * a.ks.t + b * a.ks.b + hk * a.ks.h, a.D, a.whole & kWholeK, ok, lane,
+                          k[n]);
     if constexpr (DK)
       load_row_frags<T, DP>((const T*)a.v + key * a.vs.t + b * a.vs.b + hk * a.vs.h, a.D, a.whole & kWholeV, ok, lane,
-                            v);
+                            v[n]);
   }
-  // adds the terms of 32 query rows: their q and dout tiles, lse2[32] and
-  // delta[32] behind it
+  // adds the terms of 32 query rows: their q and dout tiles and (lse2, delta)
+  // pairs.  Rows past the last have zeros in all of them and add nothing.
   __device__ __forceinline__ void tile(const char* qt, const char* gt, const float* stat, float c2, int lane) {
-    f32x16_t s = zero16(), dp = zero16();
+    f32x16_t s[NS], dp[NS];
 #pragma unroll
-    for (int kb = 0; kb < TL::KB; ++kb) s = Mm<T>::mac(TL::row_frag(qt, 0, kb, lane), k[kb], s);
-    if constexpr (DK) {
+    for (int n = 0; n < NS; ++n) s[n] = dp[n] = zero16();
+    constexpr int NDT = DP / 32, NG = (DV ? 1 : 0) + (DK ? 1 : 0);
+    Ahead<(DK ? 2 : 1) * TL::KB, kAheadRows> rows;  // q, then dout
+    Ahead<TL::PB * NDT * NG, kAheadCols> cols;      // k-block, d-tile, dout then q
+    auto read_row = [&](int f) { return TL::row_frag(f < TL::KB ? qt : gt, 0, f % TL::KB, lane); };
+    auto read_col = [&](int f) {
+      return TL::col_frag(DV && f % NG == 0 ? gt : qt, TL::KR * (f / NG / NDT), f / NG % NDT, lane);
+    };
+    rows.start(read_row);
+    rows.run(read_row, [&](int f, u32x4_t x) {
 #pragma unroll
-      for (int kb = 0; kb < TL::KB; ++kb) dp = Mm<T>::mac(TL::row_frag(gt, 0, kb, lane), v[kb], dp);
-    }
+      for (int n = 0; n < NS; ++n) {
+        if (f < TL::KB) s[n] = Mm<T>::mac(x, k[n][f % TL::KB], s[n]);
+        else dp[n] = Mm<T>::mac(x, v[n][DK ? f % TL::KB : 0], dp[n]);
+      }
+    });
+    cols.start(read_col);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const f32x4_t L = *(const f32x4_t*)(stat + reg_row(4 * j, lane));
+      const float* at = stat + 2 * reg_row(4 * j, lane);
+      const f32x4_t x = *(const f32x4_t*)at, y = *(const f32x4_t*)(at + 4);
+      const float L[4] = {x[0], x[2], y[0], y[2]}, d[4] = {x[1], x[3], y[1], y[3]};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * j + e] = exp_carried<T>(__builtin_fmaf(s[4 * j + e], c2, -L[e]));
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][4 * j + e] = exp_carried<T>(__builtin_fmaf(s[n][4 * j + e], c2, -L[e]));
+          if constexpr (DK) dp[n][4 * j + e] = s[n][4 * j + e] * (dp[n][4 * j + e] - d[e]);
+        }
     }
-    if constexpr (DV) {
+    u32x4_t p[NS][TL::PB], ds[NS][TL::PB];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int pb = 0; pb < TL::PB; ++pb) {
-        const u32x4_t p = TL::reg_frag(s, pb);
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) dv[dt] = Mm<T>::mac(TL::col_frag(gt, TL::KR * pb, dt, lane), p, dv[dt]);
+        if constexpr (DV) p[n][pb] = TL::reg_frag(s[n], pb);
+        if constexpr (DK) ds[n][pb] = TL::reg_frag(dp[n], pb);
       }
-    }
-    if constexpr (DK) {
+    cols.run(read_col, [&](int f, u32x4_t x) {
+      const int pb = f / NG / NDT, dt = f / NG % NDT;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4_t d = *(const f32x4_t*)(stat + 32 + reg_row(4 * j, lane));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[4 * j + e] *= dp[4 * j + e] - d[e];
+      for (int n = 0; n < NS; ++n) {
+        if (DV && f % NG == 0) dv[n][DV ? dt : 0] = Mm<T>::mac(x, p[n][pb], dv[n][DV ? dt : 0]);
+        else dk[n][DK ? dt : 0] = Mm<T>::mac(x, ds[n][pb], dk[n][DK ? dt : 0]);
       }
-#pragma unroll
-      for (int pb = 0; pb < TL::PB; ++pb) {
-        const u32x4_t ds = TL::reg_frag(s, pb);
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = Mm<T>::mac(TL::col_frag(qt, TL::KR * pb, dt, lane), ds, dk[dt]);
-      }
-    }
+    });
   }
 };
 
 // Tiles of 32 query rows of the heads that share a key head: tile i is rows
-// [32 (i % nt), +32) of head i / nt.
+// [32 (i % nt), +32) of head i / nt.  A stage in LDS: the q tile, the dout
+// tile, and for each wave its own copy of the rows' (lse2, delta) pairs.
 template <typename T, int DP, int NW, bool DMA>
 struct QueryTiles {
   using TL = Tile<T, DP>;
-  Loader<T, DP, 32, NW, DMA> lq, lg;
-  const T *q0, *g0;
-  int64_t row0;  // of lse and delta
-  int nt, n;
-  float l, d;    // of this lane's row (lanes 0 .. 31)
-  __device__ __forceinline__ void init(const AttendArgs& a, int b, int hk, int w, int lane) {
-    q0 = (const T*)a.q + b * a.qs.b + (int64_t)hk * a.G * a.qs.h;
-    g0 = (const T*)a.dout + b * a.gs.b + (int64_t)hk * a.G * a.gs.h;
-    lq.init(q0, a.qs.t, a.D, a.whole & kWholeQ, nullptr, w, lane);
-    lg.init(g0, a.gs.t, a.D, a.whole & kWholeG, nullptr, w, lane);
-    row0 = ((int64_t)b * a.Hq + (int64_t)hk * a.G) * a.Tq;
-    nt = (a.Tq + 31) / 32;
+  using Load = Loader<T, DP, 32, NW, DMA>;
+  static constexpr int kStage = 2 * TL::kBytes32 + NW * 256;
+  // every wave has as many loads, and two stages' can be told apart
+  static constexpr bool kCounted = DMA && Load::kTotal % NW == 0 && 2 * (2 * Load::kLoads + 1) <= 63;
+  static constexpr int kLoads = 2 * Load::kLoads + 1;              // of a stage and wave
+  Load lq, lg;
+  const float* st0;  // of this head's rows
+  int nt, n, Tq, w, lane;
+  int64_t qh, gh;
+  int t0;  // first row of the tile that fetch() loads
+  __device__ __forceinline__ void init(const AttendArgs& a, int b, int hk, int w_, int lane_) {
+    w = w_; lane = lane_;
+    Tq = a.Tq; qh = a.qs.h; gh = a.gs.h;
+    lq.init((const T*)a.q + b * a.qs.b + (int64_t)hk * a.G * qh, a.qs.t, a.D, a.whole & kWholeQ, nullptr, w, lane);
+    lg.init((const T*)a.dout + b * a.gs.b + (int64_t)hk * a.G * gh, a.gs.t, a.D, a.whole & kWholeG, nullptr, w, lane);
+    st0 = a.stats + 2 * ((int64_t)b * a.Hq + (int64_t)hk * a.G) * Tq;
+    nt = (Tq + 31) / 32;
     n = nt * a.G;
+    t0 = 0;
   }
-  __device__ __forceinline__ void fetch(const AttendArgs& a, int i, char* lds, bool stats, int lane) {
-    const int hd = i / nt, t0 = (i - hd * nt) * 32;
-    lq.p = q0 + hd * a.qs.h;
-    lg.p = g0 + hd * a.gs.h;
-    lq.load(t0, a.Tq, lds);
-    lg.load(t0, a.Tq, lds + TL::kBytes32);
-    l = INFINITY;  // rows past the last, and rows without keys: p = 0
-    d = 0.f;
-    const int t = t0 + lane;
-    if (stats && lane < 32 && t < a.Tq) {
-      const int64_t li = row0 + (int64_t)hd * a.Tq + t;
-      const float x = a.lse[li];
-      if (x != -INFINITY) l = x * kLog2e - kInExponent<T>;
-      d = a.delta[li];
+  // on by `by` tiles
+  __device__ __forceinline__ void skip(int by) {
+    t0 += 32 * by;
+    while (t0 >= 32 * nt && nt > 0) {
+      t0 -= 32 * nt;
+      lq.p += qh;
+      lg.p += gh;
+      st0 += 2 * (int64_t)Tq;
     }
   }
-  __device__ __forceinline__ void keep(float* stat, bool stats, int lane) const {
-    if (stats && lane < 32) {
-      stat[lane] = l;
-      stat[32 + lane] = d;
+  __device__ __forceinline__ static const float* stat(const char* stage, int w) {
+    return (const float*)(stage + 2 * TL::kBytes32 + w * 256);
+  }
+  __device__ __forceinline__ void fetch(char* stage) {
+    lq.load(t0, Tq, stage);
+    lg.load(t0, Tq, stage + TL::kBytes32);
+    const float* s = st0 + 2 * (int64_t)t0;
+    const int rows = Tq - t0 < 32 ? Tq - t0 : 32;
+    char* to = stage + 2 * TL::kBytes32 + w * 256;
+    if constexpr (DMA) {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)s, 0, rows * 8, 0x00020000);
+      lds_dma4(r, to, lane * 4);
+    } else {
+      ((float*)to)[lane] = lane < 2 * rows ? s[lane] : 0.f;
     }
   }
 };
 
-// 128 keys per work-group, 32 per wave, which share the tiles of query rows.
+// 128 NS keys per work-group, 32 NS per wave, which share the tiles of query
+// rows, in a ring of stages (one barrier a tile: the stage that is loaded next
+// was read before it).  NS = 2 reads every fragment from LDS once for two
+// products; it takes one wave's whole registers.
+template <typename T, int DP, bool DMA> constexpr int dkv_ring() {
+  constexpr int stage = QueryTiles<T, DP, 4, DMA>::kStage;
+  return 4 * stage <= 96 * 1024 ? 4 : 3 * stage <= 150 * 1024 ? 3 : 2;
+}
+template <typename T, int DP> constexpr int dkv_subtiles() { return 1; }
+
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_kernel(AttendArgs a) {
-  constexpr int TB = Tile<T, DP>::kBytes32;
-  extern __shared__ __attribute__((aligned(16))) char lds[];  // q, dout tiles, twice
-  __shared__ __attribute__((aligned(16))) float stat[2][64];
+  constexpr int TB = Tile<T, DP>::kBytes32, NS = dkv_subtiles<T, DP>(), R = dkv_ring<T, DP, DMA>();
+  using Tiles = QueryTiles<T, DP, 4, DMA>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int grp, tile;
   if (!group_of(a, blockIdx.x, &grp, &tile)) return;
   const int b = grp / a.Hk, hk = grp - b * a.Hk;
   const int end = keys_of(a, b);
-  const int key = tile * 128 + w * 32 + (lane & 31);
-  const bool ok = key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0);
-  Key<T, DP, DV, DK> me;
+  const int key0 = (tile * 4 + w) * 32 * NS + (lane & 31);
+  Keys<T, DP, NS, DV, DK> me;
   me.clear();
-  if (tile * 128 < end) {
-    me.load(a, b, hk, key, ok, lane);
+  if (tile * 128 * NS < end) {
     const float c2 = a.scale * kLog2e;
-    QueryTiles<T, DP, 4, DMA> qt;
+    Tiles qt;
     qt.init(a, b, hk, w, lane);
-    if (qt.n > 0) {
-      qt.fetch(a, 0, lds, w == 0, lane);
-      qt.keep(stat[0], w == 0, lane);
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const int key = key0 + 32 * n;
+      me.load(a, b, hk, n, key, key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0), lane);
     }
+    wait_vmem();  // from here on the ring's loads alone are counted
+#pragma unroll
+    for (int i = 0; i < R - 1; ++i)
+      if (i < qt.n) {
+        qt.fetch(lds + i * Tiles::kStage);
+        qt.skip(1);
+      }
+    int at = 0;  // stage of tile i
     for (int i = 0; i < qt.n; ++i) {
-      wait_vmem();
+      // tile i has arrived; up to R - 2 younger ones may be on their way
+      const int young = qt.n - 1 - i;
+      if (Tiles::kCounted && R == 4 && young >= 2) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Tiles::kCounted ? 2 * Tiles::kLoads : 0));
+      else if (Tiles::kCounted && R >= 3 && young >= 1) __builtin_amdgcn_s_waitcnt(vmcnt_imm(Tiles::kCounted ? Tiles::kLoads : 0));
+      else wait_vmem();
       __syncthreads();
-      const int buf = i & 1;
-      const char* cur = lds + buf * 2 * TB;
-      if (i + 1 < qt.n) qt.fetch(a, i + 1, lds + (buf ^ 1) * 2 * TB, w == 0, lane);
-      me.tile(cur, cur + TB, stat[buf], c2, lane);
-      if (i + 1 < qt.n) qt.keep(stat[buf ^ 1], w == 0, lane);
+      char* cur = lds + at * Tiles::kStage;
+      if (i + R - 1 < qt.n) {
+        qt.fetch(lds + ((at + R - 1) % R) * Tiles::kStage);
+        qt.skip(1);
+      }
+      me.tile(cur, cur + TB, Tiles::stat(cur, w), c2, lane);
+      at = (at + 1) % R;
     }
   }
-  if (key >= a.Tk) return;
-  if (!ok) me.clear();  // keys of no query: zeros, whatever the products of their zeroed rows were
-  if constexpr (DK)
-    store_col<T, DP>((T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h, me.dk, a.scale / kCarry<T>, a.D,
-                     a.whole & kWholeDk, lane);
-  if constexpr (DV)
-    store_col<T, DP>((T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h, me.dv, 1.f / kCarry<T>, a.D,
-                     a.whole & kWholeDv, lane);
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    const int key = key0 + 32 * n;
+    if (key >= a.Tk) continue;
+    // keys of no query: zeros, whatever the products of their zeroed rows were
+    const bool ok = key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0);
+    if constexpr (DK)
+      store_col<T, DP>((T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h, me.dk[n], a.scale / kCarry<T>, a.D,
+                       a.whole & kWholeDk, lane, ok);
+    if constexpr (DV)
+      store_col<T, DP>((T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h, me.dv[n], 1.f / kCarry<T>, a.D,
+                       a.whole & kWholeDv, lane, ok);
+  }
 }
 
 // Few keys: 32 per work-group, the tiles of query rows dealt to its waves.
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_kernel(AttendArgs a) {
   constexpr int NW = step_waves<T, DP>(), TB = Tile<T, DP>::kBytes32;
-  extern __shared__ __attribute__((aligned(16))) char lds[];  // per wave: q, dout tile
-  __shared__ __attribute__((aligned(16))) float stat[NW][64];
+  using Tiles = QueryTiles<T, DP, 1, DMA>;
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // per wave: a stage
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int grp, tile;
   if (!group_of(a, blockIdx.x, &grp, &tile)) return;
@@ -356,37 +419,38 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
   const int end = keys_of(a, b);
   const int key = tile * 32 + (lane & 31);
   const bool ok = key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0);
-  char* mine = lds + w * 2 * TB;
-  Key<T, DP, DV, DK> me;
+  char* mine = lds + w * Tiles::kStage;
+  Keys<T, DP, 1, DV, DK> me;
   me.clear();
   if (tile * 32 < end) {
     const float c2 = a.scale * kLog2e;
-    QueryTiles<T, DP, 1, DMA> qt;
+    Tiles qt;
     qt.init(a, b, hk, 0, lane);
-    if (w < qt.n) qt.fetch(a, w, mine, true, lane);
-    me.load(a, b, hk, key, ok, lane);
+    qt.skip(w);
+    if (w < qt.n) qt.fetch(mine);
+    me.load(a, b, hk, 0, key, ok, lane);
     for (int i = w; i < qt.n; i += NW) {
-      qt.keep(stat[w], true, lane);
       wait_vmem();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      me.tile(mine, mine + TB, stat[w], c2, lane);
+      me.tile(mine, mine + TB, Tiles::stat(mine, 0), c2, lane);
       if (i + NW < qt.n) {
         __builtin_amdgcn_s_waitcnt(kLgkm0);  // every fragment of this tile is read
-        qt.fetch(a, i + NW, mine, true, lane);
+        qt.skip(NW);
+        qt.fetch(mine);
       }
     }
   }
   const bool store = key < a.Tk;
   if constexpr (DK) {
     T* out = (T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h;
-    join_waves<T, DP>(me.dk, lds, a.D, w, lane, [&](int d, float v) {
+    join_waves<T, DP>(me.dk[0], lds, a.D, w, lane, [&](int d, float v) {
       if (store) out[d] = Elem<T>::from_f(ok ? as_f32(v * (a.scale / kCarry<T>)) : 0.f);
     });
   }
   if constexpr (DV) {
     T* out = (T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h;
-    join_waves<T, DP>(me.dv, lds, a.D, w, lane, [&](int d, float v) {
+    join_waves<T, DP>(me.dv[0], lds, a.D, w, lane, [&](int d, float v) {
       if (store) out[d] = Elem<T>::from_f(ok ? as_f32(v / kCarry<T>) : 0.f);
     });
   }
@@ -396,8 +460,10 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 static hipError_t attend_dkv_t(const AttendPlan& p, AttendArgs a, hipStream_t s) {
   const bool few = p.few_keys;
-  const size_t lds = (few ? 2 * step_waves<T, DP>() : 4) * (size_t)Tile<T, DP>::kBytes32;
-  a.tiles = few ? (a.Tk + 31) / 32 : (a.Tk + 127) / 128;
+  const size_t lds = few ? step_waves<T, DP>() * (size_t)QueryTiles<T, DP, 1, DMA>::kStage
+                         : dkv_ring<T, DP, DMA>() * (size_t)QueryTiles<T, DP, 4, DMA>::kStage;
+  const int keys = few ? 32 : 128 * dkv_subtiles<T, DP>();
+  a.tiles = (a.Tk + keys - 1) / keys;
   const unsigned grid = attend_grid(&a);
   const hipError_t e = few ? allow_lds<attend_dkv_few_kernel<T, DP, DMA, DV, DK>>(lds)
                            : allow_lds<attend_dkv_kernel<T, DP, DMA, DV, DK>>(lds);

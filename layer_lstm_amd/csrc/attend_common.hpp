@@ -113,6 +113,31 @@ struct Tile {
   }
 };
 
+// F fragments read from LDS LA ahead of their products: start() issues the
+// first LA reads, run() multiplies fragment f and issues the read of f + LA in
+// its place.  The order is pinned (left alone, the compiler reads each
+// fragment right before its product and waits for it).
+template <int F, int LA_>
+struct Ahead {
+  static constexpr int LA = LA_ < F ? LA_ : F;
+  u32x4_t buf[LA];
+  template <class Read>
+  __device__ __forceinline__ void start(Read read) {
+#pragma unroll
+    for (int f = 0; f < LA; ++f) buf[f] = read(f);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <class Read, class Use>
+  __device__ __forceinline__ void run(Read read, Use use) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      use(f, buf[f % LA]);
+      if (f + LA < F) buf[f % LA] = read(f + LA);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
 __device__ __forceinline__ f32x16_t zero16() {
   f32x16_t z;
 #pragma unroll
@@ -126,6 +151,19 @@ __device__ __forceinline__ int reg_row(int i, int lane) { return 8 * (i >> 2) + 
 __device__ __forceinline__ float other_half(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// 4 bytes per lane from a buffer straight into LDS, to lds + 4 * lane (see
+// lds_dma16).
+__device__ __forceinline__ void lds_dma4(__amdgpu_buffer_rsrc_t r, void* lds, uint32_t voff) {
+  const uint32_t m0v = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t*)lds);
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %0, %2, 0 offen lds"
+               :
+               : "v"(voff), "s"(m0v), "s"(r)
+               : "memory", "m0");
+#pragma clang diagnostic pop
 }
 
 // 16 bytes of a row of D values from d: element by element where rows are
@@ -149,7 +187,7 @@ struct AttendArgs {
   void *out, *dq, *dk, *dv;
   lstm_stride qs, ks, vs, os, gs, dqs, dks, dvs;  // gs: of dout
   float* lse;            // [B][Hq][Tq] (the backward reads it)
-  float* delta;          // [B][Hq][Tq] sum_d dout o
+  float* stats;          // [B][Hq][Tq][2] backward: lse in powers of two (+inf: no key), sum_d dout o
   const int32_t* len;    // [B] or null
   const uint8_t* mask;   // [B][Tk] or null
   int64_t mask_b;
@@ -324,9 +362,10 @@ __device__ __forceinline__ void load_row_frags(const T* row, int D, bool whole, 
 }
 
 // A row's column of products (register i of d-tile dt: d = 32 dt +
-// reg_row(i)) times `by` to global memory.
+// reg_row(i)) times `by`, or zeros, to global memory.
 template <typename T, int DP>
-__device__ __forceinline__ void store_col(T* row, const f32x16_t* acc, float by, int D, bool whole, int lane) {
+__device__ __forceinline__ void store_col(T* row, const f32x16_t* acc, float by, int D, bool whole, int lane,
+                                          bool ok = true) {
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
@@ -334,7 +373,7 @@ __device__ __forceinline__ void store_col(T* row, const f32x16_t* acc, float by,
       const int d = 32 * dt + reg_row(4 * i, lane);
       float f[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = as_f32(acc[dt][4 * i + j] * by);
+      for (int j = 0; j < 4; ++j) f[j] = ok ? as_f32(acc[dt][4 * i + j] * by) : 0.f;
       if (whole) {
         if (d < D) {
           if constexpr (sizeof(T) == 4) {

@@ -252,7 +252,7 @@ int lstm_attend_bwd(const lstm_attend_shape* shape, const void* dout, const void
   if (workspace_bytes < p.total_bwd) return LSTM_ERR_WORKSPACE;
   a.q = q; a.k = k; a.v = v; a.o = o; a.dout = dout; a.dq = dq; a.dk = dk; a.dv = dv;
   a.lse = const_cast<float*>(lse);
-  a.delta = (float*)workspace;
+  a.stats = (float*)workspace;
   a.len = (const int32_t*)k_length;
   a.mask = (const uint8_t*)key_mask;
   const int64_t D = shape->D;

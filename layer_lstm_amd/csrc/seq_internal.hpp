@@ -109,7 +109,7 @@ struct AttendPlan {
   int splits;       //   the keys of a row tile split over this many work-groups
   int few_rows, few_keys;  // backward: dq, dk and dv by the kernels that split the sums over waves
   int row_tiles32;  // tiles of 32 rows per (sequence, key head)
-  size_t off_part, off_ml, off_delta, total_fwd, total_bwd;
+  size_t off_part, off_ml, total_fwd, total_bwd;
 };
 void make_attend_plan(const lstm_attend_shape& s, int cus, AttendPlan* p);
 hipError_t launch_attend_fwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s);
