@@ -36,6 +36,38 @@ __device__ __forceinline__ float exp_carried(float y) {
   }
 }
 
+// Long sums in fp32 storage: after every kFoldTiles tiles the products' sums
+// are added to a second set of registers and start again, so that a sum of n
+// terms carries the rounding of about n / 16 + 16 tiles' additions and not of
+// n (dq over 4096 keys: 1.1e-6 of its norm without).  In 16 bits the operands'
+// rounding is far above it, and past 128 values a row there are no registers.
+constexpr int kFoldTiles = 16;
+template <typename T, int DP> constexpr bool kFold = std::is_same<T, float>::value && DP <= 128;
+template <typename T, int DP>
+struct Sums {
+  static constexpr int N = kFold<T, DP> ? DP / 32 : 1;
+  f32x16_t total[N];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) total[i] = zero16();
+  }
+  __device__ __forceinline__ void fold(f32x16_t* acc) {
+    if constexpr (kFold<T, DP>) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        total[i] += acc[i];
+        acc[i] = zero16();
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(f32x16_t* acc) const {
+    if constexpr (kFold<T, DP>) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] += total[i];
+    }
+  }
+};
+
 // What a query row (column lane % 32 of the products) keeps in registers.
 template <typename T, int DP>
 struct QueryRow {
@@ -127,6 +159,8 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
   f32x16_t dq[DP / 32];
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = zero16();
+  Sums<T, DP> sums;
+  sums.clear();
   const float c2 = a.scale * kLog2e;
   const int n = (end + NK - 1) / NK;
   if (n > 0) {
@@ -148,7 +182,9 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
 #pragma unroll
     for (int kt = 0; kt < NK / 32; ++kt)
       row.tile(cur + kt * TL::kBytes32, cur + TB + kt * TL::kBytes32, (uint32_t)(now >> (32 * kt)), dq, c2, lane);
+    if (i % kFoldTiles == kFoldTiles - 1) sums.fold(dq);
   }
+  sums.finish(dq);
   if (row.ok)
     store_col<T, DP>((T*)a.dq + row.t * a.dqs.t + b * a.dqs.b + row.h * a.dqs.h, dq, a.scale / kCarry<T>, a.D,
                      a.whole & kWholeDq, lane);
@@ -211,7 +247,27 @@ struct Keys {
   static constexpr int kAheadRows = kTight ? 4 : 8, kAheadCols = kTight ? 2 : 4;
   u32x4_t k[NS][TL::KB], v[NS][DK ? TL::KB : 1];
   f32x16_t dk[NS][DK ? DP / 32 : 1], dv[NS][DV ? DP / 32 : 1];
+  Sums<T, DP> sk[NS], sv[NS];
+  __device__ __forceinline__ void fold() {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      if constexpr (DK) sk[n].fold(dk[n]);
+      if constexpr (DV) sv[n].fold(dv[n]);
+    }
+  }
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      if constexpr (DK) sk[n].finish(dk[n]);
+      if constexpr (DV) sv[n].finish(dv[n]);
+    }
+  }
   __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      sk[n].clear();
+      sv[n].clear();
+    }
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
 #pragma unroll
@@ -388,8 +444,10 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
         qt.skip(1);
       }
       me.tile(cur, cur + TB, Tiles::stat(cur, w), c2, lane);
+      if (i % kFoldTiles == kFoldTiles - 1) me.fold();
       at = (at + 1) % R;
     }
+    me.finish();
   }
 #pragma unroll
   for (int n = 0; n < NS; ++n) {
