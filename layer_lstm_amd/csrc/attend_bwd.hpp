@@ -242,9 +242,10 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dq_few_k
 template <typename T, int DP, int NS, bool DV, bool DK>
 struct Keys {
   using TL = Tile<T, DP>;
-  // 16-bit rows of 128 values leave registers for fewer
+  // fragments read ahead: 16-bit rows of 128 values (two waves a SIMD, 256
+  // registers) leave 16 registers for them beside s, 8 beside s and dp
   static constexpr bool kTight = sizeof(T) == 2 && DP == 128;
-  static constexpr int kAheadRows = kTight ? 4 : 8, kAheadCols = kTight ? 2 : 4;
+  static constexpr int kAheadRows = kTight ? 4 : 8, kAheadGrads = kTight ? 2 : 8, kAheadCols = 4;
   u32x4_t k[NS][TL::KB], v[NS][DK ? TL::KB : 1];
   f32x16_t dk[NS][DK ? DP / 32 : 1], dv[NS][DV ? DP / 32 : 1];
   Sums<T, DP> sk[NS], sv[NS];
@@ -290,21 +291,27 @@ struct Keys {
 #pragma unroll
     for (int n = 0; n < NS; ++n) s[n] = dp[n] = zero16();
     constexpr int NDT = DP / 32, NG = (DV ? 1 : 0) + (DK ? 1 : 0);
-    Ahead<(DK ? 2 : 1) * TL::KB, kAheadRows> rows;  // q, then dout
+    Ahead<TL::KB, kAheadRows> rq;
+    Ahead<TL::KB, kAheadGrads> rg;
     Ahead<TL::PB * NDT * NG, kAheadCols> cols;      // k-block, d-tile, dout then q
-    auto read_row = [&](int f) { return TL::row_frag(f < TL::KB ? qt : gt, 0, f % TL::KB, lane); };
+    auto read_q = [&](int f) { return TL::row_frag(qt, 0, f, lane); };
+    auto read_g = [&](int f) { return TL::row_frag(gt, 0, f, lane); };
     auto read_col = [&](int f) {
       return TL::col_frag(DV && f % NG == 0 ? gt : qt, TL::KR * (f / NG / NDT), f / NG % NDT, lane);
     };
-    rows.start(read_row);
-    rows.run(read_row, [&](int f, u32x4_t x) {
+    rq.start(read_q);
+    rq.run(read_q, [&](int f, u32x4_t x) {
 #pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        if (f < TL::KB) s[n] = Mm<T>::mac(x, k[n][f % TL::KB], s[n]);
-        else dp[n] = Mm<T>::mac(x, v[n][DK ? f % TL::KB : 0], dp[n]);
-      }
+      for (int n = 0; n < NS; ++n) s[n] = Mm<T>::mac(x, k[n][f], s[n]);
     });
-    cols.start(read_col);
+    if constexpr (DK) {
+      rg.start(read_g);
+      rg.run(read_g, [&](int f, u32x4_t x) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n) dp[n] = Mm<T>::mac(x, v[n][f], dp[n]);
+      });
+    }
+    if constexpr (!kTight) cols.start(read_col);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float* at = stat + 2 * reg_row(4 * j, lane);
@@ -317,6 +324,7 @@ struct Keys {
           s[n][4 * j + e] = exp_carried<T>(__builtin_fmaf(s[n][4 * j + e], c2, -L[e]));
           if constexpr (DK) dp[n][4 * j + e] = s[n][4 * j + e] * (dp[n][4 * j + e] - d[e]);
         }
+      if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);  // or all the pairs would be read at once
     }
     u32x4_t p[NS][TL::PB], ds[NS][TL::PB];
 #pragma unroll
@@ -326,6 +334,10 @@ struct Keys {
         if constexpr (DV) p[n][pb] = TL::reg_frag(s[n], pb);
         if constexpr (DK) ds[n][pb] = TL::reg_frag(dp[n], pb);
       }
+    if constexpr (kTight) {  // in the registers that s and dp leave
+      __builtin_amdgcn_sched_barrier(0);
+      cols.start(read_col);
+    }
     cols.run(read_col, [&](int f, u32x4_t x) {
       const int pb = f / NG / NDT, dt = f / NG % NDT;
 #pragma unroll
@@ -337,17 +349,18 @@ struct Keys {
   }
 };
 
-// Tiles of 32 query rows of the heads that share a key head: tile i is rows
-// [32 (i % nt), +32) of head i / nt.  A stage in LDS: the q tile, the dout
+// Tiles of NR query rows of the heads that share a key head: tile i is rows
+// [NR (i % nt), +NR) of head i / nt.  A stage in LDS: the q tile, the dout
 // tile, and for each wave its own copy of the rows' (lse2, delta) pairs.
-template <typename T, int DP, int NW, bool DMA>
+template <typename T, int DP, int NR, int NW, bool DMA>
 struct QueryTiles {
   using TL = Tile<T, DP>;
-  using Load = Loader<T, DP, 32, NW, DMA>;
-  static constexpr int kStage = 2 * TL::kBytes32 + NW * 256;
+  using Load = Loader<T, DP, NR, NW, DMA>;
+  static constexpr int kTile = NR / 32 * TL::kBytes32, kStat = NR * 8, kStage = 2 * kTile + NW * kStat;
+  static constexpr int kStatLoads = NR / 32;
   // every wave has as many loads, and two stages' can be told apart
-  static constexpr bool kCounted = DMA && Load::kTotal % NW == 0 && 2 * (2 * Load::kLoads + 1) <= 63;
-  static constexpr int kLoads = 2 * Load::kLoads + 1;              // of a stage and wave
+  static constexpr bool kCounted = DMA && Load::kTotal % NW == 0 && 2 * (2 * Load::kLoads + kStatLoads) <= 63;
+  static constexpr int kLoads = 2 * Load::kLoads + kStatLoads;     // of a stage and wave
   Load lq, lg;
   const float* st0;  // of this head's rows
   int nt, n, Tq, w, lane;
@@ -359,34 +372,35 @@ struct QueryTiles {
     lq.init((const T*)a.q + b * a.qs.b + (int64_t)hk * a.G * qh, a.qs.t, a.D, a.whole & kWholeQ, nullptr, w, lane);
     lg.init((const T*)a.dout + b * a.gs.b + (int64_t)hk * a.G * gh, a.gs.t, a.D, a.whole & kWholeG, nullptr, w, lane);
     st0 = a.stats + 2 * ((int64_t)b * a.Hq + (int64_t)hk * a.G) * Tq;
-    nt = (Tq + 31) / 32;
+    nt = (Tq + NR - 1) / NR;
     n = nt * a.G;
     t0 = 0;
   }
   // on by `by` tiles
   __device__ __forceinline__ void skip(int by) {
-    t0 += 32 * by;
-    while (t0 >= 32 * nt && nt > 0) {
-      t0 -= 32 * nt;
+    t0 += NR * by;
+    while (t0 >= NR * nt && nt > 0) {
+      t0 -= NR * nt;
       lq.p += qh;
       lg.p += gh;
       st0 += 2 * (int64_t)Tq;
     }
   }
   __device__ __forceinline__ static const float* stat(const char* stage, int w) {
-    return (const float*)(stage + 2 * TL::kBytes32 + w * 256);
+    return (const float*)(stage + 2 * kTile + w * kStat);
   }
   __device__ __forceinline__ void fetch(char* stage) {
     lq.load(t0, Tq, stage);
-    lg.load(t0, Tq, stage + TL::kBytes32);
+    lg.load(t0, Tq, stage + kTile);
     const float* s = st0 + 2 * (int64_t)t0;
-    const int rows = Tq - t0 < 32 ? Tq - t0 : 32;
-    char* to = stage + 2 * TL::kBytes32 + w * 256;
+    const int rows = Tq - t0 < NR ? Tq - t0 : NR;
+    char* to = stage + 2 * kTile + w * kStat;
     if constexpr (DMA) {
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)s, 0, rows * 8, 0x00020000);
-      lds_dma4(r, to, lane * 4);
+#pragma unroll
+      for (int i = 0; i < kStatLoads; ++i) lds_dma4(r, to + 256 * i, 256 * i + lane * 4);
     } else {
-      ((float*)to)[lane] = lane < 2 * rows ? s[lane] : 0.f;
+      for (int i = lane; i < 2 * NR; i += 64) ((float*)to)[i] = i < 2 * rows ? s[i] : 0.f;
     }
   }
 };
@@ -395,16 +409,17 @@ struct QueryTiles {
 // rows, in a ring of stages (one barrier a tile: the stage that is loaded next
 // was read before it).  NS = 2 reads every fragment from LDS once for two
 // products; it takes one wave's whole registers.
+template <typename T, int DP> constexpr int dkv_rows() { return DP * sizeof(T) <= 128 ? 64 : 32; }
 template <typename T, int DP, bool DMA> constexpr int dkv_ring() {
-  constexpr int stage = QueryTiles<T, DP, 4, DMA>::kStage;
-  return 4 * stage <= 96 * 1024 ? 4 : 3 * stage <= 150 * 1024 ? 3 : 2;
+  constexpr int stage = QueryTiles<T, DP, dkv_rows<T, DP>(), 4, DMA>::kStage;
+  return dkv_rows<T, DP>() == 64 ? 2 : 4 * stage <= 96 * 1024 ? 4 : 3 * stage <= 150 * 1024 ? 3 : 2;
 }
 template <typename T, int DP> constexpr int dkv_subtiles() { return 1; }
 
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_kernel(AttendArgs a) {
   constexpr int TB = Tile<T, DP>::kBytes32, NS = dkv_subtiles<T, DP>(), R = dkv_ring<T, DP, DMA>();
-  using Tiles = QueryTiles<T, DP, 4, DMA>;
+  using Tiles = QueryTiles<T, DP, dkv_rows<T, DP>(), 4, DMA>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int grp, tile;
@@ -443,7 +458,9 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
         qt.fetch(lds + ((at + R - 1) % R) * Tiles::kStage);
         qt.skip(1);
       }
-      me.tile(cur, cur + TB, Tiles::stat(cur, w), c2, lane);
+#pragma unroll
+      for (int h = 0; h < Tiles::kStatLoads; ++h)
+        me.tile(cur + h * TB, cur + Tiles::kTile + h * TB, Tiles::stat(cur, w) + 64 * h, c2, lane);
       if (i % kFoldTiles == kFoldTiles - 1) me.fold();
       at = (at + 1) % R;
     }
@@ -468,7 +485,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_kernel(AttendArgs a) {
   constexpr int NW = step_waves<T, DP>(), TB = Tile<T, DP>::kBytes32;
-  using Tiles = QueryTiles<T, DP, 1, DMA>;
+  using Tiles = QueryTiles<T, DP, 32, 1, DMA>;
   extern __shared__ __attribute__((aligned(16))) char lds[];  // per wave: a stage
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int grp, tile;
@@ -518,8 +535,8 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 static hipError_t attend_dkv_t(const AttendPlan& p, AttendArgs a, hipStream_t s) {
   const bool few = p.few_keys;
-  const size_t lds = few ? step_waves<T, DP>() * (size_t)QueryTiles<T, DP, 1, DMA>::kStage
-                         : dkv_ring<T, DP, DMA>() * (size_t)QueryTiles<T, DP, 4, DMA>::kStage;
+  const size_t lds = few ? step_waves<T, DP>() * (size_t)QueryTiles<T, DP, 32, 1, DMA>::kStage
+                         : dkv_ring<T, DP, DMA>() * (size_t)QueryTiles<T, DP, dkv_rows<T, DP>(), 4, DMA>::kStage;
   const int keys = few ? 32 : 128 * dkv_subtiles<T, DP>();
   a.tiles = (a.Tk + keys - 1) / keys;
   const unsigned grid = attend_grid(&a);

@@ -275,14 +275,21 @@ struct Loader {
   int64_t st;
   const uint8_t* mask;
   int D, whole, w, lane;
-  uint32_t off[DMA ? kLoads : 1];  // byte offset of this lane's chunk of each load in the tile's rows
+  // Byte offset of this lane's chunk of each load in the tile's rows.  Where
+  // a load is whole rows, a multiple of the swizzle's eight, on from the one
+  // before, one offset and the (uniform) step between them stand for all.
+  static constexpr int kStepRows = 64 * NW % TL::C == 0 ? 64 * NW / TL::C : 0;
+  static constexpr bool kStep = kStepRows > 0 && kStepRows % 8 == 0;
+  uint32_t off[DMA && !kStep ? kLoads : 1];
+  uint32_t step;
 
   __device__ __forceinline__ void init(const T* p_, int64_t st_, int D_, int whole_, const uint8_t* mask_, int w_,
                                        int lane_) {
     p = p_; st = st_; D = D_; whole = whole_; mask = mask_; w = w_; lane = lane_;
+    step = (uint32_t)(kStepRows * (int)st * (int)sizeof(T));
     if constexpr (DMA) {
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
+      for (int j = 0; j < (kStep ? 1 : kLoads); ++j) {
         const int i = (j * NW + w) * 64 + lane, r = i / TL::C, c = (i % TL::C) ^ TL::swizzle(r);
         off[j] = c * 16 < D * (int)sizeof(T) ? (uint32_t)(r * (int)st * (int)sizeof(T) + c * 16) : kNoRow;
       }
@@ -297,7 +304,7 @@ struct Loader {
       uint32_t o[kLoads];
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        o[j] = off[j];
+        o[j] = kStep ? off[0] + j * step : off[j];  // (past every end stays past it)
         if (mask) {
           const int k = row0 + ((j * NW + w) * 64 + lane) / TL::C;
           if (mine(j) && (k >= end || mask[k] == 0)) o[j] = kNoRow;
