@@ -237,79 +237,67 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dq_few_k
 }
 
 // ---------------------------------------------------------------------------
-// What 32 NS keys (subtile n: column lane % 32) keep in registers.  DV, DK:
-// which of the two gradients (both, where a wave has the registers).
-template <typename T, int DP, int NS, bool DV, bool DK>
+// What 32 keys (column lane % 32) keep in registers.  DV, DK: which of the two
+// gradients (both, where a wave has the registers).
+template <typename T, int DP, bool DV, bool DK>
 struct Keys {
   using TL = Tile<T, DP>;
-  // fragments read ahead: 16-bit rows of 128 values (two waves a SIMD, 256
-  // registers) leave 16 registers for them beside s, 8 beside s and dp
+  // Fragments read ahead.  16-bit rows of 128 values run two waves a SIMD in
+  // 256 registers, 224 of them k, v, dk, dv, s and dp: there fewer are read
+  // ahead, the columns' first ones only when s and dp have left their
+  // registers, and the statistics a quarter at a time.  (A spilled register
+  // in the loop costs more than its traffic: its reload waits for every
+  // load into LDS before it.  Tried on 8 sequences, 32/8 heads of 128, 1024
+  // x 4096: this 0.94 ms; one wave a SIMD in 512 registers 1.11; 64 keys a
+  // wave in 512, half the LDS reads, spilled, 2.0; dv and dk in two kernels
+  // 0.43 + 0.53.)
   static constexpr bool kTight = sizeof(T) == 2 && DP == 128;
   static constexpr int kAheadRows = kTight ? 4 : 8, kAheadGrads = kTight ? 2 : 8, kAheadCols = 4;
-  u32x4_t k[NS][TL::KB], v[NS][DK ? TL::KB : 1];
-  f32x16_t dk[NS][DK ? DP / 32 : 1], dv[NS][DV ? DP / 32 : 1];
-  Sums<T, DP> sk[NS], sv[NS];
+  u32x4_t k[TL::KB], v[DK ? TL::KB : 1];
+  f32x16_t dk[DK ? DP / 32 : 1], dv[DV ? DP / 32 : 1];
+  Sums<T, DP> sk, sv;
   __device__ __forceinline__ void fold() {
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      if constexpr (DK) sk[n].fold(dk[n]);
-      if constexpr (DV) sv[n].fold(dv[n]);
-    }
+    if constexpr (DK) sk.fold(dk);
+    if constexpr (DV) sv.fold(dv);
   }
   __device__ __forceinline__ void finish() {
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      if constexpr (DK) sk[n].finish(dk[n]);
-      if constexpr (DV) sv[n].finish(dv[n]);
-    }
+    if constexpr (DK) sk.finish(dk);
+    if constexpr (DV) sv.finish(dv);
   }
   __device__ __forceinline__ void clear() {
+    sk.clear();
+    sv.clear();
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      sk[n].clear();
-      sv[n].clear();
-    }
+    for (int dt = 0; dt < (DK ? DP / 32 : 1); ++dt) dk[dt] = zero16();
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-#pragma unroll
-      for (int dt = 0; dt < (DK ? DP / 32 : 1); ++dt) dk[n][dt] = zero16();
-#pragma unroll
-      for (int dt = 0; dt < (DV ? DP / 32 : 1); ++dt) dv[n][dt] = zero16();
-    }
+    for (int dt = 0; dt < (DV ? DP / 32 : 1); ++dt) dv[dt] = zero16();
   }
-  __device__ __forceinline__ void load(const AttendArgs& a, int b, int hk, int n, int key, bool ok, int lane) {
-    load_row_frags<T, DP>((const T*)a.k + key * a.ks.t + b * a.ks.b + hk * a.ks.h, a.D, a.whole & kWholeK, ok, lane,
-                          k[n]);
+  __device__ __forceinline__ void load(const AttendArgs& a, int b, int hk, int key, bool ok, int lane) {
+    load_row_frags<T, DP>((const T*)a.k + key * a.ks.t + b * a.ks.b + hk * a.ks.h, a.D, a.whole & kWholeK, ok, lane, k);
     if constexpr (DK)
       load_row_frags<T, DP>((const T*)a.v + key * a.vs.t + b * a.vs.b + hk * a.vs.h, a.D, a.whole & kWholeV, ok, lane,
-                            v[n]);
+                            v);
   }
   // adds the terms of 32 query rows: their q and dout tiles and (lse2, delta)
   // pairs.  Rows past the last have zeros in all of them and add nothing.
   __device__ __forceinline__ void tile(const char* qt, const char* gt, const float* stat, float c2, int lane) {
-    f32x16_t s[NS], dp[NS];
-#pragma unroll
-    for (int n = 0; n < NS; ++n) s[n] = dp[n] = zero16();
+    // or the addresses of every fragment would be kept in registers over all tiles
+    if constexpr (kTight) asm volatile("" : "+v"(lane));
+    f32x16_t s = zero16(), dp = zero16();
     constexpr int NDT = DP / 32, NG = (DV ? 1 : 0) + (DK ? 1 : 0);
     Ahead<TL::KB, kAheadRows> rq;
     Ahead<TL::KB, kAheadGrads> rg;
-    Ahead<TL::PB * NDT * NG, kAheadCols> cols;      // k-block, d-tile, dout then q
+    Ahead<TL::PB * NDT * NG, kAheadCols> cols;  // k-block, d-tile, dout then q
     auto read_q = [&](int f) { return TL::row_frag(qt, 0, f, lane); };
     auto read_g = [&](int f) { return TL::row_frag(gt, 0, f, lane); };
     auto read_col = [&](int f) {
       return TL::col_frag(DV && f % NG == 0 ? gt : qt, TL::KR * (f / NG / NDT), f / NG % NDT, lane);
     };
     rq.start(read_q);
-    rq.run(read_q, [&](int f, u32x4_t x) {
-#pragma unroll
-      for (int n = 0; n < NS; ++n) s[n] = Mm<T>::mac(x, k[n][f], s[n]);
-    });
+    rq.run(read_q, [&](int f, u32x4_t x) { s = Mm<T>::mac(x, k[f], s); });
     if constexpr (DK) {
       rg.start(read_g);
-      rg.run(read_g, [&](int f, u32x4_t x) {
-#pragma unroll
-        for (int n = 0; n < NS; ++n) dp[n] = Mm<T>::mac(x, v[n][f], dp[n]);
-      });
+      rg.run(read_g, [&](int f, u32x4_t x) { dp = Mm<T>::mac(x, v[f], dp); });
     }
     if constexpr (!kTight) cols.start(read_col);
 #pragma unroll
@@ -318,33 +306,26 @@ struct Keys {
       const f32x4_t x = *(const f32x4_t*)at, y = *(const f32x4_t*)(at + 4);
       const float L[4] = {x[0], x[2], y[0], y[2]}, d[4] = {x[1], x[3], y[1], y[3]};
 #pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][4 * j + e] = exp_carried<T>(__builtin_fmaf(s[n][4 * j + e], c2, -L[e]));
-          if constexpr (DK) dp[n][4 * j + e] = s[n][4 * j + e] * (dp[n][4 * j + e] - d[e]);
-        }
-      if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);  // or all the pairs would be read at once
-    }
-    u32x4_t p[NS][TL::PB], ds[NS][TL::PB];
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-#pragma unroll
-      for (int pb = 0; pb < TL::PB; ++pb) {
-        if constexpr (DV) p[n][pb] = TL::reg_frag(s[n], pb);
-        if constexpr (DK) ds[n][pb] = TL::reg_frag(dp[n], pb);
+      for (int e = 0; e < 4; ++e) {
+        s[4 * j + e] = exp_carried<T>(__builtin_fmaf(s[4 * j + e], c2, -L[e]));
+        if constexpr (DK) dp[4 * j + e] = s[4 * j + e] * (dp[4 * j + e] - d[e]);
       }
-    if constexpr (kTight) {  // in the registers that s and dp leave
+      if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
+    }
+    u32x4_t p[TL::PB], ds[TL::PB];
+#pragma unroll
+    for (int pb = 0; pb < TL::PB; ++pb) {
+      if constexpr (DV) p[pb] = TL::reg_frag(s, pb);
+      if constexpr (DK) ds[pb] = TL::reg_frag(dp, pb);
+    }
+    if constexpr (kTight) {
       __builtin_amdgcn_sched_barrier(0);
       cols.start(read_col);
     }
     cols.run(read_col, [&](int f, u32x4_t x) {
       const int pb = f / NG / NDT, dt = f / NG % NDT;
-#pragma unroll
-      for (int n = 0; n < NS; ++n) {
-        if (DV && f % NG == 0) dv[n][DV ? dt : 0] = Mm<T>::mac(x, p[n][pb], dv[n][DV ? dt : 0]);
-        else dk[n][DK ? dt : 0] = Mm<T>::mac(x, ds[n][pb], dk[n][DK ? dt : 0]);
-      }
+      if (DV && f % NG == 0) dv[DV ? dt : 0] = Mm<T>::mac(x, p[pb], dv[DV ? dt : 0]);
+      else dk[DK ? dt : 0] = Mm<T>::mac(x, ds[pb], dk[DK ? dt : 0]);
     });
   }
 };
@@ -405,20 +386,21 @@ struct QueryTiles {
   }
 };
 
-// 128 NS keys per work-group, 32 NS per wave, which share the tiles of query
-// rows, in a ring of stages (one barrier a tile: the stage that is loaded next
-// was read before it).  NS = 2 reads every fragment from LDS once for two
-// products; it takes one wave's whole registers.
+// 128 keys per work-group, 32 per wave, which share the tiles of query rows,
+// in a ring of stages (one barrier a tile: the stage that is loaded next was
+// read before it): 64 rows a stage and two stages up to rows of 128 bytes
+// (64 sequences, 16 heads of 64, 256 x 256: 62 us, with stages of 32 rows
+// 66-69), else 32 rows and as many stages, up to four, as leave LDS to two
+// work-groups.
 template <typename T, int DP> constexpr int dkv_rows() { return DP * sizeof(T) <= 128 ? 64 : 32; }
 template <typename T, int DP, bool DMA> constexpr int dkv_ring() {
   constexpr int stage = QueryTiles<T, DP, dkv_rows<T, DP>(), 4, DMA>::kStage;
   return dkv_rows<T, DP>() == 64 ? 2 : 4 * stage <= 96 * 1024 ? 4 : 3 * stage <= 150 * 1024 ? 3 : 2;
 }
-template <typename T, int DP> constexpr int dkv_subtiles() { return 1; }
 
 template <typename T, int DP, bool DMA, bool DV, bool DK>
 __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_kernel(AttendArgs a) {
-  constexpr int TB = Tile<T, DP>::kBytes32, NS = dkv_subtiles<T, DP>(), R = dkv_ring<T, DP, DMA>();
+  constexpr int TB = Tile<T, DP>::kBytes32, R = dkv_ring<T, DP, DMA>();
   using Tiles = QueryTiles<T, DP, dkv_rows<T, DP>(), 4, DMA>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -426,18 +408,16 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
   if (!group_of(a, blockIdx.x, &grp, &tile)) return;
   const int b = grp / a.Hk, hk = grp - b * a.Hk;
   const int end = keys_of(a, b);
-  const int key0 = (tile * 4 + w) * 32 * NS + (lane & 31);
-  Keys<T, DP, NS, DV, DK> me;
+  const int key = tile * 128 + w * 32 + (lane & 31);
+  // whether key takes part, asked again at the end: kept, it would take registers from the loop
+  auto takes_part = [&] { return key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0); };
+  Keys<T, DP, DV, DK> me;
   me.clear();
-  if (tile * 128 * NS < end) {
+  if (tile * 128 < end) {
     const float c2 = a.scale * kLog2e;
     Tiles qt;
     qt.init(a, b, hk, w, lane);
-#pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      const int key = key0 + 32 * n;
-      me.load(a, b, hk, n, key, key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0), lane);
-    }
+    me.load(a, b, hk, key, takes_part(), lane);
     wait_vmem();  // from here on the ring's loads alone are counted
 #pragma unroll
     for (int i = 0; i < R - 1; ++i)
@@ -466,19 +446,14 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dkv_
     }
     me.finish();
   }
-#pragma unroll
-  for (int n = 0; n < NS; ++n) {
-    const int key = key0 + 32 * n;
-    if (key >= a.Tk) continue;
-    // keys of no query: zeros, whatever the products of their zeroed rows were
-    const bool ok = key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0);
-    if constexpr (DK)
-      store_col<T, DP>((T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h, me.dk[n], a.scale / kCarry<T>, a.D,
-                       a.whole & kWholeDk, lane, ok);
-    if constexpr (DV)
-      store_col<T, DP>((T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h, me.dv[n], 1.f / kCarry<T>, a.D,
-                       a.whole & kWholeDv, lane, ok);
-  }
+  if (key >= a.Tk) return;
+  const bool ok = takes_part();  // keys of no query: zeros, whatever the products of their zeroed rows were
+  if constexpr (DK)
+    store_col<T, DP>((T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h, me.dk, a.scale / kCarry<T>, a.D,
+                     a.whole & kWholeDk, lane, ok);
+  if constexpr (DV)
+    store_col<T, DP>((T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h, me.dv, 1.f / kCarry<T>, a.D,
+                     a.whole & kWholeDv, lane, ok);
 }
 
 // Few keys: 32 per work-group, the tiles of query rows dealt to its waves.
@@ -495,7 +470,7 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
   const int key = tile * 32 + (lane & 31);
   const bool ok = key < end && (!a.mask || a.mask[b * a.mask_b + key] != 0);
   char* mine = lds + w * Tiles::kStage;
-  Keys<T, DP, 1, DV, DK> me;
+  Keys<T, DP, DV, DK> me;
   me.clear();
   if (tile * 32 < end) {
     const float c2 = a.scale * kLog2e;
@@ -503,7 +478,7 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
     qt.init(a, b, hk, 0, lane);
     qt.skip(w);
     if (w < qt.n) qt.fetch(mine);
-    me.load(a, b, hk, 0, key, ok, lane);
+    me.load(a, b, hk, key, ok, lane);
     for (int i = w; i < qt.n; i += NW) {
       wait_vmem();
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -519,13 +494,13 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
   const bool store = key < a.Tk;
   if constexpr (DK) {
     T* out = (T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h;
-    join_waves<T, DP>(me.dk[0], lds, a.D, w, lane, [&](int d, float v) {
+    join_waves<T, DP>(me.dk, lds, a.D, w, lane, [&](int d, float v) {
       if (store) out[d] = Elem<T>::from_f(ok ? as_f32(v * (a.scale / kCarry<T>)) : 0.f);
     });
   }
   if constexpr (DV) {
     T* out = (T*)a.dv + key * a.dvs.t + b * a.dvs.b + hk * a.dvs.h;
-    join_waves<T, DP>(me.dv[0], lds, a.D, w, lane, [&](int d, float v) {
+    join_waves<T, DP>(me.dv, lds, a.D, w, lane, [&](int d, float v) {
       if (store) out[d] = Elem<T>::from_f(ok ? as_f32(v / kCarry<T>) : 0.f);
     });
   }
@@ -537,8 +512,7 @@ static hipError_t attend_dkv_t(const AttendPlan& p, AttendArgs a, hipStream_t s)
   const bool few = p.few_keys;
   const size_t lds = few ? step_waves<T, DP>() * (size_t)QueryTiles<T, DP, 32, 1, DMA>::kStage
                          : dkv_ring<T, DP, DMA>() * (size_t)QueryTiles<T, DP, dkv_rows<T, DP>(), 4, DMA>::kStage;
-  const int keys = few ? 32 : 128 * dkv_subtiles<T, DP>();
-  a.tiles = (a.Tk + keys - 1) / keys;
+  a.tiles = few ? (a.Tk + 31) / 32 : (a.Tk + 127) / 128;
   const unsigned grid = attend_grid(&a);
   const hipError_t e = few ? allow_lds<attend_dkv_few_kernel<T, DP, DMA, DV, DK>>(lds)
                            : allow_lds<attend_dkv_kernel<T, DP, DMA, DV, DK>>(lds);
