@@ -8,7 +8,14 @@
 // order (no atomics): attend_dq_kernel walks over the keys with 32 query rows
 // in registers, as the forward does, and writes delta on its way;
 // attend_dkv_kernel walks over the query rows of every head of the group with
-// 32 keys in registers.  Both recompute s (seven products in place of five).
+// 32 keys in registers.  Both recompute s and dp (seven products in place of
+// five).  The matrix products are the bound, and beside them the reads of
+// their fragments from LDS: 8 sequences, 32/8 heads of 128, 1024 x up to 4096
+// keys, bf16: dq 470 us, 1090 TFLOP/s; dk and dv 750 us, 910 TFLOP/s.  At 64
+// sequences, 16 heads of 64, 256 x 256 the rows' way to LDS counts as much:
+// dq 52 us, dk and dv 62.  In fp32, with few rows and keys (8 sequences, 6/3
+// heads of 80, 37 x 191), dq takes 24 us and dk, dv 16, a chain of a few
+// dependent tiles.
 #pragma once
 #include <type_traits>
 
@@ -248,7 +255,7 @@ struct Keys {
   // registers, and the statistics a quarter at a time.  (A spilled register
   // in the loop costs more than its traffic: its reload waits for every
   // load into LDS before it.  Tried on 8 sequences, 32/8 heads of 128, 1024
-  // x 4096: this 0.94 ms; one wave a SIMD in 512 registers 1.11; 64 keys a
+  // x 4096: this 0.75 ms; with reloads 0.96; one wave a SIMD in 512 registers 1.11; 64 keys a
   // wave in 512, half the LDS reads, spilled, 2.0; dv and dk in two kernels
   // 0.43 + 0.53.)
   static constexpr bool kTight = sizeof(T) == 2 && DP == 128;

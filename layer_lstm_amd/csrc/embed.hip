@@ -6,9 +6,9 @@
 // together in ascending n (so that every call gives the same bits) and writes
 // every row once, in one of two ways:
 //
-// Few tokens (kFew): one launch.  A work-group owns a run of rows, reads all
-// ids, keeps its own rows' tokens in LDS, ordered by a counting sort, and sums
-// them.
+// Few tokens (kFew) and a table that one round of work-groups covers: one
+// launch.  A work-group owns a run of rows, reads all ids, keeps its own rows'
+// tokens in LDS, ordered by a counting sort, and sums them.
 //
 // Many: a stable radix sort of the tokens by id, the sums of the whole chunks
 // of kChunk sorted positions that hold one id alone, and then every row from
@@ -16,6 +16,15 @@
 // other ids one by one, its whole chunks by their sums.  A row therefore
 // costs at most 2 kChunk rows of dout and one sum per chunk, whatever its
 // share of the tokens.
+//
+// Bound by memory: each row of dout is read once and each of dtable written
+// once (65536 tokens, 50000 x 1024 bf16: 236 MB in 85 us, 2.8 TB/s: the sort's
+// four launches take 22 us of it, the chunks 8, the rows 32, and the gaps
+// between six launches most of the rest).  Which way, in us for one launch / the sort, bf16: 4096 tokens of 1000 x 256 9 / 19,
+// of 32000 x 512 24 / 30, of 32000 x 1024 37 / 34, of 32000 x 2048 68 / 43;
+// 32 tokens of 32000 x 512 21 / 29, of 32000 x 2048 58 / 39: past one round of
+// work-groups (kFewGroups of kFewRows rows and a slab) the launch repeats its
+// reading of the ids, and the sort wins whatever the number of tokens.
 #include "internal.hpp"
 #include "seq_internal.hpp"
 
@@ -23,7 +32,8 @@ namespace lstm {
 
 constexpr int kChunk = 64;         // sorted positions per chunk
 constexpr int kMaxDigit = 11;      // bits per pass of the sort
-constexpr int kFew = 4096;         // tokens the one-launch gradient takes
+constexpr int kFew = 4096;         // tokens the one-launch gradient takes (their list is in LDS),
+constexpr int kFewRows = 128, kFewGroups = 512;  // rows per work-group at most, and work-groups
 constexpr int kEmbThreads = 256;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSlab = 512;         // columns of a row a wave holds, 8 per lane
@@ -42,7 +52,8 @@ void make_embed_plan(const lstm_embed_shape& s, EmbedPlan* p) {
   p->blocks = (int)((s.N + kSortThreads * (int64_t)p->rounds - 1) / (kSortThreads * (int64_t)p->rounds));
   size_t off = 0;
   p->off_pair0 = p->off_pair1 = p->off_hist = p->off_seg = p->off_part = p->total = 0;
-  if (s.N <= kFew) return;
+  p->few = s.N == 0 || (s.N <= kFew && s.V * ((s.D + kSlab - 1) / kSlab) <= (int64_t)kFewRows * kFewGroups);
+  if (p->few) return;
   p->off_pair0 = off; off += align256_seq((size_t)s.N * 8);
   p->off_pair1 = off; off += align256_seq((size_t)s.N * 8);
   p->off_hist = off; off += align256_seq(((size_t)p->blocks << p->digit) * 4);
@@ -127,7 +138,9 @@ __device__ __forceinline__ void add_rows(uint32_t at, uint32_t m, const T* dout,
 }
 
 // ---------------------------------------------------------------------------
-// Forward: a wave per (row, slab).
+// Forward: a wave per (row, slab), bound by memory (65536 rows of 1024 bf16 out
+// of 50000: 27 us from the last-level cache, 48 from memory, 185 MB) or, for
+// the tokens of one step, by the launch (2.5 us).
 template <typename T, typename ID, bool VEC>
 __global__ void __launch_bounds__(kEmbThreads) embed_fwd_kernel(const ID* ids, const T* table, T* out, int64_t N,
                                                                 int64_t V, int64_t D, int64_t ldt, int64_t ldo,
@@ -174,7 +187,7 @@ __device__ __forceinline__ uint32_t take_place(volatile uint32_t* place, uint32_
 // owns the rows b, b + n, b + 2 n, ...: in most vocabularies the frequent
 // tokens have ids side by side.  A wave sums a row of up to kLight tokens, all
 // sixteen together one of more.
-constexpr int kFewThreads = 1024, kFewWaves = 16, kFewRows = 128, kLight = 16;
+constexpr int kFewThreads = 1024, kFewWaves = 16, kLight = 16;
 
 template <typename T, typename ID, bool VEC>
 __global__ void __launch_bounds__(kFewThreads) embed_few(const ID* ids, const T* dout, T* dtable, int N, int64_t V,
@@ -526,9 +539,8 @@ template <typename T, typename ID, bool VEC>
 static hipError_t embed_bwd_t(const EmbedPlan& p, const void* ids, const void* dout, char* ws, void* dtable,
                               hipStream_t s) {
   const unsigned slabs = slabs_of(p.D);
-  if (p.N <= kFew) {
-    // rows per work-group: two work-groups a compute unit, 16 to 128 rows
-    int64_t R = (p.V * slabs + 511) / 512;
+  if (p.few) {
+    int64_t R = (p.V * slabs + kFewGroups - 1) / kFewGroups;  // two work-groups a compute unit
     R = R < 16 ? 16 : R > kFewRows ? kFewRows : (R + 15) / 16 * 16;
     int rbits = 4;
     while ((1 << rbits) < R) ++rbits;

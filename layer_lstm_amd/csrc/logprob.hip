@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(64) logprob_join_kernel(const T* logits, const
 // ---------------------------------------------------------------------------
 // Gradient: a work-group per (row, chunk of kGradVecs vectors a thread); the
 // few elements that have a term of their own (the target, the alternatives)
-// are written again by the group that owns them.
+// are written again by the group that owns them.  One read and one write of
+// the logits are all it does: 16384 x 32768 bf16, 2.15 GB, 353-366 us, 6 TB/s.
 constexpr int kGradVecs = 4;
 
 template <typename T, bool VEC>

@@ -76,7 +76,8 @@ struct EmbedPlan {
   float scale;
   int dtype, id64;
   int bits, passes, digit;  // of the sort: bits of an id, passes of `digit` bits
-  int rounds, blocks;       // tokens per block = 256 * rounds
+  int few;                  // the gradient in one launch, without a workspace
+  int rounds, blocks;       // of the sort: blocks of 1024 * rounds tokens
   size_t off_pair0, off_pair1, off_hist, off_seg, off_part, total;
 };
 void make_embed_plan(const lstm_embed_shape& s, EmbedPlan* p);
@@ -89,8 +90,8 @@ struct LogprobPlan {
   int64_t N, V, ld, ldg;
   float scale;
   int top, dtype, id64;
-  int parts;        // work-groups a row of the forward is split over
-  int64_t part;     // logits of each (a multiple of one pass of a work-group)
+  int parts;        // waves a row of the forward is split over
+  int64_t part;     // logits of each (a multiple of one round of a wave's loads)
   size_t off_key, off_sum, total;
 };
 void make_logprob_plan(const lstm_logprob_shape& s, int cus, LogprobPlan* p);

@@ -174,3 +174,22 @@ def test_refusals(lstm):
     assert L.lstm_embed_fwd(ctypes.byref(s), P(ids), P(table), P(out), None) == -3
     torch.cuda.synchronize()
     assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,V,D,kind", [
+    (1, 65537, 3, "flat"), (50, 70001, 8, "one"), (300, 33001, 600, "zipf"), (4096, 66000, 20, "zipf"),
+])
+def test_few_tokens_of_a_large_table(lstm, dt, N, V, D, kind):
+    """Few tokens, but a table too large for the one-launch gradient."""
+    test_embedding(lstm, dt, N, V, D, kind)
+    assert lstm.Embedding(N, V, D, code(lstm, dt)).workspace.numel() > 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_no_tokens_of_a_large_table(lstm, dt):
+    m = lstm.Embedding(0, 70001, 8, code(lstm, dt))
+    d = m.backward(torch.zeros(0, dtype=torch.int64, device="cuda"),
+                   torch.zeros(0, 8, dtype=lstm.torch_dtype(code(lstm, dt)), device="cuda"))
+    torch.cuda.synchronize()
+    assert d.shape == (70001, 8) and not d.any()
