@@ -21,8 +21,8 @@
 // once (65536 tokens, 50000 x 1024 bf16: 236 MB in 85 us, 2.8 TB/s: the sort's
 // four launches take 22 us of it, the chunks 8, the rows 32, and the gaps
 // between six launches most of the rest).  Which way, in us for one launch / the sort, bf16: 4096 tokens of 1000 x 256 9 / 19,
-// of 32000 x 512 24 / 30, of 32000 x 1024 37 / 34, of 32000 x 2048 68 / 43;
-// 32 tokens of 32000 x 512 21 / 29, of 32000 x 2048 58 / 39: past one round of
+// of 32000 x 512 24 / 30, of 32000 x 1024 37 / 34, of 32000 x 2048 68 / 40;
+// 32 tokens of 32000 x 512 21 / 29, of 32000 x 2048 58 / 35: past one round of
 // work-groups (kFewGroups of kFewRows rows and a slab) the launch repeats its
 // reading of the ids, and the sort wins whatever the number of tokens.
 #include "internal.hpp"
@@ -303,11 +303,12 @@ __device__ __forceinline__ uint32_t key_of(const ID* ids, int64_t n, int64_t V, 
 }
 
 // Digit counts of each block's tokens.  In the first pass the rows' ranges
-// start empty here.
+// start empty here, with the help of work-groups past the blocks where there
+// are few tokens and many rows.
 template <typename ID, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) embed_hist(const ID* ids, const uint2* in, uint32_t* hist, uint2* seg,
                                                            int64_t N, int64_t V, int64_t padding, int shift, int digit,
-                                                           int rounds) {
+                                                           int rounds, int blocks) {
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   uint32_t* cnt = (uint32_t*)lds_raw;
   const int bins = 1 << digit, tid = threadIdx.x;
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_hist(const ID* ids, const 
   if (FIRST) {
     const int64_t all = (int64_t)gridDim.x * kSortThreads;
     for (int64_t i = (int64_t)blockIdx.x * kSortThreads + tid; i < V; i += all) seg[i] = make_uint2(0, 0);
+    if ((int)blockIdx.x >= blocks) return;
   }
   __syncthreads();
   const int64_t n0 = (int64_t)blockIdx.x * kSortThreads * rounds;
@@ -519,13 +521,15 @@ static hipError_t embed_sort(const EmbedPlan& p, const ID* ids, char* ws, uint2*
   for (int k = 0; k < p.passes; ++k) {
     const int shift = k * p.digit;
     if (k == 0) {
-      embed_hist<ID, true><<<p.blocks, kSortThreads, lds, s>>>(ids, nullptr, hist, seg, p.N, p.V, p.padding, shift,
-                                                               p.digit, p.rounds);
+      const int64_t clear = p.V / (4 * kSortThreads) < 512 ? p.V / (4 * kSortThreads) : 512;
+      const unsigned grid = (unsigned)(clear > p.blocks ? clear : p.blocks);
+      embed_hist<ID, true><<<grid, kSortThreads, lds, s>>>(ids, nullptr, hist, seg, p.N, p.V, p.padding, shift, p.digit,
+                                                           p.rounds, p.blocks);
       embed_scatter<ID, true><<<p.blocks, kSortThreads, lds_all, s>>>(ids, nullptr, a, hist, p.N, p.V, p.padding, shift,
                                                                       p.digit, p.rounds);
     } else {
       embed_hist<ID, false><<<p.blocks, kSortThreads, lds, s>>>(nullptr, a, hist, nullptr, p.N, p.V, p.padding, shift,
-                                                                p.digit, p.rounds);
+                                                                p.digit, p.rounds, p.blocks);
       embed_scatter<ID, false><<<p.blocks, kSortThreads, lds_all, s>>>(nullptr, a, b, hist, p.N, p.V, p.padding, shift,
                                                                        p.digit, p.rounds);
       uint2* t = a; a = b; b = t;
