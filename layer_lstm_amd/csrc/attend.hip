@@ -32,6 +32,7 @@ template <typename T, int DP, int KT>
 __device__ __forceinline__ void attend_tile(const char* kt, const char* vt, uint64_t bits, const u32x4_t* q, f32x16_t* o,
                                             float& m, float& l, float c2, int lane) {
   using TL = Tile<T, DP>;
+  lane = tile_lane<DP == 256 || (sizeof(T) == 4 && DP == 128)>(lane);
   f32x16_t s[KT];
 #pragma unroll
   for (int t = 0; t < KT; ++t) s[t] = zero16();
@@ -87,8 +88,11 @@ __device__ __forceinline__ void attend_tile(const char* kt, const char* vt, uint
 // Keys per tile of the shared kernel: two double-buffered tiles within 128 KB.
 template <typename T, int DP> constexpr int fwd_keys() { return 4 * 64 * Tile<T, DP>::C * 16 <= 128 * 1024 ? 64 : 32; }
 
+// Two waves a SIMD but for rows of 512 bytes and more: q, o and s alone are
+// 224 registers there (bf16 heads of 256, 16 sequences, 16/8 heads, 512 x 512:
+// two waves, spilled, 548 us, one 131).
 template <typename T, int DP, bool DMA>
-__global__ void __launch_bounds__(256, DP * sizeof(T) > 512 ? 1 : 2) attend_fwd_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(256, DP * sizeof(T) >= 512 ? 1 : 2) attend_fwd_kernel(AttendArgs a) {
   using TL = Tile<T, DP>;
   constexpr int NK = fwd_keys<T, DP>(), TB = NK * TL::C * 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];  // K, V tiles, twice

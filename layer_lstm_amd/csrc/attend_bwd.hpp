@@ -116,6 +116,7 @@ struct QueryRow {
   // adds 32 keys' terms to dq (the factor `scale` of ds goes to the end)
   __device__ __forceinline__ void tile(const char* kt, const char* vt, uint32_t bits, f32x16_t* dq, float c2,
                                        int lane) const {
+    lane = tile_lane<DP == 256>(lane);
     f32x16_t s = zero16(), dp = zero16();
     constexpr int NDT = DP / 32;
     Ahead<2 * TL::KB, 8> rows;  // keys, then values
@@ -288,8 +289,7 @@ struct Keys {
   // adds the terms of 32 query rows: their q and dout tiles and (lse2, delta)
   // pairs.  Rows past the last have zeros in all of them and add nothing.
   __device__ __forceinline__ void tile(const char* qt, const char* gt, const float* stat, float c2, int lane) {
-    // or the addresses of every fragment would be kept in registers over all tiles
-    if constexpr (kTight) asm volatile("" : "+v"(lane));
+    lane = tile_lane<kTight || DP == 256 || (sizeof(T) == 4 && (DP == 64 || DP == 128))>(lane);
     f32x16_t s = zero16(), dp = zero16();
     constexpr int NDT = DP / 32, NG = (DV ? 1 : 0) + (DK ? 1 : 0);
     Ahead<TL::KB, kAheadRows> rq;
