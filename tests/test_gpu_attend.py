@@ -274,3 +274,22 @@ def test_refusals(lstm):
     assert fwd(P(q), P(k), P(k), None, None, P(ws), ws.numel(), P(out), P(m.lse)) == -2
     torch.cuda.synchronize()
     assert (out == 7.0).all()
+
+
+@pytest.mark.skip(reason="a run of this file with a variant of the fp16 backward, since taken out, faulted the GPU near "
+                         "this case; the cause is not shown yet")
+def test_fp16_probabilities_among_denormals(lstm):
+    """p of about 2^-17 each, below fp16's normal numbers, where dv is a normal number: its error is p's rounding and
+    its own, one unit each, and less than a third for the sums."""
+    Tq, Tk, D = 16, 131072, 16
+    rng = np.random.default_rng(3)
+    q, q64 = stored(torch, rng.normal(size=(Tq, 1, 1, D)), "f16")
+    k, k64 = stored(torch, rng.normal(size=(Tk, 1, 1, D)), "f16")
+    v, v64 = stored(torch, rng.normal(size=(Tk, 1, 1, D)), "f16")
+    g, g64 = stored(torch, 64 * rng.normal(size=(Tq, 1, 1, D)), "f16")
+    m = lstm.Attention(Tq, Tk, 1, 1, 1, D, lstm.F16)
+    m.forward(q, k, v)
+    dv = host(m.backward(g, q, k, v)[2])
+    want = so.attend(q64, k64, v64, D**-0.5, None, None, g64)[4]
+    err = np.linalg.norm(dv - want) / np.linalg.norm(want)
+    assert err <= 3 * UNIT["f16"], err
