@@ -402,6 +402,28 @@ class Stack:
 _ID_TYPES = {torch.int64: I64, torch.int32: I32}
 
 
+# A kernel that is given the address of host memory, or of another device's,
+# faults: the operators take tensors of the device that their buffers are on,
+# and launch while it is the current one.
+def _device_index(device):
+    d = torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"device {device}: a GPU")
+    return torch.cuda.current_device() if d.index is None else d.index
+
+
+def _on_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor on cuda:{index}, where the operator's buffers are (one is on {t.device})")
+
+
+def _stream_on(index, stream):
+    if torch.cuda.current_device() != index or (stream is not None and stream.device_index != index):
+        raise ValueError(f"cuda:{index} has to be the current device, and the stream's")
+    return _stream(stream)
+
+
 def _workspace(fn, name, shape, device):
     n = ctypes.c_size_t(0)
     rc = fn(ctypes.byref(shape), ctypes.byref(n))
@@ -422,6 +444,7 @@ class Embedding:
         self.shape = EmbedShape(N, V, D, D, D, -1 if padding is None else int(padding), float(scale), int(dtype), I64)
         self._ref = ctypes.byref(self.shape)
         self.workspace = _workspace(_lib.lstm_embed_query, "lstm_embed_query", self.shape, device)
+        self._dev = _device_index(device)
         self.tdtype = torch_dtype(dtype)
         self.out = self.dtable = None
 
@@ -433,12 +456,13 @@ class Embedding:
     def forward(self, ids, table, stream=None):
         """out [*ids.shape, D] = scale * table[ids]."""
         self._ids(ids)
+        _on_device(self._dev, ids, table)
         if table.dtype != self.tdtype or table.shape != (self.V, self.D) or (self.D > 1 and table.stride(1) != 1):
             raise ValueError(f"table: [{self.V}, {self.D}] of {self.tdtype}, rows contiguous")
         if self.out is None or self.out.shape[:-1] != ids.shape:
             self.out = torch.empty((*ids.shape, self.D), dtype=self.tdtype, device=self.device)
         self.shape.ld_table, self.shape.ld_out = max(table.stride(0), self.D), self.D
-        rc = _lib.lstm_embed_fwd(self._ref, _ptr(ids), _ptr(table), _ptr(self.out), _stream(stream))
+        rc = _lib.lstm_embed_fwd(self._ref, _ptr(ids), _ptr(table), _ptr(self.out), _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_embed_fwd")
         return self.out
@@ -446,6 +470,7 @@ class Embedding:
     def backward(self, ids, dout, stream=None):
         """dtable [V, D] of dout [*ids.shape, D]."""
         self._ids(ids)
+        _on_device(self._dev, ids, dout)
         if dout.dtype != self.tdtype or dout.shape != (*ids.shape, self.D):
             raise ValueError(f"dout: {[*ids.shape, self.D]} of {self.tdtype}")
         rows = dout if dout.dim() == 2 else dout.view(self.N, self.D)
@@ -455,7 +480,7 @@ class Embedding:
             self.dtable = torch.empty((self.V, self.D), dtype=self.tdtype, device=self.device)
         self.shape.ld_table, self.shape.ld_out = self.D, max(rows.stride(0), self.D)
         rc = _lib.lstm_embed_bwd(self._ref, _ptr(ids), _ptr(rows), _ptr(self.workspace), self.workspace.numel(),
-                                 _ptr(self.dtable), _stream(stream))
+                                 _ptr(self.dtable), _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_embed_bwd")
         return self.dtable
@@ -480,6 +505,7 @@ class Attention:
         if rc != OK:
             raise LstmError(rc, "lstm_attend_query")
         self._ref = ctypes.byref(self.shape)
+        self._dev = _device_index(device)
         self.ws_bytes = max(nf.value, nb.value)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.tdtype = torch_dtype(dtype)
@@ -504,12 +530,14 @@ class Attention:
                     (self.Tk > 1 and key_mask.stride(1) != 1):
                 raise ValueError(f"key_mask: bool or uint8 {[self.B, self.Tk]}, rows contiguous")
             self.shape.mask_b = key_mask.stride(0)
+        _on_device(self._dev, q, k, v, k_length, key_mask)
 
     def forward(self, q, k, v, k_length=None, key_mask=None, stream=None):
         """o [Tq, B, Hq, D] and lse [B, Hq, Tq]."""
         self._inputs(q, k, v, k_length, key_mask)
         rc = _lib.lstm_attend_fwd(self._ref, _ptr(q), _ptr(k), _ptr(v), _ptr(k_length), _ptr(key_mask),
-                                  _ptr(self.workspace), self.ws_bytes, _ptr(self.o), _ptr(self.lse), _stream(stream))
+                                  _ptr(self.workspace), self.ws_bytes, _ptr(self.o), _ptr(self.lse),
+                                  _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_attend_fwd")
         return self.o, self.lse
@@ -518,13 +546,14 @@ class Attention:
         """dq, dk, dv after a forward on the same inputs."""
         self._inputs(q, k, v, k_length, key_mask)
         self._strides("dout", self.shape.dout, dout, self.Tq, self.Hq)
+        _on_device(self._dev, dout)
         if self.dq is None:
             self.dq = torch.empty((self.Tq, self.B, self.Hq, self.D), dtype=self.tdtype, device=self.device)
             self.dk, self.dv = (torch.empty((self.Tk, self.B, self.Hk, self.D), dtype=self.tdtype, device=self.device)
                                 for _ in range(2))
         rc = _lib.lstm_attend_bwd(self._ref, _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length),
                                   _ptr(key_mask), _ptr(self.o), _ptr(self.lse), _ptr(self.workspace), self.ws_bytes,
-                                  _ptr(self.dq), _ptr(self.dk), _ptr(self.dv), _stream(stream))
+                                  _ptr(self.dq), _ptr(self.dk), _ptr(self.dv), _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_attend_bwd")
         return self.dq, self.dk, self.dv
@@ -541,6 +570,7 @@ class LogProb:
         self.shape = LogprobShape(N, V, V, V, float(scale), int(top), int(dtype), I64)
         self._ref = ctypes.byref(self.shape)
         self.workspace = _workspace(_lib.lstm_logprob_query, "lstm_logprob_query", self.shape, device)
+        self._dev = _device_index(device)
         self.tdtype = torch_dtype(dtype)
         self.record = torch.empty((N, 2), dtype=torch.float32, device=device)
         self.lse, self.logp, self.entropy = (torch.empty(N, dtype=torch.float32, device=device) for _ in range(3))
@@ -552,6 +582,7 @@ class LogProb:
             raise ValueError(f"logits: [{self.N}, {self.V}] of {self.tdtype}, rows contiguous")
         if targets.shape != (self.N,) or not targets.is_contiguous() or targets.dtype not in _ID_TYPES:
             raise ValueError(f"targets: [{self.N}] int32 or int64, contiguous")
+        _on_device(self._dev, logits, targets)
         self.shape.id_type = _ID_TYPES[targets.dtype]
         self.shape.ld = max(logits.stride(0), self.V)
 
@@ -562,7 +593,8 @@ class LogProb:
             self.top_ids = torch.empty((self.N, self.top), dtype=targets.dtype, device=self.device)
         rc = _lib.lstm_logprob_fwd(self._ref, _ptr(logits), _ptr(targets), _ptr(self.workspace),
                                    self.workspace.numel(), _ptr(self.record), _ptr(self.lse), _ptr(self.logp),
-                                   _ptr(self.entropy), _ptr(self.top_logp), _ptr(self.top_ids), _stream(stream))
+                                   _ptr(self.entropy), _ptr(self.top_logp), _ptr(self.top_ids),
+                                   _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_logprob_fwd")
         if not self.top:
@@ -576,13 +608,15 @@ class LogProb:
                                ("dtop", dtop, (self.N, self.top))):
             if g is not None and (g.dtype != torch.float32 or g.shape != shape or not g.is_contiguous()):
                 raise ValueError(f"{name}: {list(shape)} of float32, contiguous")
+        _on_device(self._dev, dlogp, dentropy, dtop)
         if dtop is not None and self.top and (self.top_ids is None or self.top_ids.dtype != targets.dtype):
             raise ValueError("backward follows a forward on the same targets")
         if self.dlogits is None:
             self.dlogits = torch.empty((self.N, self.V), dtype=self.tdtype, device=self.device)
         rc = _lib.lstm_logprob_bwd(self._ref, _ptr(logits), _ptr(targets), _ptr(self.record),
                                    _ptr(self.entropy), _ptr(self.top_ids), _ptr(dlogp), _ptr(dentropy),
-                                   _ptr(dtop) if self.top else None, _ptr(self.dlogits), _stream(stream))
+                                   _ptr(dtop) if self.top else None, _ptr(self.dlogits),
+                                   _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_logprob_bwd")
         return self.dlogits
