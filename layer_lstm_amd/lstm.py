@@ -418,6 +418,17 @@ def _on_device(index, *tensors):
             raise ValueError(f"every tensor on cuda:{index}, where the operator's buffers are (one is on {t.device})")
 
 
+def _row_stride(name, x, width):
+    """Elements between the rows of x [n, width], which the kernels take to be
+    at least width (the stride of one row alone means nothing)."""
+    if x.shape[0] <= 1:
+        return width
+    st = x.stride(0)
+    if st < width:
+        raise ValueError(f"{name}: rows {st} elements apart, at least {width} (an expanded tensor has to be copied)")
+    return st
+
+
 def _stream_on(index, stream):
     if torch.cuda.current_device() != index or (stream is not None and stream.device_index != index):
         raise ValueError(f"cuda:{index} has to be the current device, and the stream's")
@@ -461,7 +472,7 @@ class Embedding:
             raise ValueError(f"table: [{self.V}, {self.D}] of {self.tdtype}, rows contiguous")
         if self.out is None or self.out.shape[:-1] != ids.shape:
             self.out = torch.empty((*ids.shape, self.D), dtype=self.tdtype, device=self.device)
-        self.shape.ld_table, self.shape.ld_out = max(table.stride(0), self.D), self.D
+        self.shape.ld_table, self.shape.ld_out = _row_stride("table", table, self.D), self.D
         rc = _lib.lstm_embed_fwd(self._ref, _ptr(ids), _ptr(table), _ptr(self.out), _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_embed_fwd")
@@ -473,12 +484,15 @@ class Embedding:
         _on_device(self._dev, ids, dout)
         if dout.dtype != self.tdtype or dout.shape != (*ids.shape, self.D):
             raise ValueError(f"dout: {[*ids.shape, self.D]} of {self.tdtype}")
-        rows = dout if dout.dim() == 2 else dout.view(self.N, self.D)
+        try:
+            rows = dout if dout.dim() == 2 else dout.view(self.N, self.D)
+        except RuntimeError:
+            raise ValueError("dout: rows at one stride") from None
         if self.D > 1 and rows.stride(1) != 1:
             raise ValueError("dout: rows contiguous")
         if self.dtable is None:
             self.dtable = torch.empty((self.V, self.D), dtype=self.tdtype, device=self.device)
-        self.shape.ld_table, self.shape.ld_out = self.D, max(rows.stride(0), self.D)
+        self.shape.ld_table, self.shape.ld_out = self.D, _row_stride("dout", rows, self.D)
         rc = _lib.lstm_embed_bwd(self._ref, _ptr(ids), _ptr(rows), _ptr(self.workspace), self.workspace.numel(),
                                  _ptr(self.dtable), _stream_on(self._dev, stream))
         if rc != OK:
@@ -584,7 +598,7 @@ class LogProb:
             raise ValueError(f"targets: [{self.N}] int32 or int64, contiguous")
         _on_device(self._dev, logits, targets)
         self.shape.id_type = _ID_TYPES[targets.dtype]
-        self.shape.ld = max(logits.stride(0), self.V)
+        self.shape.ld = _row_stride("logits", logits, self.V)
 
     def forward(self, logits, targets, stream=None):
         """logp [N], entropy [N] and, with alternatives, top_logp and top_ids [N, top] (ids of targets' type)."""

@@ -71,3 +71,25 @@ def test_buffers_are_on_a_gpu_and_it_is_the_current_one(lib, monkeypatch):
     assert not launches
     m.forward(ids, table)
     assert launches == ["lstm_embed_fwd"]
+
+
+def test_rows_that_overlap_are_refused(lib, monkeypatch):
+    """A row expanded over the tokens (the gradient of a sum over them), a
+    table or logits of one row, rows closer than their width: the kernels
+    would read past them.  One row alone may have any stride."""
+    lstm, launches = lib
+    monkeypatch.setattr(lstm, "_on_device", lambda *a: None)
+    e, p = lstm.Embedding(6, 9, 8), lstm.LogProb(6, 8)
+    ids, row = torch.zeros(6, dtype=torch.int64), torch.zeros(8)
+    near = torch.zeros(100).as_strided((6, 8), (7, 1))
+    for call in (lambda: e.forward(ids, row.expand(9, 8)), lambda: e.backward(ids, row.expand(6, 8)),
+                 lambda: e.backward(ids.view(2, 3), row.expand(2, 3, 8)), lambda: e.backward(ids, near),
+                 lambda: e.backward(ids.view(2, 3), torch.zeros(3, 2, 8).transpose(0, 1)),
+                 lambda: p.forward(row.expand(6, 8), ids), lambda: p.forward(near, ids),
+                 lambda: p.backward(row.expand(6, 8), ids), lambda: lstm.LogProb(6, 1).forward(row[:1].expand(6, 1), ids)):
+        with pytest.raises(ValueError, match="rows"):
+            call()
+    assert not launches
+    lstm.Embedding(1, 9, 8).backward(ids[:1], torch.zeros(100).as_strided((1, 8), (3, 1)))
+    lstm.LogProb(1, 8).forward(row.expand(1, 8), ids[:1])
+    assert len(launches) == 2
