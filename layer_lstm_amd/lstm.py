@@ -429,6 +429,15 @@ def _row_stride(name, x, width):
     return st
 
 
+def _buffer(shape, dtype, device, stream):
+    """An output made when it is first needed, from the memory of the stream
+    that writes it: memory of the current stream may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _stream_on(index, stream):
     if torch.cuda.current_device() != index or (stream is not None and stream.device_index != index):
         raise ValueError(f"cuda:{index} has to be the current device, and the stream's")
@@ -471,7 +480,7 @@ class Embedding:
         if table.dtype != self.tdtype or table.shape != (self.V, self.D) or (self.D > 1 and table.stride(1) != 1):
             raise ValueError(f"table: [{self.V}, {self.D}] of {self.tdtype}, rows contiguous")
         if self.out is None or self.out.shape[:-1] != ids.shape:
-            self.out = torch.empty((*ids.shape, self.D), dtype=self.tdtype, device=self.device)
+            self.out = _buffer((*ids.shape, self.D), self.tdtype, self.device, stream)
         self.shape.ld_table, self.shape.ld_out = _row_stride("table", table, self.D), self.D
         rc = _lib.lstm_embed_fwd(self._ref, _ptr(ids), _ptr(table), _ptr(self.out), _stream_on(self._dev, stream))
         if rc != OK:
@@ -491,7 +500,7 @@ class Embedding:
         if self.D > 1 and rows.stride(1) != 1:
             raise ValueError("dout: rows contiguous")
         if self.dtable is None:
-            self.dtable = torch.empty((self.V, self.D), dtype=self.tdtype, device=self.device)
+            self.dtable = _buffer((self.V, self.D), self.tdtype, self.device, stream)
         self.shape.ld_table, self.shape.ld_out = self.D, _row_stride("dout", rows, self.D)
         rc = _lib.lstm_embed_bwd(self._ref, _ptr(ids), _ptr(rows), _ptr(self.workspace), self.workspace.numel(),
                                  _ptr(self.dtable), _stream_on(self._dev, stream))
@@ -562,8 +571,8 @@ class Attention:
         self._strides("dout", self.shape.dout, dout, self.Tq, self.Hq)
         _on_device(self._dev, dout)
         if self.dq is None:
-            self.dq = torch.empty((self.Tq, self.B, self.Hq, self.D), dtype=self.tdtype, device=self.device)
-            self.dk, self.dv = (torch.empty((self.Tk, self.B, self.Hk, self.D), dtype=self.tdtype, device=self.device)
+            self.dq = _buffer((self.Tq, self.B, self.Hq, self.D), self.tdtype, self.device, stream)
+            self.dk, self.dv = (_buffer((self.Tk, self.B, self.Hk, self.D), self.tdtype, self.device, stream)
                                 for _ in range(2))
         rc = _lib.lstm_attend_bwd(self._ref, _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(k_length),
                                   _ptr(key_mask), _ptr(self.o), _ptr(self.lse), _ptr(self.workspace), self.ws_bytes,
@@ -604,7 +613,7 @@ class LogProb:
         """logp [N], entropy [N] and, with alternatives, top_logp and top_ids [N, top] (ids of targets' type)."""
         self._rows(logits, targets)
         if self.top_ids is None or self.top_ids.dtype != targets.dtype:
-            self.top_ids = torch.empty((self.N, self.top), dtype=targets.dtype, device=self.device)
+            self.top_ids = _buffer((self.N, self.top), targets.dtype, self.device, stream)
         rc = _lib.lstm_logprob_fwd(self._ref, _ptr(logits), _ptr(targets), _ptr(self.workspace),
                                    self.workspace.numel(), _ptr(self.record), _ptr(self.lse), _ptr(self.logp),
                                    _ptr(self.entropy), _ptr(self.top_logp), _ptr(self.top_ids),
@@ -626,7 +635,7 @@ class LogProb:
         if dtop is not None and self.top and (self.top_ids is None or self.top_ids.dtype != targets.dtype):
             raise ValueError("backward follows a forward on the same targets")
         if self.dlogits is None:
-            self.dlogits = torch.empty((self.N, self.V), dtype=self.tdtype, device=self.device)
+            self.dlogits = _buffer((self.N, self.V), self.tdtype, self.device, stream)
         rc = _lib.lstm_logprob_bwd(self._ref, _ptr(logits), _ptr(targets), _ptr(self.record),
                                    _ptr(self.entropy), _ptr(self.top_ids), _ptr(dlogp), _ptr(dentropy),
                                    _ptr(dtop) if self.top else None, _ptr(self.dlogits),

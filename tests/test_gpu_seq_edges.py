@@ -38,3 +38,32 @@ def test_each_tensor_has_to_be_on_the_device(lstm):
             with pytest.raises(ValueError, match="cuda:0"):
                 f(*(x.cpu() if j == i else x for j, x in enumerate(args)))
     torch.cuda.synchronize()
+
+
+def test_outputs_made_for_another_stream(lstm):
+    """The current stream still has a fill of a freed tensor ahead of it; an
+    output first made for a call on another stream is not that memory."""
+    N, V, D, busy = 64, 20000, 1024, 400_000_000  # clock cycles, about 0.2 s
+    s = torch.cuda.Stream()
+    ids, dout = torch.zeros(N, dtype=torch.int64, device="cuda"), torch.ones(N, D, device="cuda")
+    x, g = torch.randn(N, V, device="cuda"), torch.ones(N, device="cuda")
+    q, k = torch.randn(512, 8, 16, 64, device="cuda"), torch.randn(512, 8, 16, 64, device="cuda")
+    e, p, a = lstm.Embedding(N, V, D), lstm.LogProb(N, V, top=2), lstm.Attention(512, 512, 8, 16, 16, 64)
+    p.forward(x, ids), a.forward(q, k, k)
+    e2, p2, a2 = lstm.Embedding(N, V, D), lstm.LogProb(N, V, top=2), lstm.Attention(512, 512, 8, 16, 16, 64)
+    p2.forward(x, ids), a2.forward(q, k, k)
+    calls = [(V * D, lambda m, st: m.backward(ids, dout, stream=st), e, e2),
+             (N * V, lambda m, st: m.backward(x, ids, g, stream=st), p, p2),
+             (q.numel(), lambda m, st: m.backward(q, q, k, k, stream=st), a, a2)]
+    for n, call, other, own in calls:
+        want = call(own, None)
+        want = [t.clone() for t in (want if isinstance(want, tuple) else (want,))]
+        torch.cuda.synchronize()
+        freed = [torch.empty(n, device="cuda") for _ in want]
+        torch.cuda._sleep(busy)
+        for t in freed:
+            t.fill_(7.0)
+        del freed, t
+        got = call(other, s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got if isinstance(got, tuple) else (got,), want))
