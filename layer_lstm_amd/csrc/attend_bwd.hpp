@@ -75,6 +75,54 @@ struct Sums {
   }
 };
 
+// ds as an operand of fp16.  Its size is that of dout, which a scaled loss may
+// bring to thousands, times p, which long keys bring to millionths: rounded as
+// it stands, ds overflows or falls among the denormals although the gradients
+// are normal numbers.  Each lane therefore carries the ds of its column (a row
+// of dq, a key of dk) times a power of two `by`, which falls when a tile's
+// largest passes 2^14 (to 2^9 .. 2^10, and the lane's sums with it) and else
+// stays: what the reference of a softmax is to p.  It starts so high that
+// nothing of 2^-66 or more stays below.  The other types have the exponents.
+// (Backward without / with it, 16 sequences, 16/8 heads, 512 x 512, us: heads
+// of 64 96 / 103, of 128 165 / 171, of 192 305 / 331, of 256 382 / 497; 8
+// sequences, 32/8 heads of 128, 1024 x 4096: 1970 / 2053.)
+template <typename T>
+struct DsRange {
+  static constexpr bool kMoves = std::is_same<T, f16_t>::value;
+  float by = 0x1p80f;
+  // N accumulators of 16 registers
+  template <int N>
+  __device__ __forceinline__ void fit(f32x16_t& ds, f32x16_t* acc) {
+    if constexpr (kMoves) {
+      float top = fabsf(ds[0]);
+#pragma unroll
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, fabsf(ds[j]));
+      top = fmaxf(top, other_half(top));
+      const bool past = top * by > 0x1p14f;
+      if (__ballot(past)) {
+        const float to = past ? __builtin_ldexpf(1.f, 10 - __builtin_amdgcn_frexp_expf(top)) : by, r = to / by;
+        by = to;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[i][j] *= r;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) ds[j] *= by;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void finish(f32x16_t* acc) const {
+    if constexpr (kMoves) {
+      const float r = 1.f / by;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] *= r;
+    }
+  }
+};
+
 // What a query row (column lane % 32 of the products) keeps in registers.
 template <typename T, int DP>
 struct QueryRow {
@@ -114,8 +162,8 @@ struct QueryRow {
     }
   }
   // adds 32 keys' terms to dq (the factor `scale` of ds goes to the end)
-  __device__ __forceinline__ void tile(const char* kt, const char* vt, uint32_t bits, f32x16_t* dq, float c2,
-                                       int lane) const {
+  __device__ __forceinline__ void tile(const char* kt, const char* vt, uint32_t bits, f32x16_t* dq, DsRange<T>& range,
+                                       float c2, int lane) const {
     lane = tile_lane<DP == 256>(lane);
     f32x16_t s = zero16(), dp = zero16();
     constexpr int NDT = DP / 32;
@@ -137,6 +185,7 @@ struct QueryRow {
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) s[j] = exp_carried<T>(__builtin_fmaf(s[j], c2, -lse2)) * (dp[j] - delta);
+    range.template fit<NDT>(s, dq);
     u32x4_t ds[TL::PB];
 #pragma unroll
     for (int pb = 0; pb < TL::PB; ++pb) ds[pb] = TL::reg_frag(s, pb);
@@ -169,6 +218,7 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
   for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = zero16();
   Sums<T, DP> sums;
   sums.clear();
+  DsRange<T> range;
   const float c2 = a.scale * kLog2e;
   const int n = (end + NK - 1) / NK;
   if (n > 0) {
@@ -189,10 +239,11 @@ __global__ void __launch_bounds__(256, DP * sizeof(T) > 256 ? 1 : 2) attend_dq_k
     }
 #pragma unroll
     for (int kt = 0; kt < NK / 32; ++kt)
-      row.tile(cur + kt * TL::kBytes32, cur + TB + kt * TL::kBytes32, (uint32_t)(now >> (32 * kt)), dq, c2, lane);
+      row.tile(cur + kt * TL::kBytes32, cur + TB + kt * TL::kBytes32, (uint32_t)(now >> (32 * kt)), dq, range, c2, lane);
     if (i % kFoldTiles == kFoldTiles - 1) sums.fold(dq);
   }
   sums.finish(dq);
+  range.template finish<DP / 32>(dq);
   if (row.ok)
     store_col<T, DP>((T*)a.dq + row.t * a.dqs.t + b * a.dqs.b + row.h * a.dqs.h, dq, a.scale / kCarry<T>, a.D,
                      a.whole & kWholeDq, lane);
@@ -227,17 +278,19 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dq_few_k
   f32x16_t dq[DP / 32];
 #pragma unroll
   for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = zero16();
+  DsRange<T> range;
   const float c2 = a.scale * kLog2e;
   for (int i = w; i < n; i += NW) {
     wait_vmem();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    row.tile(mine, mine + TB, (uint32_t)bits, dq, c2, lane);
+    row.tile(mine, mine + TB, (uint32_t)bits, dq, range, c2, lane);
     if (i + NW < n) {
       __builtin_amdgcn_s_waitcnt(kLgkm0);  // every fragment of this tile is read
       fetch(i + NW);
     }
   }
+  range.template finish<DP / 32>(dq);
   T* out = (T*)a.dq + row.t * a.dqs.t + b * a.dqs.b + row.h * a.dqs.h;
   join_waves<T, DP>(dq, lds, a.D, w, lane, [&](int d, float v) {
     if (row.ok) out[d] = Elem<T>::from_f(as_f32(v * (a.scale / kCarry<T>)));
@@ -264,12 +317,16 @@ struct Keys {
   u32x4_t k[TL::KB], v[DK ? TL::KB : 1];
   f32x16_t dk[DK ? DP / 32 : 1], dv[DV ? DP / 32 : 1];
   Sums<T, DP> sk, sv;
+  DsRange<T> range;
   __device__ __forceinline__ void fold() {
     if constexpr (DK) sk.fold(dk);
     if constexpr (DV) sv.fold(dv);
   }
   __device__ __forceinline__ void finish() {
-    if constexpr (DK) sk.finish(dk);
+    if constexpr (DK) {
+      sk.finish(dk);
+      range.template finish<DP / 32>(dk);
+    }
     if constexpr (DV) sv.finish(dv);
   }
   __device__ __forceinline__ void clear() {
@@ -320,10 +377,13 @@ struct Keys {
       if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);
     }
     u32x4_t p[TL::PB], ds[TL::PB];
+    if constexpr (DV)
 #pragma unroll
-    for (int pb = 0; pb < TL::PB; ++pb) {
-      if constexpr (DV) p[pb] = TL::reg_frag(s, pb);
-      if constexpr (DK) ds[pb] = TL::reg_frag(dp, pb);
+      for (int pb = 0; pb < TL::PB; ++pb) p[pb] = TL::reg_frag(s, pb);
+    if constexpr (DK) {
+      range.template fit<NDT>(dp, dk);
+#pragma unroll
+      for (int pb = 0; pb < TL::PB; ++pb) ds[pb] = TL::reg_frag(dp, pb);
     }
     if constexpr (kTight) {
       __builtin_amdgcn_sched_barrier(0);
@@ -500,6 +560,7 @@ __global__ void __launch_bounds__((64 * step_waves<T, DP>()), 1) attend_dkv_few_
   }
   const bool store = key < a.Tk;
   if constexpr (DK) {
+    me.range.template finish<DP / 32>(me.dk);
     T* out = (T*)a.dk + key * a.dks.t + b * a.dks.b + hk * a.dks.h;
     join_waves<T, DP>(me.dk, lds, a.D, w, lane, [&](int d, float v) {
       if (store) out[d] = Elem<T>::from_f(ok ? as_f32(v * (a.scale / kCarry<T>)) : 0.f);
@@ -549,8 +610,10 @@ static hipError_t attend_bwd_t(const AttendPlan& p, const AttendArgs& a0, hipStr
       attend_dq_kernel<T, DP, DMA><<<grid, 256, lds, s>>>(a);
   }
   if (a.Tk > 0) {
-    // fp32 rows of more than 128 values leave no registers for both sums
-    if constexpr (DP * sizeof(T) > 512) {
+    // fp32 rows of more than 128 values leave no registers for both sums, nor
+    // do fp16 rows of 256 beside the moving range (16 sequences, 16/8 heads,
+    // 512 x 512, the whole backward: one launch 924 us, spilled, two 497)
+    if constexpr (DP * sizeof(T) > 512 || (DsRange<T>::kMoves && DP == 256)) {
       const hipError_t e = attend_dkv_t<T, DP, DMA, true, false>(p, a, s);
       if (e != hipSuccess) return e;
       return attend_dkv_t<T, DP, DMA, false, true>(p, a, s);

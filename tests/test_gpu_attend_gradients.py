@@ -47,3 +47,33 @@ def test_gradients_of_shared_tiles(lstm, dt, D):
 @pytest.mark.parametrize("size", [s for s in SIZES if s[1] >= 5000] + [(300, 4096, 2, 2, 2, 128)])
 def test_gradients_over_thousands_of_keys(lstm, dt, size):
     run(lstm, dt, size)
+
+
+@pytest.mark.parametrize("dout", [3e-4, 12000.0])
+@pytest.mark.parametrize("size", [(32, 16, 1, 1, 1, 128), (60, 48, 3, 4, 2, 64), (40, 300, 20, 8, 8, 192), (34, 70, 20, 8, 8, 256),
+                                  (5, 33, 2, 2, 1, 250), (600, 90, 1, 3, 3, 128)])
+def test_fp16_gradients_at_the_ends_of_the_range(lstm, size, dout):
+    """dout as a scaled loss brings it, so large that p (dp - delta) passes fp16's largest number where the gradients
+    do not, and so small that it falls among the denormals where they do not."""
+    x64 = inputs("f16", *size, dout=dout)[1]
+    want = ab.results("f16", *x64, size[-1] ** -0.5)[0]
+    big = {n: abs(want[n]).max() for n in ("dq", "dk", "dv")}
+    assert all(b < 60000 for b in big.values()), big
+    run(lstm, "f16", size, dout)
+
+
+def test_fp16_gradients_that_grow_and_shrink_along_the_sum(lstm):
+    """Rows of dout over eight powers of ten, rising and falling along the rows and the keys' values alike."""
+    size = (256, 512, 1, 2, 2, 64)
+    x, x64 = inputs("f16", *size)
+    for name, n, turn in (("rise", 1, False), ("fall", 1, True)):
+        by = [10.0 ** (-4 + 8 * i / 255) for i in range(256)]
+        at = torch.tensor(by[::-1] if turn else by)[:, None, None, None]
+        vat = torch.logspace(-3, 0, 512)[:, None, None, None]
+        g, v = (x[3].float() * at / 4).half(), (x[2].float() * (vat.flip(0) if turn else vat)).half()
+        c = [t.cuda() for t in (x[0], x[1], v, g)]
+        m = lstm.Attention(256, 512, 1, 2, 2, 64, lstm.F16)
+        o, _ = m.forward(*c[:3])
+        got = dict(zip(("o", "dq", "dk", "dv"), (host(t) for t in (o, *m.backward(c[3], *c[:3])))))
+        print(name, flush=True)
+        ab.check("f16", got, x64[0], x64[1], v.double().numpy(), g.double().numpy(), m.shape.scale)
