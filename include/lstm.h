@@ -377,8 +377,11 @@ int lstm_embed_bwd(const lstm_embed_shape* shape, const void* ids, const void* d
  * [Tk], NULL = all).  Rows of k and v that are not valid are not used: they
  * may hold anything, infinities and NaN included.  A query with no valid key
  * has o = 0, lse = -inf and no gradient; dk and dv of such keys are zeros.
- * p enters sum p v rounded to the storage type, ds the products of dq and dk
- * (the operands of the matrix cores); scores, sums and statistics are fp32.
+ * In 16 bits the operands of the matrix cores are rounded to the storage type:
+ * p in the sums of o and dv, ds = p (dout . v - dout . o) in those of dq and dk
+ * (in fp16 times a power of two, so that neither overflows nor, for p of the
+ * backward down to 2^-29, falls among the denormals); the backward reads o as it was
+ * stored.  Scores, sums and statistics are fp32.
  * Any D in [1, 256], scale > 0; rows of whole aligned 16-byte chunks (t
  * stride included) are the fast case. */
 typedef struct {

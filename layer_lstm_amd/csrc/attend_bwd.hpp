@@ -23,16 +23,18 @@
 
 namespace lstm {
 
-// The exponential gives 0 below 2^-126: where the storage type has the range,
-// p is carried 2^32 times larger through the products and their sums, and the
-// factor goes with `scale` when the sums are stored, so that the gradients of
-// the smallest p survive as far as the type reaches.  (fp16 would overflow.)
-// In bf16 the factor is in the exponent, y + 32, whose rounding (2^-19 of p)
-// is far below the storage type's; in fp32 it would be the largest error of
-// all, so there the factor is multiplied on, and the exponent of a small p is
-// raised by 64 first.
-template <typename T> constexpr float kCarry = std::is_same<T, f16_t>::value ? 1.f : 4294967296.f;
-template <typename T> constexpr float kInExponent = std::is_same<T, bf16_t>::value ? 32.f : 0.f;
+// The exponential gives 0 below 2^-126: p is carried 2^32 times larger through
+// the products and their sums, in fp16, whose largest is 2^16, 2^15 times (p is
+// an operand of dv, and its normal numbers then reach down to 2^-29 and not
+// 2^-14), and the factor goes with `scale` when the sums are stored, so that
+// the gradients of the smallest p survive as far as the type reaches.  In 16
+// bits the factor is in the exponent, y + 32 or y + 15, whose rounding (2^-19
+// of p) is far below the storage type's; in fp32 it would be the largest error
+// of all, so there the factor is multiplied on, and the exponent of a small p
+// is raised by 64 first.
+template <typename T> constexpr float kCarry = std::is_same<T, f16_t>::value ? 32768.f : 4294967296.f;
+template <typename T>
+constexpr float kInExponent = std::is_same<T, float>::value ? 0.f : std::is_same<T, f16_t>::value ? 15.f : 32.f;
 template <typename T>
 __device__ __forceinline__ float exp_carried(float y) {
   if constexpr (std::is_same<T, float>::value) {

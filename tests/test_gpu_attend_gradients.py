@@ -1,9 +1,10 @@
 """Cross attention's results against fp64 within what their own roundings
 account for (attend_bounds.py)."""
+import numpy as np
 import pytest
 
 import attend_bounds as ab
-from seq_util import code, host
+from seq_util import UNIT, code, host
 from test_attend_bounds import SIZES, inputs
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +78,22 @@ def test_fp16_gradients_that_grow_and_shrink_along_the_sum(lstm):
         got = dict(zip(("o", "dq", "dk", "dv"), (host(t) for t in (o, *m.backward(c[3], *c[:3])))))
         print(name, flush=True)
         ab.check("f16", got, x64[0], x64[1], v.double().numpy(), g.double().numpy(), m.shape.scale)
+
+
+@pytest.mark.parametrize("size", [s for s in SIZES if s[1] >= 5000] + [(300, 4096, 2, 2, 2, 128), (64, 4096, 1, 1, 1, 64)])
+@pytest.mark.parametrize("dout", [0.01, 1.0, 100.0])
+def test_fp16_gradients_over_thousands_of_keys(lstm, size, dout):
+    run(lstm, "f16", size, dout)
+
+
+def test_fp16_probabilities_of_millionths(lstm):
+    """p of about 2^-17 each, below fp16's normal numbers, where dv is a normal number: its error is p's rounding and
+    its own, one unit each, and less than a third for the sums."""
+    Tq, Tk, D = 16, 131072, 16
+    x, x64 = inputs("f16", Tq, Tk, 1, 1, 1, D, dout=64.0)
+    q, k, v, g = (t.cuda() for t in x)
+    m = lstm.Attention(Tq, Tk, 1, 1, 1, D, lstm.F16)
+    m.forward(q, k, v)
+    dv = host(m.backward(g, q, k, v)[2])
+    want = ab.results("f16", *x64, m.shape.scale)[0]["dv"]
+    assert np.linalg.norm(dv - want) <= 3 * UNIT["f16"] * np.linalg.norm(want)
