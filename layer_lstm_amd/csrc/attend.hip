@@ -10,7 +10,9 @@
 // memory.  Scores are kept in powers of two, y = s log2 e - m, against a
 // reference m that moves only when a score passes it by more than kMaxLag
 // (2^kMaxLag times the largest p is no loss of precision in floating point);
-// most tiles rescale nothing.
+// most tiles rescale nothing.  In fp16 the reference stays kLift below the
+// largest score seen, so that p, as an operand, is a normal number down to
+// 2^-21 of the largest and not 2^-14.
 //
 // Two kernels.  attend_fwd_kernel: four waves of 32 rows share each tile of
 // keys, double-buffered, one barrier a tile; the matrix products are the
@@ -20,11 +22,14 @@
 // every wave walks over its own tiles with no barrier, the keys split over the
 // waves and over `splits` work-groups, joined at the end; the keys' and
 // values' bytes are the bound (see the kernel).
+#include <type_traits>
+
 #include "attend_common.hpp"
 
 namespace lstm {
 
-constexpr float kMaxLag = 8.f;
+template <typename T> constexpr float kLift = std::is_same<T, f16_t>::value ? 7.f : 0.f;
+template <typename T> constexpr float kMaxLag = 8.f + kLift<T>;  // fp16: p up to 2^15
 constexpr int kAheadRows = 8, kAheadCols = 4;  // fragments read ahead of their products
 
 // One tile of 32 KT keys for a wave's 32 rows.
@@ -62,8 +67,8 @@ __device__ __forceinline__ void attend_tile(const char* kt, const char* vt, uint
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
   top = fmaxf(top, other_half(top)) * c2;
-  if (__ballot(top > m + kMaxLag)) {
-    const float to = fmaxf(m, top), by = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+  if (__ballot(top > m + kMaxLag<T>)) {
+    const float to = fmaxf(m, top - kLift<T>), by = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
     m = to;
     l *= by;
 #pragma unroll

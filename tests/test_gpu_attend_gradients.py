@@ -97,3 +97,19 @@ def test_fp16_probabilities_of_millionths(lstm):
     dv = host(m.backward(g, q, k, v)[2])
     want = ab.results("f16", *x64, m.shape.scale)[0]["dv"]
     assert np.linalg.norm(dv - want) <= 3 * UNIT["f16"] * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("B,Tq", [(1, 1), (130, 33)])
+def test_fp16_small_probabilities_beside_a_large_one(lstm, B, Tq):
+    """One key of value 0 with nearly all of p, the others of value 1 with p of 2^-14 to 2^-20 each: o is their share,
+    whose error is p's rounding and its own, half a unit each, and less than a quarter for the sums."""
+    Tk, D = 1500, 16
+    k, v = torch.zeros(Tk, B, 1, D), torch.ones(Tk, B, 1, D)
+    k[0], v[0] = 1.0, 0.0
+    q, k, v = (t.half().cuda() for t in (torch.ones(Tq, B, 1, D), k, v))
+    for lower in (14.3, 15.6, 16.7, 17.6, 18.6, 19.7, 20.4):
+        scale = float(np.float32(lower * np.log(2) / D))
+        o, _ = lstm.Attention(Tq, Tk, B, 1, 1, D, lstm.F16, scale=scale).forward(q, k, v)
+        rest = (Tk - 1) * np.exp(-scale * D)
+        want = rest / (1 + rest)
+        assert (abs(host(o) - want) <= 1.25 * UNIT["f16"] * want + 2.0**-25).all(), lower
