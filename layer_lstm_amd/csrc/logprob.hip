@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
   RowSums r = {-INFINITY, 0.f, 0.f};
   TopList list;
   list.clear();
-  // C logits of this lane, E at a time 64 E apart, the first at id0 of the
-  // part (count: past its end, where -inf stands for them)
   const uint32_t count = (uint32_t)(hi - lo);
-  auto take = [&](float* f, auto C, uint32_t id0) {
+  // C logits of this lane, E at a time 64 E apart, the first at id0 of the
+  // part; from id `end` on -inf stands for them and they are nobody's keys
+  auto take = [&](float* f, auto C, uint32_t id0, uint32_t end) {
     constexpr int c = decltype(C)::value;
     float vm = f[0];
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
       while (__ballot(bits != 0)) {
         const int j = bits ? __builtin_ctz(bits) : 0;
         const uint32_t id = id0 + (j / E) * (64 * E) + j % E;
-        const bool in = bits != 0 && id < count;
+        const bool in = bits != 0 && id < end;
         const uint64_t key = ((uint64_t)order_of(pick<c>(f, bits & -bits)) << 32) | ~((uint32_t)lo + id);
         bits &= bits - 1;
         list.append(lds, in ? key : 0, __ballot(bits != 0) != 0, top, lane);
@@ -356,14 +356,14 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
     }
     list.set_floor(wave_threshold(lane < (int)nv ? order_of(vm) : 0, top));
   }
-  if (head > 0 || tail0 < count) take(edge, One{}, edge_id);
+  if (head > 0 || tail0 < count) take(edge, One{}, edge_id, count);
 #pragma unroll 1
   for (uint32_t v0 = 0; v0 < nv; v0 += 64 * U) {  // one copy of its long body: the next loads run beside it
     float f[U * E];
 #pragma unroll
     for (int u = 0; u < U; ++u) unpack<T>(raw[u], f + u * E);
     if (v0 + 64 * U < nv) fetch(v0 + 64 * U);
-    take(f, Take{}, head + (v0 + lane) * E);
+    take(f, Take{}, head + (v0 + lane) * E, tail0);
   }
   if (TOP) list.merge(lds, top, lane);
   r.s = wave_sum(r.s);

@@ -67,3 +67,18 @@ def test_outputs_made_for_another_stream(lstm):
         got = call(other, s)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got if isinstance(got, tuple) else (got,), want))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_alternatives_of_short_rows_are_all_there(lstm, dt):
+    """Rows of a few logits, banned ones among them, as many alternatives as logits, at every offset from 16 bytes: each
+    id once, ties by the lower."""
+    rng = np.random.default_rng(2)
+    for V in (1, 2, 3, 5, 6, 7, 9, 13, 18, 21, 27, 31):
+        x = rng.normal(size=(17, V))  # 17 rows of V: at most offsets
+        x[rng.random(x.shape) < 0.4] = -np.inf
+        x[3] = -np.inf
+        xs, x64 = stored(torch, x, dt)
+        m = lstm.LogProb(17, V, code(lstm, dt), top=V)
+        ids = m.forward(xs.cuda(), torch.zeros(17, dtype=torch.int64, device="cuda"))[3].cpu().numpy()
+        np.testing.assert_array_equal(ids, so.logprob(x64, np.zeros(17), 1.0, V)["top_ids"], err_msg=f"V = {V}")
