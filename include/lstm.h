@@ -423,7 +423,8 @@ int lstm_attend_bwd(const lstm_attend_shape* shape, const void* dout, const void
  * targets and top_ids have id_type.  Logits of -inf are banned tokens: p =
  * 0, no gradient.  A row of nothing but -inf has lse = logp = top_logp =
  * -inf (logp of a target outside [0, V) stays 0), entropy 0 and no gradient.
- * A NaN or +inf in a row makes its sums NaN.  0 <= top <= LSTM_MAX_TOP,
+ * A NaN or +inf in a row makes its sums NaN; among the alternatives NaN ranks
+ * above all numbers.  0 <= top <= LSTM_MAX_TOP,
  * top <= V; N < 2^24, V < 2^30, and N V < 2^37. */
 #define LSTM_MAX_TOP 32
 typedef struct {

@@ -54,10 +54,11 @@ void make_logprob_plan(const lstm_logprob_shape& s, int cus, LogprobPlan* p) {
   p->total = off;
 }
 
-// A logit as an unsigned integer of the same order (-0 taken as +0).
+// A logit as an unsigned integer of the same order (-0 taken as +0; NaN of
+// either sign above all others, so that it has a place in the list).
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);
-  return u ^ (uint32_t)(((int32_t)u >> 31) | (int32_t)0x80000000);
+  return x != x ? 0xffffffffu : u ^ (uint32_t)(((int32_t)u >> 31) | (int32_t)0x80000000);
 }
 __device__ __forceinline__ float from_order(uint32_t o) {
   return __uint_as_float(o ^ ((o & 0x80000000u) ? 0x80000000u : 0xffffffffu));

@@ -82,3 +82,24 @@ def test_alternatives_of_short_rows_are_all_there(lstm, dt):
         m = lstm.LogProb(17, V, code(lstm, dt), top=V)
         ids = m.forward(xs.cuda(), torch.zeros(17, dtype=torch.int64, device="cuda"))[3].cpu().numpy()
         np.testing.assert_array_equal(ids, so.logprob(x64, np.zeros(17), 1.0, V)["top_ids"], err_msg=f"V = {V}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [5, 300, 70000])
+def test_ids_of_rows_with_nan_are_tokens(lstm, dt, V):
+    """NaN of either sign, a few, among banned tokens, or nothing else: the alternatives are NaN first, then the largest,
+    and every id is one of the row's, once."""
+    rng = np.random.default_rng(3)
+    x, _ = stored(torch, rng.normal(size=(8, V)), dt)
+    nan = torch.tensor([0x7FC00000, -0x400000], dtype=torch.int32).view(torch.float32).to(x.dtype)
+    x[0], x[1] = nan[0], nan[1]
+    x[2], x[3] = -np.inf, -np.inf
+    x[2, V // 2], x[3, V // 2] = nan[0], nan[1]
+    x[4, 1::2], x[5, 1::2] = nan[0], nan[1]
+    x[6, V - 1] = nan[1]
+    top = 4
+    m = lstm.LogProb(8, V, code(lstm, dt), top=top)
+    ids = m.forward(x.cuda(), torch.zeros(8, dtype=torch.int64, device="cuda"))[3]
+    h = x.double().numpy()
+    want = np.argsort(-np.where(np.isnan(h), np.inf, h), axis=1, kind="stable")[:, :top]
+    np.testing.assert_array_equal(ids.cpu().numpy(), want)
