@@ -210,9 +210,10 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int64_t i, int id64) {
   return id64 ? ((const int64_t*)ids)[i] : (int64_t)((const int32_t*)ids)[i];
 }
 
-// (m, ls): a row's record
+// (m, ls): a row's record.  Without a number above -inf m is -inf, and ls -inf,
+// or NaN where the row has one.
 __device__ __forceinline__ float log_prob(float x, float scale, float m, float ls) {
-  return m == -INFINITY ? -INFINITY : (x - m) * scale - ls;
+  return m == -INFINITY ? ls : (x - m) * scale - ls;
 }
 
 // The target's logit, which lane 32 of the wave that writes a row reads
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_bwd_kernel(const T* logits
   const T* row = logits + n * ld;
   T* grad = dlogits + n * ldg;
   const float m = record[2 * n], ls = record[2 * n + 1];
-  const bool none = m == -INFINITY;
+  const bool none = m == -INFINITY && ls == -INFINITY;
   const float H = dentropy ? entropy[n] : 0.f, gH = dentropy ? dentropy[n] : 0.f;
   int64_t target = -1;
   float gl = 0.f;

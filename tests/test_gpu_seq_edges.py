@@ -103,3 +103,20 @@ def test_ids_of_rows_with_nan_are_tokens(lstm, dt, V):
     h = x.double().numpy()
     want = np.argsort(-np.where(np.isnan(h), np.inf, h), axis=1, kind="stable")[:, :top]
     np.testing.assert_array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [5, 300, 70000])
+def test_nan_in_a_row_without_numbers(lstm, dt, V):
+    """A row of NaN, one of banned tokens and a NaN: every sum and gradient of it is NaN, its neighbours' are not."""
+    x = torch.zeros(4, V, dtype=tdtype(torch, dt), device="cuda")
+    x[0], x[1], x[3] = float("nan"), float("-inf"), float("-inf")
+    x[1, V - 1] = float("nan")
+    t = torch.tensor([0, 1, 2, 3], device="cuda")
+    one = torch.ones(4, device="cuda")
+    m = lstm.LogProb(4, V, code(lstm, dt), top=2)
+    logp, H, tl, _ = m.forward(x, t)
+    g = m.backward(x, t, one, one)
+    for a in (logp, m.lse, H, tl, g):
+        assert torch.isnan(a[:2]).all() and not torch.isnan(a[2:]).any()
+    assert torch.isneginf(logp[3]) and torch.isneginf(m.lse[3]) and H[3] == 0 and not g[3].any()
