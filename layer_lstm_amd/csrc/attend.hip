@@ -399,7 +399,7 @@ hipError_t launch_attend_fwd(const AttendPlan& p, const AttendArgs& a, hipStream
 }
 
 hipError_t launch_attend_bwd(const AttendPlan& p, const AttendArgs& a, hipStream_t s) {
-  if (a.B == 0) return hipSuccess;
+  if (a.B == 0 || a.Hk == 0) return hipSuccess;
   Timed tm(8, s);
   if (p.dtype == LSTM_F32) return launch_attend_bwd_f32(p, a, s);
   if (p.dtype == LSTM_BF16) return launch_attend_bwd_bf16(p, a, s);

@@ -120,3 +120,12 @@ def test_nan_in_a_row_without_numbers(lstm, dt, V):
     for a in (logp, m.lse, H, tl, g):
         assert torch.isnan(a[:2]).all() and not torch.isnan(a[2:]).any()
     assert torch.isneginf(logp[3]) and torch.isneginf(m.lse[3]) and H[3] == 0 and not g[3].any()
+
+
+def test_attention_without_heads(lstm):
+    m = lstm.Attention(3, 4, 2, 0, 0, 16)
+    q, k = torch.empty(3, 2, 0, 16, device="cuda"), torch.empty(4, 2, 0, 16, device="cuda")
+    o, lse = m.forward(q, k, k)
+    grads = m.backward(q, q, k, k)
+    torch.cuda.synchronize()
+    assert o.shape == (3, 2, 0, 16) and lse.shape == (2, 0, 3) and [g.shape for g in grads] == [q.shape, k.shape, k.shape]
