@@ -437,7 +437,7 @@ typedef struct {
 } lstm_logprob_shape;
 
 /* record [N][2]: required; receives a reference m near the row's largest
- * logit (-inf: a row of nothing but -inf) and log sum_v exp(scale (x_v - m)),
+ * logit (-inf: no number above -inf) and log sum_v exp(scale (x_v - m)),
  * which log p = scale (x - m) - that sum needs where lse = scale m + that sum
  * has been rounded.  lse, logp (needs targets), entropy: each optional (NULL =
  * not computed); top > 0 needs top_logp and top_ids.  Workspace:

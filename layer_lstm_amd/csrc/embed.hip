@@ -497,9 +497,11 @@ static unsigned slabs_of(int64_t D) { return (unsigned)((D + kSlab - 1) / kSlab)
 
 template <typename T, typename ID, bool VEC>
 static hipError_t embed_fwd_t(const EmbedPlan& p, const void* ids, const void* table, void* out, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + 3) / 4), slabs_of(p.D));
-  embed_fwd_kernel<T, ID, VEC><<<grid, kEmbThreads, 0, s>>>((const ID*)ids, (const T*)table, (T*)out, p.N, p.V, p.D,
-                                                            p.ldt, p.ldo, p.scale);
+  for (int64_t n0 = 0; n0 < p.N; n0 += 4 * kMaxGroups) {
+    const int64_t N = p.N - n0 < 4 * kMaxGroups ? p.N - n0 : 4 * kMaxGroups;
+    embed_fwd_kernel<T, ID, VEC><<<dim3((unsigned)((N + 3) / 4), slabs_of(p.D)), kEmbThreads, 0, s>>>(
+        (const ID*)ids + n0, (const T*)table, (T*)out + n0 * p.ldo, N, p.V, p.D, p.ldt, p.ldo, p.scale);
+  }
   return hipGetLastError();
 }
 
@@ -558,9 +560,12 @@ static hipError_t embed_bwd_t(const EmbedPlan& p, const void* ids, const void* d
   if (e != hipSuccess) return e;
   embed_chunks<T, VEC><<<dim3((unsigned)((p.N + kChunk - 1) / kChunk), slabs), 64, 0, s>>>(
       sorted, (uint2*)(ws + p.off_seg), (float*)(ws + p.off_part), (const T*)dout, p.N, p.V, p.D, p.ldo, ldp);
-  embed_rows<T, VEC><<<dim3((unsigned)((p.V + 3) / 4), slabs), kEmbThreads, 0, s>>>(
-      sorted, (const uint2*)(ws + p.off_seg), (const float*)(ws + p.off_part), (const T*)dout, (T*)dtable, p.V, p.D,
-      p.ldo, p.ldt, ldp, p.scale);
+  for (int64_t v0 = 0; v0 < p.V; v0 += 4 * kMaxGroups) {
+    const int64_t V = p.V - v0 < 4 * kMaxGroups ? p.V - v0 : 4 * kMaxGroups;
+    embed_rows<T, VEC><<<dim3((unsigned)((V + 3) / 4), slabs), kEmbThreads, 0, s>>>(
+        sorted, (const uint2*)(ws + p.off_seg) + v0, (const float*)(ws + p.off_part), (const T*)dout,
+        (T*)dtable + v0 * p.ldt, V, p.D, p.ldo, p.ldt, ldp, p.scale);
+  }
   return hipGetLastError();
 }
 

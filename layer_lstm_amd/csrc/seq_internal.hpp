@@ -64,6 +64,9 @@ __device__ __forceinline__ u32x4_t pack(const float* f) {
   return v;
 }
 
+// A launch has fewer than 2^32 threads: work-groups of 256 that one may have.
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
+
 static inline size_t align256_seq(size_t v) { return (v + 255) & ~(size_t)255; }
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 

@@ -129,3 +129,24 @@ def test_attention_without_heads(lstm):
     grads = m.backward(q, q, k, k)
     torch.cuda.synchronize()
     assert o.shape == (3, 2, 0, 16) and lse.shape == (2, 0, 3) and [g.shape for g in grads] == [q.shape, k.shape, k.shape]
+
+
+def test_embedding_of_the_most_tokens_and_rows(lstm):
+    """One less than 2^26 of each: more rows than one launch of a wave each has threads for."""
+    n = (1 << 26) - 1
+    torch.cuda.empty_cache()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(-1, 10, (n,), generator=g, device="cuda", dtype=torch.int32)
+    table = torch.randn(10, 2, generator=g, device="cuda").half()
+    out = lstm.Embedding(n, 10, 2, lstm.F16).forward(ids, table)
+    for lo in (0, n // 2, n - 1000):
+        part = ids[lo : lo + 1000].long()
+        want = torch.where((part >= 0)[:, None], table[part.clamp(min=0)], 0.0)
+        assert torch.equal(out[lo : lo + 1000], want.half())
+    del out
+    ids, dout = torch.tensor([0, n - 1, n - 2, n // 2, n - 1], device="cuda"), torch.randn(5, 2, generator=g, device="cuda").half()
+    m = lstm.Embedding(5, n, 2, lstm.F16)
+    m.dtable = torch.full((n, 2), float("nan"), dtype=torch.float16, device="cuda")
+    got = m.backward(ids, dout)
+    assert torch.equal(got[[0, n - 2, n // 2]], dout[[0, 2, 3]]) and (got != 0).any(1).sum() == 4
+    assert torch.equal(got[n - 1], (dout[1].float() + dout[4].float()).half())
