@@ -556,16 +556,20 @@ static hipError_t logprob_bwd_t(const LogprobPlan& p, const void* logits, const 
                  ((p.ld - p.ldg) * (int64_t)sizeof(T)) % 16 == 0;
   const int64_t span = (int64_t)kLpThreads * kGradVecs * vec_of<T>();
   const int chunks = (int)((p.V + span - 1) / span);
-  const unsigned grid = (unsigned)(p.N * chunks);
-  const int top = dtop ? p.top : 0;
-  if (v)
-    logprob_bwd_kernel<T, true><<<grid, kLpThreads, 0, s>>>((const T*)logits, targets, record, entropy, top_ids, dlogp,
-                                                            dentropy, dtop, (T*)dlogits, p.V, p.ld, p.ldg, p.scale, top,
-                                                            p.id64, chunks);
-  else
-    logprob_bwd_kernel<T, false><<<grid, kLpThreads, 0, s>>>((const T*)logits, targets, record, entropy, top_ids, dlogp,
-                                                             dentropy, dtop, (T*)dlogits, p.V, p.ld, p.ldg, p.scale,
-                                                             top, p.id64, chunks);
+  const int64_t step = kMaxGroups / chunks;  // rows a launch
+  const int top = dtop ? p.top : 0, ids = p.id64 ? 8 : 4;
+  for (int64_t n = 0; n < p.N; n += step) {
+    const unsigned grid = (unsigned)((p.N - n < step ? p.N - n : step) * chunks);
+    auto from = [n](const auto* at, int64_t row) { return at ? at + n * row : nullptr; };
+    auto launch = [&](auto vec) {
+      logprob_bwd_kernel<T, decltype(vec)::value><<<grid, kLpThreads, 0, s>>>(
+          (const T*)logits + n * p.ld, from((const char*)targets, ids), record + 2 * n, from(entropy, 1),
+          from((const char*)top_ids, (int64_t)ids * p.top), from(dlogp, 1), from(dentropy, 1), from(dtop, p.top),
+          (T*)dlogits + n * p.ldg, p.V, p.ld, p.ldg, p.scale, top, p.id64, chunks);
+    };
+    if (v) launch(std::true_type{});
+    else launch(std::false_type{});
+  }
   return hipGetLastError();
 }
 

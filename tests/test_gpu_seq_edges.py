@@ -150,3 +150,33 @@ def test_embedding_of_the_most_tokens_and_rows(lstm):
     got = m.backward(ids, dout)
     assert torch.equal(got[[0, n - 2, n // 2]], dout[[0, 2, 3]]) and (got != 0).any(1).sum() == 4
     assert torch.equal(got[n - 1], (dout[1].float() + dout[4].float()).half())
+
+
+def test_gradient_of_the_most_rows(lstm):
+    """2^23 rows of 4097 logits, 137 GB, in place: more work-groups than one launch has threads for.  All rows but
+    a few are equal logits with no cotangent."""
+    N, V = 1 << 23, 4097
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 160e9:
+        pytest.skip("needs 160 GB of free device memory")
+    x = torch.zeros(N, V, device="cuda")
+    # one launch has 2^24 - 1 work-groups, two of them a row: the first starts again at row 2^23 - 1
+    rows = [0, 12345, N // 2, N - 3, N - 2, N - 1]
+    rng = np.random.default_rng(5)
+    part, part64 = stored(torch, rng.normal(size=(len(rows), V)), "f32")
+    x[rows] = part.cuda()
+    t = torch.full((N,), -1, device="cuda")
+    dl, dh = torch.zeros(N, device="cuda"), torch.zeros(N, device="cuda")
+    tr, lr, hr = rng.integers(0, V, len(rows)), rng.normal(size=len(rows)), rng.normal(size=len(rows))
+    t[rows], dl[rows], dh[rows] = (torch.from_numpy(a).to(b.dtype).cuda() for a, b in ((tr, t), (lr, dl), (hr, dh)))
+    m = lstm.LogProb(N, V, lstm.F32)
+    m.forward(x, t)
+    m.dlogits = x
+    m.backward(x, t, dl, dh)
+    got = host(x[rows])
+    want = so.logprob(part64, tr, 1.0, 0, lr.astype(np.float32), hr.astype(np.float32))["dlogits"]
+    within(got, want, 2e-5 * np.abs(want) + 1e-9, "dlogits")
+    mid = [1, N // 3, N - 4]
+    assert not x[mid].any()
+    del x, m
+    torch.cuda.empty_cache()
