@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
   // part; from id `end` on -inf stands for them and they are nobody's keys
   auto take = [&](float* f, auto C, uint32_t id0, uint32_t end) {
     constexpr int c = decltype(C)::value;
-    float vm = f[0];
+    float vm = f[0];  // NaN if one of them is, for the list
 #pragma unroll
-    for (int j = 1; j < c; ++j) vm = fmaxf(vm, f[j]);
+    for (int j = 1; j < c; ++j) vm = __builtin_elementwise_maximum(vm, f[j]);
     if (__ballot(vm > r.m + slack || (vm > r.m && r.m == -INFINITY))) r.move(fmaxf(wave_max(vm), r.m), c2);
     if (TOP && __ballot(list.wants(vm))) {
       // each lane's candidates as bits, then one of every lane at a time

@@ -106,6 +106,20 @@ def test_ids_of_rows_with_nan_are_tokens(lstm, dt, V):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_nan_far_along_a_row_of_numbers(lstm, dt):
+    """Each row a NaN at another place, among logits that rank high and low, in one and in several parts."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for N, V in ((2300, 20011), (40, 20011)):
+        x = torch.randn(N, V, generator=g, device="cuda")
+        x[:, 7] = 50.0
+        at = torch.randint(8, V, (N,), generator=g, device="cuda")
+        x[torch.arange(N, device="cuda"), at] = float("nan")
+        m = lstm.LogProb(N, V, code(lstm, dt), top=2)
+        ids = m.forward(x.to(tdtype(torch, dt)), torch.zeros(N, dtype=torch.int64, device="cuda"))[3]
+        assert torch.equal(ids, torch.stack([at, torch.full_like(at, 7)], 1))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("V", [5, 300, 70000])
 def test_nan_in_a_row_without_numbers(lstm, dt, V):
     """A row of NaN, one of banned tokens and a NaN: every sum and gradient of it is NaN, its neighbours' are not."""
