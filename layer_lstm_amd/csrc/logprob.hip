@@ -1,17 +1,18 @@
 // logprob.hip -- log probabilities of given tokens, entropy, best
 // alternatives, and the logits' gradient (gfx950).
 //
-// One pass over a row keeps, per lane, s = sum 2^y and t = sum 2^y y of
-// y = (x - m) scale log2(e) against a reference m of the wave, so that
-//   lse = scale m + ln 2 log2 s,   entropy = ln 2 (log2 s - t / s),
-//   log p = scale (x - m) - ln 2 log2 s,
+// One pass over a row keeps, against the largest logit m of the wave so far,
+// the number c of logits equal to m and, per lane, s = sum 2^y and t = sum 2^y y
+// of y = (x - m) scale log2(e) over the others, so that
+//   log sum exp(scale (x - m)) = log1p(c - 1 + s) =: ls,
+//   lse = scale m + ls,   entropy = ls - ln 2 t / (c + s),
+//   log p = scale (x - m) - ls,
 // the last without the rounding of lse, which for logits of large magnitude
 // (a row of the type's lowest value, say) would be all of the result: the
-// gradient therefore reads m and ln s (the record) and not lse.
-// The reference need not be the running maximum: any m that no logit passes
-// by more than kSlack keeps 2^y in range and costs no precision (s and t are
-// floating point), so it moves only when a logit does pass it, which after
-// the first few vectors of a row is rare, and the sums are rescaled then.
+// gradient therefore reads m and ls (the record) and not lse.  The largest
+// logits' own 1 stays out of the sum so that where one token has nearly all of
+// p, ls and with it 1 - p keep all their digits: in s = 1 + 10^-5 they would be
+// two.  A new m, of which a row has few, rescales the sums.
 //
 // The alternatives are kept as a list sorted across the lanes of a wave: a
 // 64-bit key per lane, the logit in an order-preserving form above the
@@ -29,7 +30,6 @@ namespace lstm {
 constexpr int kLpThreads = 256;
 constexpr int kLpVecs = 4;      // 16-byte vectors a lane of the forward takes at a time
 constexpr int kMaxParts = 64;   // a row's parts are joined by the lanes of one wave
-constexpr float kSlack = 16.f;  // how far (in powers of two) a logit may pass the reference
 
 void make_logprob_plan(const lstm_logprob_shape& s, int cus, LogprobPlan* p) {
   p->N = s.N; p->V = s.V; p->ld = s.ld; p->ldg = s.ld_grad;
@@ -88,26 +88,33 @@ __device__ __forceinline__ float wave_sum(float v) {
   return wave_reduce(v, 0.f, [](float a, float b) { return a + b; });
 }
 
-// Sums against a reference m: s = sum 2^y, t = sum 2^y y.  y is one fused
-// multiply-add, x c2 - m2 with m2 = m c2 rounded; the rounding of m2 is put
-// back when the sums are read (lg).  Where m c2 might overflow (a row of the
-// type's lowest value) y = (x - m) c2 and m2 = 0.
+// Sums against a reference m, the largest logit seen: s = sum 2^y, t = sum 2^y
+// y over smaller ones, c the number of those equal to it.  y is one fused
+// multiply-add, x c2 - m2 with m2 = m c2 rounded; the rounding of m2, which is
+// the y of m itself, is taken off when the sums are read (lost).  Where m c2
+// might overflow (a row of the type's lowest value) y = (x - m) c2 and m2 = 0.
 struct RowSums {
-  float m, s, t;  // m = -inf: nothing but -inf so far (s = t = 0, or NaN)
+  float m, s, t, c;  // m = -inf: nothing but -inf so far (s = t = c = 0, or NaN)
   __device__ __forceinline__ bool huge(float c2) const { return !(fabsf(m * c2) < 1e37f); }
   __device__ __forceinline__ float m2(float c2) const { return huge(c2) ? 0.f : m * c2; }
+  __device__ __forceinline__ float lost(float c2) const { return huge(c2) ? 0.f : __builtin_fmaf(m, c2, -m2(c2)); }
   __device__ __forceinline__ void move(float to, float c2) {
     if (m != -INFINITY && to != m) {
-      RowSums n = {to, 0.f, 0.f};
+      RowSums n = {to, 0.f, 0.f, 0.f};
       const float d = !huge(c2) && !n.huge(c2) ? n.m2(c2) - m2(c2) : (to - m) * c2;
-      const float r = __builtin_amdgcn_exp2f(-d);
-      t = r == 0.f ? s * 0.f : (t - d * s) * r;
-      s *= r;
+      const float r = __builtin_amdgcn_exp2f(-d), y = lost(c2), own = c * __builtin_amdgcn_exp2f(y), all = s + own;
+      t = r == 0.f ? all * 0.f : (__builtin_fmaf(own, y, t) - d * all) * r;
+      s = all * r;
+      c = 0.f;
     }
     m = to;
   }
-  // log2 sum exp(scale (x - m)), and what has to go off y
-  __device__ __forceinline__ float lost(float c2) const { return huge(c2) ? 0.f : __builtin_fmaf(m, c2, -m2(c2)); }
+  // log sum exp(scale (x - m)), and the entropy
+  __device__ __forceinline__ void read(float c2, float* ls, float* entropy) const {
+    const float y = lost(c2), k = __builtin_amdgcn_exp2f(-y), rest = (c - 1.f) + s * k;
+    *ls = log1pf(rest);
+    *entropy = m == -INFINITY && s == 0.f ? 0.f : *ls - kLn2 * (k * __builtin_fmaf(-y, s, t)) / (1.f + rest);
+  }
 };
 
 // The largest threshold that at least `top` of the wave's values reach, on the
@@ -237,12 +244,13 @@ __device__ __forceinline__ Target read_target(const LogprobOut& o, int64_t n, co
 // A row's results from its sums, by one wave; lane i holds key i of the list.
 __device__ __forceinline__ void finish_row(const LogprobOut& o, int64_t n, Target target, float scale, int top,
                                            RowSums r, uint64_t key, int tid) {
-  const float l2 = log2f(r.s), ls = kLn2 * (l2 - r.lost(scale * kLog2e));
+  float ls, entropy;
+  r.read(scale * kLog2e, &ls, &entropy);
   if (tid == 0) {
     o.record[2 * n] = r.m;
     o.record[2 * n + 1] = ls;
     if (o.lse) o.lse[n] = r.m * scale + ls;
-    if (o.entropy) o.entropy[n] = r.m == -INFINITY && r.s == 0.f ? 0.f : kLn2 * (l2 - r.t / r.s);
+    if (o.entropy) o.entropy[n] = entropy;
   }
   if (tid == 32 && o.logp) o.logp[n] = target.real ? log_prob(target.x, scale, r.m, ls) : 0.f;
   if (tid < top) {
@@ -277,11 +285,11 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
   const int pt = (int)(unit - n * parts);
   const T* row = logits + n * ld;
   const int64_t lo = (int64_t)pt * part, hi = lo + part < V ? lo + part : V;
-  const float c2 = scale * kLog2e, slack = kSlack / c2;
+  const float c2 = scale * kLog2e;
   Target target = {0.f, false};
   if (parts == 1) target = read_target<T>(out, n, row, targets, V, lane);
 
-  RowSums r = {-INFINITY, 0.f, 0.f};
+  RowSums r = {-INFINITY, 0.f, 0.f, 0.f};
   TopList list;
   list.clear();
   const uint32_t count = (uint32_t)(hi - lo);
@@ -289,10 +297,17 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
   // part; from id `end` on -inf stands for them and they are nobody's keys
   auto take = [&](float* f, auto C, uint32_t id0, uint32_t end) {
     constexpr int c = decltype(C)::value;
-    float vm = f[0];  // NaN if one of them is, for the list
+    // maxima of groups of up to eight and of all, NaN if one of them is (for the list)
+    constexpr int kPer = c < 8 ? c : 8;
+    float gm[c / kPer], vm = -INFINITY;
 #pragma unroll
-    for (int j = 1; j < c; ++j) vm = __builtin_elementwise_maximum(vm, f[j]);
-    if (__ballot(vm > r.m + slack || (vm > r.m && r.m == -INFINITY))) r.move(fmaxf(wave_max(vm), r.m), c2);
+    for (int g = 0; g < c / kPer; ++g) {
+      gm[g] = f[g * kPer];
+#pragma unroll
+      for (int j = 1; j < kPer; ++j) gm[g] = __builtin_elementwise_maximum(gm[g], f[g * kPer + j]);
+      vm = __builtin_elementwise_maximum(vm, gm[g]);
+    }
+    if (__ballot(vm > r.m)) r.move(fmaxf(wave_max(vm), r.m), c2);
     if (TOP && __ballot(list.wants(vm))) {
       // each lane's candidates as bits, then one of every lane at a time
       // (mostly there is one in all)
@@ -306,6 +321,18 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
         const uint64_t key = ((uint64_t)order_of(pick<c>(f, bits & -bits)) << 32) | ~((uint32_t)lo + id);
         bits &= bits - 1;
         list.append(lds, in ? key : 0, __ballot(bits != 0) != 0, top, lane);
+      }
+    }
+    if (__ballot(vm == r.m && fabsf(vm) < INFINITY)) {  // counted, not summed
+#pragma unroll
+      for (int g = 0; g < c / kPer; ++g) {
+        if (!__ballot(gm[g] == r.m)) continue;
+#pragma unroll
+        for (int j = g * kPer; j < (g + 1) * kPer; ++j) {
+          const bool is = f[j] == r.m;
+          r.c += is ? 1.f : 0.f;
+          f[j] = is ? -INFINITY : f[j];
+        }
       }
     }
     const bool huge = r.huge(c2) && r.m != -INFINITY;
@@ -370,10 +397,11 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits
   if (TOP) list.merge(lds, top, lane);
   r.s = wave_sum(r.s);
   r.t = wave_sum(r.t);
+  r.c = wave_sum(r.c);
   if (parts == 1) {
     finish_row(out, n, target, scale, TOP ? top : 0, r, list.key, lane);
   } else {
-    if (lane == 0) wsum[unit] = f32x4_t{r.m, r.s, r.t, 0.f};
+    if (lane == 0) wsum[unit] = f32x4_t{r.m, r.s, r.t, r.c};
     if (TOP && lane < top) wkey[unit * top + lane] = list.key;
   }
 }
@@ -388,14 +416,15 @@ __global__ void __launch_bounds__(64) logprob_join_kernel(const T* logits, const
   const int64_t n = blockIdx.x;
   const float c2 = scale * kLog2e;
   const Target target = read_target<T>(out, n, logits + n * ld, targets, V, lane);
-  RowSums r = {-INFINITY, 0.f, 0.f};
+  RowSums r = {-INFINITY, 0.f, 0.f, 0.f};
   if (lane < parts) {
     const f32x4_t q = wsum[n * parts + lane];
-    r = RowSums{q[0], q[1], q[2]};
+    r = RowSums{q[0], q[1], q[2], q[3]};
   }
   r.move(wave_max(r.m), c2);
   r.s = wave_sum(r.s);
   r.t = wave_sum(r.t);
+  r.c = wave_sum(r.c);
   __shared__ TopLds lds;
   TopList list;
   list.clear();
