@@ -480,11 +480,14 @@ __global__ void __launch_bounds__(kLpThreads) logprob_bwd_kernel(const T* logits
     for (int k = 0; k < top; ++k) G += dtop[n * top + k];
   // scale (-p (G + gH (log p + H)));  p = 0: 0, log p kept finite.  The
   // exponential gives 0 below 2^-126: p is carried 2^32 times larger up to
-  // the last product.
+  // the last product, as the square of 2^16 sqrt(p).  (The factor in the
+  // exponent, y + 32, would round a p near 1 to 2^-19 of itself; one that raises
+  // small exponents alone takes 16384 x 32768 bf16 396 us.)
   const float out_scale = -scale * 2.3283064365386963e-10f;
+  auto log_p = [&](float x) { return __builtin_fmaf(x - m, scale, -ls); };
   auto value = [&](float x) {
-    const float lp = (x - m) * scale - ls, p = __builtin_amdgcn_exp2f(__builtin_fmaf(lp, kLog2e, 32.f));
-    return none ? 0.f : out_scale * (p * (G + gH * (fmaxf(lp, -1000.f) + H)));
+    const float lp = log_p(x), h = __builtin_amdgcn_exp2f(lp * (kLog2e / 2)) * 0x1p16f;
+    return none ? 0.f : out_scale * (h * h * (G + gH * (fmaxf(lp, -1000.f) + H)));
   };
   const int64_t off = VEC ? (int64_t)(((uintptr_t)row & 15u) / sizeof(T)) : 0;
   int64_t head = off ? E - off : 0;
@@ -505,10 +508,19 @@ __global__ void __launch_bounds__(kLpThreads) logprob_bwd_kernel(const T* logits
       if (of != ch) own = -1;
     }
     if (own >= 0) {
-      float g = own == target ? gl : 0.f;
+      float g = own == target ? gl : 0.f, other = own == target ? 0.f : gl;  // its cotangents, the others'
       if (dtop)
-        for (int k = 0; k < top; ++k) g += id_at(top_ids, n * top + k, id64) == own ? dtop[n * top + k] : 0.f;
-      own_g = none ? 0.f : value(Elem<T>::load(row + own)) + scale * g;
+        for (int k = 0; k < top; ++k) {
+          const float v = dtop[n * top + k];
+          const bool mine = id_at(top_ids, n * top + k, id64) == own;
+          g += mine ? v : 0.f;
+          other += mine ? 0.f : v;
+        }
+      // g - p G of a p near 1 by 1 - p = -expm1(log p), which keeps its digits
+      const float x = Elem<T>::load(row + own), lp = log_p(x), less = expm1f(lp);
+      own_g = none        ? 0.f
+              : lp > -.5f ? -scale * (other + __builtin_fmaf(G, less, gH * (lp + H) * (1.f + less)))
+                          : value(x) + scale * g;
     }
   }
   __syncthreads();
