@@ -382,7 +382,7 @@ int lstm_embed_bwd(const lstm_embed_shape* shape, const void* ids, const void* d
  * (in fp16 times a power of two, so that neither overflows nor, for p of the
  * backward down to 2^-29, falls among the denormals); the backward reads o as it was
  * stored.  Scores, sums and statistics are fp32.
- * Any D in [1, 256], scale > 0; rows of whole aligned 16-byte chunks (t
+ * Any D in [1, 256], 0 < scale <= 2.3e38; rows of whole aligned 16-byte chunks (t
  * stride included) are the fast case. */
 typedef struct {
   int64_t t, b, h;
@@ -407,7 +407,7 @@ int lstm_attend_bwd(const lstm_attend_shape* shape, const void* dout, const void
                     size_t workspace_bytes, void* dq, void* dk, void* dv, void* stream);
 
 /* Log probabilities of N rows of V logits (row stride ld >= V), z = scale *
- * logit with scale > 0 (an inverse temperature):
+ * logit with 0 < scale <= 2.3e38 (an inverse temperature):
  *   lse[n]     = log sum_v exp z[n][v]
  *   logp[n]    = z[n][targets[n]] - lse[n]     (a target outside [0, V): 0)
  *   entropy[n] = -sum_v p log p, p = exp(z - lse)   (0 where p = 0)

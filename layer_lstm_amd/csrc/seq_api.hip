@@ -8,6 +8,8 @@ namespace lstm {
 
 static bool dtype_ok(int d) { return d == LSTM_F32 || d == LSTM_BF16 || d == LSTM_F16; }
 static bool id_ok(int t) { return t == LSTM_I32 || t == LSTM_I64; }
+// a softmax's scale: scale log2 e is a positive number
+static bool scale_ok(float s) { return s > 0.f && s <= 2.3e38f; }
 static bool off_size(const void* p, int64_t e) { return p && ((uintptr_t)p % (uintptr_t)e) != 0; }
 static int status(hipError_t e) { return e == hipSuccess ? LSTM_OK : LSTM_ERR_LAUNCH; }
 static int64_t esize_of(int dtype) { return dtype == LSTM_F32 ? 4 : 2; }
@@ -31,7 +33,7 @@ static int embed_plan(const lstm_embed_shape* s, EmbedPlan* p) {
 static int logprob_plan(const lstm_logprob_shape* s, LogprobPlan* p) {
   if (!s) return LSTM_ERR_NULL;
   if (s->N < 0 || s->V < 0 || s->ld < s->V || s->ld_grad < s->V || s->top < 0 || s->top > LSTM_MAX_TOP ||
-      s->top > s->V || !(s->scale > 0.f) || s->scale > 3.0e38f)
+      s->top > s->V || !scale_ok(s->scale))
     return LSTM_ERR_DIMS;
   if (!dtype_ok(s->dtype) || !id_ok(s->id_type)) return LSTM_ERR_DTYPE;
   const int64_t far = (int64_t)1 << 36;
@@ -76,7 +78,7 @@ static bool dma_rows(const void* p, const lstm_stride& s, int64_t D, int64_t e) 
 static int attend_plan(const lstm_attend_shape* s, bool bwd, AttendPlan* p) {
   if (!s) return LSTM_ERR_NULL;
   if (s->Tq < 0 || s->Tk < 0 || s->B < 0 || s->Hq < 0 || s->Hk < 0 || s->D < 1 || (s->Hk == 0) != (s->Hq == 0) ||
-      (s->Hk > 0 && s->Hq % s->Hk != 0) || !(s->scale > 0.f) || s->scale > 3.0e38f || s->mask_b < 0 ||
+      (s->Hk > 0 && s->Hq % s->Hk != 0) || !scale_ok(s->scale) || s->mask_b < 0 ||
       !strides_ok(s->q) || !strides_ok(s->k) || !strides_ok(s->v) || !strides_ok(s->o) ||
       !disjoint(s->o, s->Tq, s->B, s->Hq, s->D))
     return LSTM_ERR_DIMS;

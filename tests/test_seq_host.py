@@ -91,3 +91,14 @@ def test_attend_strides(lstm, name, field, value):
     assert lstm.lib().lstm_attend_query(ctypes.byref(s), ctypes.byref(a), ctypes.byref(b)) in (0, -10)  # -10: no GPU
     s.dk.b = 0
     assert lstm.lib().lstm_attend_bwd(ctypes.byref(s), *([None] * 9), 0, None, None, None, None) == -2
+
+
+def test_scales_whose_exponents_overflow(lstm):
+    """scale log2 e has to be a number (above 2.36e38 it is not, and 0 times it is NaN)."""
+    L, n, k = lstm.lib(), ctypes.c_size_t(0), ctypes.c_size_t(0)
+    for scale, ok in ((2.3e38, True), (2.5e38, False), (3.0e38, False)):
+        s = attend_shape(lstm)
+        s.scale = scale
+        assert (L.lstm_attend_query(ctypes.byref(s), ctypes.byref(n), ctypes.byref(k)) == -2) != ok
+        s = lstm.LogprobShape(4, 9, 9, 9, scale, 3, 0, 1)
+        assert (L.lstm_logprob_query(ctypes.byref(s), ctypes.byref(n)) == -2) != ok
