@@ -343,8 +343,8 @@ enum { LSTM_I32 = 0, LSTM_I64 = 1 };
  * dtable is written whole (rows of no token are zeros); the row `padding`
  * (-1: none) is read like any other and takes no gradient, nor does an id
  * outside [0, V).  The sum of a row runs over n in a fixed order in fp32 and
- * is rounded once.  N, V < 2^26, D <= 2^20.  With [T][B] ids, out is
- * the x [T][B][I = D] of lstm_fwd_train() and dout its dx. */
+ * is rounded once.  scale is finite; N, V < 2^26, D <= 2^20.  With [T][B] ids,
+ * out is the x [T][B][I = D] of lstm_fwd_train() and dout its dx. */
 typedef struct {
   int64_t N, V, D;
   int64_t ld_table; /* elements between rows of table, and of dtable */

@@ -1,5 +1,7 @@
 // seq_api.hip -- the extern "C" entry points of the sequence-to-sequence
 // operators (include/lstm.h): argument checks, then the launches.
+#include <math.h>
+
 #include "attend_common.hpp"
 #include "internal.hpp"
 #include "seq_internal.hpp"
@@ -17,7 +19,7 @@ static int64_t esize_of(int dtype) { return dtype == LSTM_F32 ? 4 : 2; }
 static int embed_plan(const lstm_embed_shape* s, EmbedPlan* p) {
   if (!s) return LSTM_ERR_NULL;
   if (s->N < 0 || s->V < 0 || s->D < 0 || s->ld_table < s->D || s->ld_out < s->D || s->padding < -1 ||
-      s->padding >= (s->V > 0 ? s->V : 1))
+      s->padding >= (s->V > 0 ? s->V : 1) || !(fabsf(s->scale) <= 3.4028234e38f))
     return LSTM_ERR_DIMS;
   if (!dtype_ok(s->dtype) || !id_ok(s->id_type)) return LSTM_ERR_DTYPE;
   const int64_t lim = (int64_t)1 << 26, far = (int64_t)1 << 36;  // row strides: offsets fit 63 bits

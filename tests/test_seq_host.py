@@ -102,3 +102,11 @@ def test_scales_whose_exponents_overflow(lstm):
         assert (L.lstm_attend_query(ctypes.byref(s), ctypes.byref(n), ctypes.byref(k)) == -2) != ok
         s = lstm.LogprobShape(4, 9, 9, 9, scale, 3, 0, 1)
         assert (L.lstm_logprob_query(ctypes.byref(s), ctypes.byref(n)) == -2) != ok
+
+
+def test_embedding_scales_are_finite(lstm):
+    """An infinite or NaN scale would make NaN of the rows that are zeros by definition."""
+    L, n = lstm.lib(), ctypes.c_size_t(0)
+    for scale, ok in ((0.0, True), (-1.5, True), (float("inf"), False), (float("-inf"), False), (float("nan"), False)):
+        s = lstm.EmbedShape(4, 9, 8, 8, 8, -1, scale, 0, 1)
+        assert (L.lstm_embed_query(ctypes.byref(s), ctypes.byref(n)) == -2) != ok
