@@ -50,6 +50,27 @@ def test_gradients_over_thousands_of_keys(lstm, dt, size):
     run(lstm, dt, size)
 
 
+@pytest.mark.parametrize("dt,dout", [("f32", 1.0), ("bf16", 1.0), ("f16", 1.0), ("f16", 8000.0)])
+@pytest.mark.parametrize("size", [(5, 200, 4, 6, 2, 64), (40, 150, 40, 8, 4, 128), (130, 90, 3, 2, 2, 40)])
+def test_gradients_of_ragged_and_masked_keys(lstm, dt, dout, size):
+    """Lengths from none to all, holes, a sequence whose mask leaves nothing; NaN in every place that is no key."""
+    print(f"case: attention gradients, masked, {dt} {size} dout {dout}", flush=True)
+    Tq, Tk, B, Hq, Hk, D = size
+    rng = np.random.default_rng(Tk)
+    x, x64 = inputs(dt, *size, dout=dout)
+    length, mask = rng.integers(0, Tk + 1, B), rng.random((B, Tk)) < 0.8
+    length[0], length[1], mask[2] = Tk, 0, False
+    gone = torch.from_numpy(~(mask & (np.arange(Tk) < length[:, None]))).T
+    k, v = x[1].clone(), x[2].clone()
+    k[gone], v[gone] = float("nan"), float("nan")
+    q, k, v, g = (t.cuda() for t in (x[0], k, v, x[3]))
+    n, holes = torch.from_numpy(length.astype(np.int32)).cuda(), torch.from_numpy(mask).cuda()
+    m = lstm.Attention(Tq, Tk, B, Hq, Hk, D, code(lstm, dt))
+    o, _ = m.forward(q, k, v, n, holes)
+    got = dict(zip(("o", "dq", "dk", "dv"), (host(t) for t in (o, *m.backward(g, q, k, v, n, holes)))))
+    ab.check(dt, got, *x64, m.shape.scale, length, mask)
+
+
 @pytest.mark.parametrize("dout", [3e-4, 12000.0])
 @pytest.mark.parametrize("size", [(32, 16, 1, 1, 1, 128), (60, 48, 3, 4, 2, 64), (40, 300, 20, 8, 8, 192), (34, 70, 20, 8, 8, 256),
                                   (5, 33, 2, 2, 1, 250), (600, 90, 1, 3, 3, 128)])
