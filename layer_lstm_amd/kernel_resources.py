@@ -6,7 +6,8 @@ Compiles the kernel sources for gfx950 with the library's flags plus
 -Rpass-analysis=kernel-resource-usage and -save-temps (device code only, in a
 temporary folder; liblstm.so is not touched) and prints, for every kernel
 instance whose demangled name contains one of the --match strings (default:
-the instances the four workloads of layer_lstm_amd/synth.py launch):
+the instances the four workloads of layer_lstm_amd/synth.py launch; those of
+the sequence-to-sequence operators: --match attend_ embed_ logprob_):
 
   - VGPRs, AGPRs, SGPRs, SGPRs spilled (to VGPR lanes), VGPRs spilled and
     scratch bytes per lane, as the compiler reports them;
@@ -39,7 +40,8 @@ sys.path.insert(0, ROOT)
 
 from layer_lstm_amd import build as _build  # noqa: E402
 
-SOURCES = ("recurrent.hip", "recurrent_bwd.hip", "recurrent_vec.hip", "gemm.hip")
+SOURCES = ("recurrent.hip", "recurrent_bwd.hip", "recurrent_vec.hip", "gemm.hip", "embed.hip", "logprob.hip",
+           "attend.hip", "attend_bwd_f32.hip", "attend_bwd_bf16.hip", "attend_bwd_f16.hip")
 # kernel instances of the four workloads (rocprofv3 names, profiles/kernels_*.txt)
 DEFAULT_MATCH = (
     "fwd_rec_kernel<unsigned short, 2, 16, 0, 8, 2, false>",   # bf16_T256_B256_I1024_H1024
@@ -65,7 +67,8 @@ def demangle(names):
             break
     if tool is None:
         return {n: n for n in names}
-    r = subprocess.run([tool], input="\n".join(names), capture_output=True, text=True)
+    # DF16_ (_Float16) is unknown to some demanglers, Dh (half) is not
+    r = subprocess.run([tool], input="\n".join(n.replace("DF16_", "Dh") for n in names), capture_output=True, text=True)
     out = r.stdout.splitlines()
     return dict(zip(names, out)) if len(out) == len(names) else {n: n for n in names}
 
@@ -178,12 +181,12 @@ def main():
                 mv = loop_moves(text, fn) if text else None
                 rows.append((src, name, r, mv))
     out = ["# register use of the path's kernels (compiler resource remarks, gfx950)", "",
-           "command:", "", "    python -m layer_lstm_amd.kernel_resources" +
-           (f" --out {a.out}" if a.out else ""), "",
+           "command:", "", "    python -m layer_lstm_amd.kernel_resources" + (f" --out {a.out}" if a.out else "") +
+           (" --match " + " ".join(a.match) if tuple(a.match) != DEFAULT_MATCH else ""), "",
            "per kernel: VGPRs AGPRs SGPRs | SGPRs spilled, VGPRs spilled, scratch bytes/lane | in the step loop, "
            "per-step path: readlane/writelane/scratch instructions; failure and stamp paths: the same", ""]
     for src, name, r, mv in sorted(rows, key=lambda x: (x[0], x[1])):
-        short = re.sub(r"\(lstm::.*$", "", name)
+        short = re.sub(r"\(.*$", "", name)
         short = short.replace("void lstm::", "").replace("unsigned short", "u16")
         short = re.sub(r"lstm::", "", short)
         if len(short) > 110:
