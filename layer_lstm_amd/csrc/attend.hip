@@ -17,8 +17,9 @@
 // Two kernels.  attend_fwd_kernel: four waves of 32 rows share each tile of
 // keys, double-buffered, one barrier a tile; the matrix products are the
 // bound (8 sequences, 32/8 heads of 128, 1024 x up to 4096 keys, bf16: 340-355
-// us, 980 TFLOP/s; 64 sequences, 16 heads of 64, 256 x 256: 36 us, 3.7 TB/s of
-// its rows).  attend_step_kernel: for few rows (one token of each sequence):
+// us, 980 TFLOP/s; 64 sequences, 16 heads of 64, 256 x 256: 36 us, 3.0 TB/s of
+// its valid rows and no unit's bound: matrix units 14 % busy, vector units 40 %,
+// each wave's loop at most four tiles).  attend_step_kernel: for few rows (one token of each sequence):
 // every wave walks over its own tiles with no barrier, the keys split over the
 // waves and over `splits` work-groups, joined at the end; the keys' and
 // values' bytes are the bound (see the kernel).

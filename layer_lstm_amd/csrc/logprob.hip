@@ -263,12 +263,15 @@ __device__ __forceinline__ void finish_row(const LogprobOut& o, int64_t n, Targe
 
 // A wave per (row, part): the fixed work (joins of sums and lists, threshold)
 // is paid once per wave and covered by the row's hundred and more logits per
-// lane.  (2049 rows of 10007 fp16 logits with 5 alternatives: 19 us; with a
-// work-group of four waves per row and its joins in LDS 25 us; 16 rows of
-// 131072 fp32 with 8, in 64 parts a row: 7 us and 4 for the join, with
-// work-groups 11 and 4.)  The arithmetic, about ten vector instructions a
-// logit with the exponential counting four, is as long as the memory for
-// 16-bit logits: 16384 rows of 32768 bf16 take 195-230 us, 4.7-5.5 TB/s.
+// lane.  (2049 rows of 10007 fp16 logits with 5 alternatives: 20 us, where a
+// work-group of four waves per row and its joins in LDS took a third more; 16
+// rows of 131072 fp32 with 8, in 64 parts a row: 7 us and 4 for the join, with
+// work-groups 11 and 4.)  A logit costs nine vector instructions with the
+// exponential: 16384 rows of 32768 bf16 take 200-235 us, 4.6-5.4 TB/s, the
+// vector units 65 % busy.  On the 2049
+// rows of 10007 the fixed work and the list double the instructions, two waves
+// a SIMD do not cover the wait for the loads, and neither memory nor the vector
+// units (41 %) are the bound.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits, const void* targets, int64_t N,
                                                                  int64_t V, int64_t ld, float scale, int top, int parts,
@@ -448,7 +451,8 @@ __global__ void __launch_bounds__(64) logprob_join_kernel(const T* logits, const
 // Gradient: a work-group per (row, chunk of kGradVecs vectors a thread); the
 // few elements that have a term of their own (the target, the alternatives)
 // are written again by the group that owns them.  One read and one write of
-// the logits are all it does: 16384 x 32768 bf16, 2.15 GB, 353-366 us, 6 TB/s.
+// the logits are all it moves: 16384 x 32768 bf16, 2.15 GB, 355-380 us, 5.9
+// TB/s, with the vector units 84 % busy beside the memory.
 constexpr int kGradVecs = 4;
 
 template <typename T, bool VEC>
