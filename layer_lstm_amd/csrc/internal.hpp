@@ -102,10 +102,6 @@ constexpr size_t kColStageLds = 80 * 1024;
 constexpr int kWaves = 4;
 constexpr int kRecThreads = 64 * kWaves;
 
-// Compute units (and index) of the current device; LSTM_ERR_DEVICE if it is
-// not a gfx950.
-int device_cus(int* cus, int* devp = nullptr);
-
 // Fill the plan for a shape; returns 0 or an LSTM_ERR_* code.
 // cap_div: the recurrences' grid may take cus / cap_div compute units.
 int make_plan(int64_t T, int64_t B, int64_t I, int64_t H, int dtype, Plan* p, int cap_div = 1);

@@ -23,7 +23,7 @@ static int g_fail_step = -1, g_misplace = 0;
 constexpr int kMaxDevices = 64;
 static bool g_spread_only[kMaxDevices];
 
-int device_cus(int* cus, int* devp) {
+int device_cus(int* cus, int* devp = nullptr) {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return LSTM_ERR_DEVICE;
   if (devp) *devp = dev;

@@ -26,7 +26,7 @@ static int embed_plan(const lstm_embed_shape* s, EmbedPlan* p) {
   if (s->N >= lim || s->V >= lim || s->D > ((int64_t)1 << 20) || s->ld_table >= far || s->ld_out >= far)
     return LSTM_ERR_UNSUPPORTED;
   int cus = 0;
-  const int rc = device_cus(&cus);
+  const int rc = device_cus(&cus, nullptr);
   if (rc != LSTM_OK) return rc;
   make_embed_plan(*s, p);
   return LSTM_OK;
@@ -43,7 +43,7 @@ static int logprob_plan(const lstm_logprob_shape* s, LogprobPlan* p) {
       (s->V > 0 && s->N >= ((int64_t)1 << 37) / s->V))
     return LSTM_ERR_UNSUPPORTED;
   int cus = 0;
-  const int rc = device_cus(&cus);
+  const int rc = device_cus(&cus, nullptr);
   if (rc != LSTM_OK) return rc;
   make_logprob_plan(*s, cus, p);
   return LSTM_OK;
@@ -98,7 +98,7 @@ static int attend_plan(const lstm_attend_shape* s, bool bwd, AttendPlan* p) {
       groups * ((s->Tk + 127) / 128) >= ((int64_t)1 << 24))
     return LSTM_ERR_UNSUPPORTED;
   int cus = 0;
-  const int rc = device_cus(&cus);
+  const int rc = device_cus(&cus, nullptr);
   if (rc != LSTM_OK) return rc;
   make_attend_plan(*s, cus, p);
   return LSTM_OK;

@@ -10,6 +10,10 @@
 
 namespace lstm {
 
+// Compute units (and index) of the current device; LSTM_ERR_DEVICE if it is
+// not a gfx950 (lstm_api.hip).
+int device_cus(int* cus, int* devp);
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Elements of 16 bytes of storage type T.
