@@ -421,12 +421,12 @@ def _on_device(index, *tensors):
 def _row_stride(name, x, width):
     """Elements between the rows of x [n, width], which the kernels take to be
     at least width (the stride of one row alone means nothing)."""
-    if x.shape[0] <= 1:
-        return width
     st = x.stride(0)
-    if st < width:
+    if st >= width:
+        return st
+    if x.shape[0] > 1:
         raise ValueError(f"{name}: rows {st} elements apart, at least {width} (an expanded tensor has to be copied)")
-    return st
+    return width
 
 
 def _buffer(shape, dtype, device, stream):
@@ -441,7 +441,7 @@ def _buffer(shape, dtype, device, stream):
 def _stream_on(index, stream):
     if torch.cuda.current_device() != index or (stream is not None and stream.device_index != index):
         raise ValueError(f"cuda:{index} has to be the current device, and the stream's")
-    return _stream(stream)
+    return _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _workspace(fn, name, shape, device):

@@ -32,6 +32,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(lstm, "_lib", fake)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(lstm, "_stream", lambda stream: 0)
+    monkeypatch.setattr(lstm, "_raw_stream", None)
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
     return lstm, fake.launches
 
