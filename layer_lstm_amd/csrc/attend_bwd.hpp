@@ -14,9 +14,9 @@
 // keys, bf16: dq 470 us, 1090 TFLOP/s; dk and dv 750 us, 910 TFLOP/s.  At 64
 // sequences, 16 heads of 64, 256 x 256 no unit is (dq 52 us, dk and dv 62;
 // matrix units 15 and 18 % busy): the waves wait 40 % of their cycles for rows
-// and barriers in loops of a few tiles.  In fp32, with few rows and keys (8 sequences, 6/3
-// heads of 80, 37 x 191), dq takes 24 us and dk, dv 16, a chain of a few
-// dependent tiles.
+// and barriers in loops of a few tiles.  In fp32, with few rows and keys (8
+// sequences, 6/3 heads of 80, 37 x 191), dq takes 24 us and dk, dv 16, a chain
+// of a few dependent tiles.
 #pragma once
 #include <type_traits>
 

@@ -268,10 +268,9 @@ __device__ __forceinline__ void finish_row(const LogprobOut& o, int64_t n, Targe
 // rows of 131072 fp32 with 8, in 64 parts a row: 7 us and 4 for the join, with
 // work-groups 11 and 4.)  A logit costs nine vector instructions with the
 // exponential: 16384 rows of 32768 bf16 take 200-235 us, 4.6-5.4 TB/s, the
-// vector units 65 % busy.  On the 2049
-// rows of 10007 the fixed work and the list double the instructions, two waves
-// a SIMD do not cover the wait for the loads, and neither memory nor the vector
-// units (41 %) are the bound.
+// vector units 65 % busy.  On the 2049 rows of 10007 the fixed work and the
+// list double the instructions, two waves a SIMD do not cover the wait for the
+// loads, and neither memory nor the vector units (41 %) are the bound.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const T* logits, const void* targets, int64_t N,
                                                                  int64_t V, int64_t ld, float scale, int top, int parts,
