@@ -272,6 +272,7 @@ int lstm_check_workspace(void* workspace, size_t workspace_bytes, void* stream);
  *   5 direction copies (LSTM_BIDIRECTIONAL: y joined, dy split)
  *   6 state copies of the T = 0 / B = 0 cases
  *   7 embedding   8 cross attention   9 log probabilities
+ *   10 linear attention   11 logit penalties   12 AdamW
  * lstm_timing_enable(1) also resets the totals.  lstm_timing_read() waits for
  * the recorded events and returns the total milliseconds and the launch
  * count of one kind.  Not thread-safe; timing adds a few microseconds per
@@ -452,6 +453,146 @@ int lstm_logprob_fwd(const lstm_logprob_shape* shape, const void* logits, const 
 int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const void* targets, const float* record,
                      const float* entropy, const void* top_ids, const float* dlogp, const float* dentropy,
                      const float* dtop, void* dlogits, void* stream);
+
+/* Linear attention with a decay for each head: a recurrent layer whose state is
+ * a matrix.  For each of B sequences and Hk key heads, Hq / Hk query heads
+ * reading each (query head h reads key head h / (Hq / Hk)),
+ *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale * q_t S_t,
+ *   a = exp(min(log_decay[key head], 0))
+ * from S_{-1} = state (NULL: zeros) to state_out = S_{T-1} (NULL: not wanted):
+ *   q, dq [T][B][Hq][D], k, dk [T][B][Hk][D], v, dv [T][B][Hk][Dv], o, dout
+ *     [T][B][Hq][Dv] at strides as those of lstm_attend_*; outputs' rows do not
+ *     overlap
+ *   log_decay [Hk] fp32, device memory (-inf: no memory; it is a constant of
+ *     the model and takes no gradient)
+ *   state, state_out, dstate, dstate0 [B][Hk][D][Dv] fp32, dense
+ * length (int32 [B], NULL = all steps; clamped to [0, T]): a step past a
+ * sequence's end holds the state and has o = 0 and no gradient; its rows of q,
+ * k, v and dout are not used, they may hold anything.  state_out may be state
+ * where T <= LSTM_LINATTN_STEP; otherwise they do not overlap.
+ * Gradients: with R_t = a R_{t+1} + scale q_t dout_t^T and a R_T standing for
+ * dstate (NULL: zeros), the gradient of state_out,
+ *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate0 = a R_0
+ * (dstate0 NULL: not wanted); nothing of the forward call is needed.
+ * Rows of 16-bit types are multiplied as they are; q . k (times powers of a),
+ * S and R are rounded to the type as operands of the matrix cores (in fp16
+ * times a power of two, so that they neither overflow nor fall among the
+ * denormals), and summed, kept and handed over in fp32.  A step that is not
+ * finite may also reach the outputs of the 31 steps before it.
+ * Any D, Dv in [1, 256]; scale and 1 / scale finite and not 0; T < 2^26, B, Hq <
+ * 2^20; rows of whole aligned 16-byte chunks (t stride included) are the fast
+ * case. */
+#define LSTM_LINATTN_STEP 8
+typedef struct {
+  int64_t T, B, Hq, Hk, D, Dv;
+  lstm_stride q, k, v, o;
+  lstm_stride dout, dq, dk, dv; /* lstm_linattn_bwd only */
+  float scale;
+  int32_t dtype;
+} lstm_linattn_shape;
+/* Workspaces of the two calls (256-byte aligned, opaque, no state between
+ * calls; 0 bytes: NULL). */
+int lstm_linattn_query(const lstm_linattn_shape* shape, size_t* fwd_bytes, size_t* bwd_bytes);
+int lstm_linattn_fwd(const lstm_linattn_shape* shape, const void* q, const void* k, const void* v,
+                     const float* log_decay, const void* length, const float* state, void* workspace,
+                     size_t workspace_bytes, void* o, float* state_out, void* stream);
+int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const void* q, const void* k, const void* v,
+                     const float* log_decay, const void* length, const float* state, const float* dstate,
+                     void* workspace, size_t workspace_bytes, void* dq, void* dk, void* dv, float* dstate0,
+                     void* stream);
+
+/* Penalties, biases and masks on N rows of V logits before a token is chosen
+ * (row strides ld of logits and ld_out of out, >= V).  With c = how often v
+ * occurs among row n's tokens so far, history(n, t) for t < history_length[n],
+ *   x = logits[n][v]
+ *   c > 0:  x = x > 0 ? x / repetition[n] : x * repetition[n]
+ *           x = x - (presence[n] + frequency[n] * c)
+ *   x = x + bias[n * ld_bias + v]                 (ld_bias 0: one row for all)
+ *   x = -inf where bit v % 32 of mask[n * ld_mask + v / 32] is 0
+ *   out[n][v] = x
+ * in fp32, rounded once to the storage type (beyond its range: +-inf).  A
+ * masked logit is -inf whatever it was; a NaN that is not masked stays one.
+ * history(n, t): element n * history_n + t * history_t (strides >= 0) of ids of
+ * id_type, so [N][L] and time-major [L][N] alike; ids outside [0, V) are
+ * nobody's.  history_length: int32 [N], clamped to [0, L], NULL = L.
+ * repetition (> 0; 1 is none), presence, frequency: fp32 [N], NULL = none;
+ * with none of the three the history is not read.  bias: fp32, NULL = none;
+ * ld_bias 0 or >= V.  mask: 32-bit words, NULL = all allowed, ld_mask >=
+ * ceil(V / 32).  out may be logits itself (ld = ld_out).  N < 2^24, V < 2^30,
+ * N V < 2^37, L < 2^31. */
+typedef struct {
+  int64_t N, V;
+  int64_t ld, ld_out;
+  int64_t L, history_n, history_t;
+  int64_t ld_bias, ld_mask;
+  int32_t dtype;
+  int32_t id_type;
+} lstm_penalty_shape;
+int lstm_penalty(const lstm_penalty_shape* shape, const void* logits, const void* history, const void* history_length,
+                 const float* repetition, const float* presence, const float* frequency, const float* bias,
+                 const uint32_t* mask, void* out, void* stream);
+
+/* One AdamW step over `count` tensors at once (decoupled weight decay):
+ *   g = scale * grad                                (scale: see control; else 1)
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, each operation rounded as it stands.  w is `master` where it is
+ * given, and param its rounding; else param.  t is shape->step, the number of
+ * the step (1 the first), or control->step.
+ *   param, grad [n]   storage type, dense, element-aligned (16-byte aligned
+ *                     tensors are the fast case); master [n] fp32 or NULL
+ *   m, v [n]          bits = 32: fp32
+ *                     bits = 8: e4m3 numbers, with m_scale, v_scale fp32
+ *                     [ceil(n / LSTM_ADAMW_BLOCK)]; m is number * scale and
+ *                     sqrt(v) is number * scale, of blocks of LSTM_ADAMW_BLOCK
+ *                     values; scale is the block's largest / 448, the numbers
+ *                     rounded to nearest even, a sqrt(v) over zero to at least
+ *                     2^-9.  A block of nothing above 2^-100 is held as zeros.
+ * States of zeros are the beginning.  The tensors of a call do not overlap.
+ * The tensors' descriptions are host memory, read during the call.  lr, eps >=
+ * 0, betas in [0, 1), weight_decay >= 0, step >= 1, n < 2^40, count < 2^20. */
+#define LSTM_ADAMW_BLOCK 256
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  double weight_decay;
+} lstm_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;   /* without control */
+  int32_t dtype;  /* of param and grad */
+  int32_t bits;   /* 32 or 8: of m and v */
+} lstm_adamw_shape;
+/* Device memory that lstm_adamw_norm writes and lstm_adamw_step reads: where
+ * steps are replayed from a graph, gradients held to a norm, or a step that
+ * overflowed is to be left out, nothing of that passes the host.  step counts
+ * the steps taken; the caller sets it (and skip) to begin, the rest is written. */
+typedef struct {
+  int64_t step;
+  float scale;      /* what gradients are multiplied by */
+  float norm;       /* of the gradients times unscale */
+  float rate, root; /* lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step) */
+  int32_t skip;     /* 1: the norm is not finite; lstm_adamw_step changes nothing */
+  int32_t reserved;
+} lstm_adamw_control;
+/* norm = unscale * sqrt(sum of grad^2) over all tensors, summed in fp64 in a
+ * fixed order; scale = unscale * min(1, max_norm / norm); a finite norm raises
+ * control->step by one.  max_norm > 0, INFINITY for none; unscale > 0 and
+ * finite (1 / the loss's scale).  Only grad and n of the tensors are read.
+ * Workspace: lstm_adamw_query() bytes, 256-byte aligned, no state between
+ * calls.  control: 8-byte aligned. */
+int lstm_adamw_query(const lstm_adamw_shape* shape, const lstm_adamw_tensor* tensors, int64_t count,
+                     size_t* workspace_bytes);
+int lstm_adamw_norm(const lstm_adamw_shape* shape, const lstm_adamw_tensor* tensors, int64_t count, double max_norm,
+                    double unscale, void* workspace, size_t workspace_bytes, lstm_adamw_control* control, void* stream);
+int lstm_adamw_step(const lstm_adamw_shape* shape, const lstm_adamw_tensor* tensors, int64_t count,
+                    const lstm_adamw_control* control, void* stream);
 
 /* The floor under a recurrence step, for measurement: runs the forward
  * recurrence's per-step exchange alone -- the step flags of the batch group,

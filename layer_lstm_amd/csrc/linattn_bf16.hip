@@ -1,0 +1,10 @@
+// linattn_bf16.hip -- linear attention by chunks, bf16 storage (linattn_common.hpp).
+#include <type_traits>
+
+#include "linattn_common.hpp"
+
+namespace lstm {
+hipError_t launch_linattn_bf16(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s) {
+  return linattn_of<bf16_t>(a, dp, nw, dma, groups, s);
+}
+}  // namespace lstm

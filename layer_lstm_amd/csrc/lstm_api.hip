@@ -245,7 +245,7 @@ static int status_of(hipError_t e) {
 static bool misaligned(const void* ptr, int esize) { return ptr && ((uintptr_t)ptr % (uintptr_t)esize) != 0; }
 
 // ---- per-kernel event timing (lstm_timing_enable / lstm_timing_read) ----
-enum { kKinds = 10 };
+enum { kKinds = 13 };
 struct Pending { int kind; hipEvent_t a, b; };
 static bool g_timing_on = false;
 static std::vector<Pending> g_pending;

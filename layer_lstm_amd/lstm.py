@@ -9,6 +9,7 @@ this module raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,6 +30,8 @@ BIDIRECTIONAL = 8  # lstm_shape.flags: both directions of time, outputs side by 
 GATE_I, GATE_F, GATE_G, GATE_O = 0, 1, 2, 3
 I32, I64 = 0, 1  # id_type of token ids
 MAX_TOP = 32  # LSTM_MAX_TOP
+LINATTN_STEP = 8  # LSTM_LINATTN_STEP: the most steps whose state may be moved on in place
+ADAMW_BLOCK = 256  # LSTM_ADAMW_BLOCK: values of an 8-bit state that share a scale
 F32, BF16, F16 = 0, 1, 2
 OK = 0
 STATUS = {0: "OK", -1: "ERR_NULL", -2: "ERR_DIMS", -3: "ERR_DTYPE", -4: "ERR_ALIGN",
@@ -43,10 +46,13 @@ EXPORTS = ("lstm_abi_version", "lstm_status_string", "lstm_query", "lstm_query_p
            "lstm_fwd_train_scratch", "lstm_bwd", "lstm_check_workspace", "lstm_timing_enable", "lstm_timing_read",
            "lstm_stamps_set", "lstm_probe_exchange", "lstm_probe_mfma_stage", "lstm_debug_inject", "lstm_stack_query",
            "lstm_stack_fwd_train", "lstm_stack_bwd", "lstm_embed_query", "lstm_embed_fwd", "lstm_embed_bwd",
-           "lstm_attend_query", "lstm_attend_fwd", "lstm_attend_bwd", "lstm_logprob_query", "lstm_logprob_fwd", "lstm_logprob_bwd")
+           "lstm_attend_query", "lstm_attend_fwd", "lstm_attend_bwd", "lstm_logprob_query", "lstm_logprob_fwd", "lstm_logprob_bwd",
+           "lstm_linattn_query", "lstm_linattn_fwd", "lstm_linattn_bwd", "lstm_penalty", "lstm_adamw_query",
+           "lstm_adamw_norm", "lstm_adamw_step")
 STAMP_WGS, STAMP_POINTS = 8, 6
 KERNEL_KINDS = ("input_projection", "forward_recurrence", "backward_recurrence", "dW_product",
-                "dx_product", "direction_copy", "state_copy", "embedding", "cross_attention", "log_probability")
+                "dx_product", "direction_copy", "state_copy", "embedding", "cross_attention", "log_probability",
+                "linear_attention", "penalty", "adamw")
 
 
 class Shape(ctypes.Structure):
@@ -79,6 +85,32 @@ class AttendShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("Tq", "Tk", "B", "Hq", "Hk", "D")] + \
                [(n, Stride) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")] + \
                [("mask_b", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class LinattnShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "B", "Hq", "Hk", "D", "Dv")] + \
+               [(n, Stride) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")] + \
+               [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class PenaltyShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("N", "V", "ld", "ld_out", "L", "history_n", "history_t", "ld_bias", "ld_mask")] + \
+               [("dtype", ctypes.c_int32), ("id_type", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "master", "m", "v", "m_scale", "v_scale")] + \
+               [("n", ctypes.c_int64), ("weight_decay", ctypes.c_double)]
+
+
+class AdamwShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + \
+               [("step", ctypes.c_int64), ("dtype", ctypes.c_int32), ("bits", ctypes.c_int32)]
+
+
+class AdamwControl(ctypes.Structure):  # in device memory
+    _fields_ = [("step", ctypes.c_int64)] + [(n, ctypes.c_float) for n in ("scale", "norm", "rate", "root")] + \
+               [("skip", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -124,7 +156,16 @@ for _n, _a in (("lstm_embed_query", [ctypes.POINTER(EmbedShape), ctypes.POINTER(
                ("lstm_attend_bwd", [ctypes.POINTER(AttendShape)] + [_P] * 9 + [ctypes.c_size_t] + [_P] * 4),
                ("lstm_logprob_query", [ctypes.POINTER(LogprobShape), ctypes.POINTER(ctypes.c_size_t)]),
                ("lstm_logprob_fwd", [ctypes.POINTER(LogprobShape)] + [_P] * 3 + [ctypes.c_size_t] + [_P] * 7),
-               ("lstm_logprob_bwd", [ctypes.POINTER(LogprobShape)] + [_P] * 10)):
+               ("lstm_logprob_bwd", [ctypes.POINTER(LogprobShape)] + [_P] * 10),
+               ("lstm_linattn_query", [ctypes.POINTER(LinattnShape)] + [ctypes.POINTER(ctypes.c_size_t)] * 2),
+               ("lstm_linattn_fwd", [ctypes.POINTER(LinattnShape)] + [_P] * 7 + [ctypes.c_size_t] + [_P] * 3),
+               ("lstm_linattn_bwd", [ctypes.POINTER(LinattnShape)] + [_P] * 9 + [ctypes.c_size_t] + [_P] * 5),
+               ("lstm_penalty", [ctypes.POINTER(PenaltyShape)] + [_P] * 10),
+               ("lstm_adamw_query", [ctypes.POINTER(AdamwShape), ctypes.POINTER(AdamwTensor), ctypes.c_int64,
+                                     ctypes.POINTER(ctypes.c_size_t)]),
+               ("lstm_adamw_norm", [ctypes.POINTER(AdamwShape), ctypes.POINTER(AdamwTensor), ctypes.c_int64,
+                                    ctypes.c_double, ctypes.c_double, _P, ctypes.c_size_t, _P, _P]),
+               ("lstm_adamw_step", [ctypes.POINTER(AdamwShape), ctypes.POINTER(AdamwTensor), ctypes.c_int64, _P, _P])):
     getattr(_lib, _n).restype = ctypes.c_int
     getattr(_lib, _n).argtypes = _a
 _lib.lstm_debug_inject.restype = ctypes.c_int
@@ -400,6 +441,7 @@ class Stack:
 
 # --- sequence-to-sequence operators -------------------------------------------
 _ID_TYPES = {torch.int64: I64, torch.int32: I32}
+_STORAGE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
 # A kernel that is given the address of host memory, or of another device's,
@@ -643,3 +685,276 @@ class LogProb:
         if rc != OK:
             raise LstmError(rc, "lstm_logprob_bwd")
         return self.dlogits
+
+
+class LinearAttention:
+    """Linear attention with a decay for each head (lstm_linattn_*) of T steps
+    of B sequences, with workspace and output buffers on the current device.
+    q [T, B, Hq, D], k [T, B, Hk, D], v [T, B, Hk, Dv] (any strides >= 0, the
+    last dimension contiguous; an expanded k or v gets the gradient of its
+    expanded form), log_decay fp32 [Hk], states fp32 [B, Hk, D, Dv], length:
+    int32 [B] steps of each sequence.  o, dq, dk, dv are dense."""
+
+    def __init__(self, T, B, Hq, Hk, D, Dv=None, dtype=F32, scale=None, device="cuda"):
+        Dv = D if Dv is None else Dv
+        self.T, self.B, self.Hq, self.Hk, self.D, self.Dv, self.dtype, self.device = T, B, Hq, Hk, D, Dv, dtype, device
+        rows = [Stride(B * h * d, h * d, d) for h, d in ((Hq, D), (Hk, D), (Hk, Dv), (Hq, Dv))]
+        q, k, v, o = rows
+        self.shape = LinattnShape(T, B, Hq, Hk, D, Dv, q, k, v, o, o, q, k, v,
+                                  float(max(D, 1) ** -0.5 if scale is None else scale), int(dtype))
+        nf, nb = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        rc = _lib.lstm_linattn_query(ctypes.byref(self.shape), ctypes.byref(nf), ctypes.byref(nb))
+        if rc != OK:
+            raise LstmError(rc, "lstm_linattn_query")
+        self._ref = ctypes.byref(self.shape)
+        self._dev = _device_index(device)
+        self.tdtype = torch_dtype(dtype)
+        self._fwd_bytes, self._bwd_bytes = nf.value, nb.value
+        self.workspace = torch.empty(self._fwd_bytes, dtype=torch.uint8, device=device)
+        self.o = torch.empty((T, B, Hq, Dv), dtype=self.tdtype, device=device)
+        self.state = self.dq = self.dk = self.dv = self.dstate = None
+
+    def _rows(self, name, s, x, H, D):
+        if x.dtype != self.tdtype or x.shape != (self.T, self.B, H, D) or (D > 1 and x.stride(3) != 1):
+            raise ValueError(f"{name}: {[self.T, self.B, H, D]} of {self.tdtype}, last dimension contiguous")
+        s.t, s.b, s.h = x.stride()[:3]
+
+    def _state(self, name, x):
+        if x is not None and (x.dtype != torch.float32 or x.shape != (self.B, self.Hk, self.D, self.Dv) or
+                              not x.is_contiguous()):
+            raise ValueError(f"{name}: float32 {[self.B, self.Hk, self.D, self.Dv]}, contiguous")
+
+    def _inputs(self, q, k, v, log_decay, state, length):
+        self._rows("q", self.shape.q, q, self.Hq, self.D)
+        self._rows("k", self.shape.k, k, self.Hk, self.D)
+        self._rows("v", self.shape.v, v, self.Hk, self.Dv)
+        if log_decay.dtype != torch.float32 or log_decay.shape != (self.Hk,) or not log_decay.is_contiguous():
+            raise ValueError(f"log_decay: float32 [{self.Hk}], contiguous")
+        self._state("state", state)
+        if length is not None and (length.dtype != torch.int32 or length.shape != (self.B,) or not length.is_contiguous()):
+            raise ValueError(f"length: int32 [{self.B}], contiguous")
+        _on_device(self._dev, q, k, v, log_decay, state, length)
+
+    def _forward(self, q, k, v, log_decay, state, length, out, stream):
+        rc = _lib.lstm_linattn_fwd(self._ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(length), _ptr(state),
+                                   _ptr(self.workspace), self._fwd_bytes, _ptr(self.o), _ptr(out),
+                                   _stream_on(self._dev, stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_linattn_fwd")
+
+    def forward(self, q, k, v, log_decay, state=None, length=None, stream=None):
+        """o [T, B, Hq, Dv] and the state after the last step (a buffer of its own: pass a copy of it as the next
+        call's `state`)."""
+        self._inputs(q, k, v, log_decay, state, length)
+        if self.state is None:
+            self.state = _buffer((self.B, self.Hk, self.D, self.Dv), torch.float32, self.device, stream)
+        if state is not None and state.numel() and state.data_ptr() == self.state.data_ptr():
+            raise ValueError("state: not the buffer that the new state is written to")
+        self._forward(q, k, v, log_decay, state, length, self.state, stream)
+        return self.o, self.state
+
+    def step(self, q, k, v, log_decay, state, length=None, stream=None):
+        """o [T, B, Hq, Dv] of at most LINATTN_STEP steps; `state` is moved on in place."""
+        if self.T > LINATTN_STEP:
+            raise ValueError(f"step: at most {LINATTN_STEP} steps")
+        self._inputs(q, k, v, log_decay, state, length)
+        self._forward(q, k, v, log_decay, state, length, state, stream)
+        return self.o
+
+    def backward(self, dout, q, k, v, log_decay, state=None, length=None, dstate=None, stream=None):
+        """dq, dk, dv and the gradient of `state`; dstate: the gradient of the state after the last step."""
+        self._inputs(q, k, v, log_decay, state, length)
+        self._rows("dout", self.shape.dout, dout, self.Hq, self.Dv)
+        self._state("dstate", dstate)
+        _on_device(self._dev, dout, dstate)
+        if self.dq is None:
+            if self._bwd_bytes > self.workspace.numel():
+                self.workspace = _buffer((self._bwd_bytes,), torch.uint8, self.device, stream)
+            self.dq = _buffer((self.T, self.B, self.Hq, self.D), self.tdtype, self.device, stream)
+            self.dk = _buffer((self.T, self.B, self.Hk, self.D), self.tdtype, self.device, stream)
+            self.dv = _buffer((self.T, self.B, self.Hk, self.Dv), self.tdtype, self.device, stream)
+            self.dstate = _buffer((self.B, self.Hk, self.D, self.Dv), torch.float32, self.device, stream)
+        if dstate is not None and dstate.numel() and dstate.data_ptr() == self.dstate.data_ptr():
+            raise ValueError("dstate: not the buffer that the gradient of the state before is written to")
+        rc = _lib.lstm_linattn_bwd(self._ref, _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(length),
+                                   _ptr(state), _ptr(dstate), _ptr(self.workspace), self.workspace.numel(),
+                                   _ptr(self.dq), _ptr(self.dk), _ptr(self.dv), _ptr(self.dstate),
+                                   _stream_on(self._dev, stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_linattn_bwd")
+        return self.dq, self.dk, self.dv, self.dstate
+
+
+class Penalty:
+    """Penalties for repeated tokens, biases and masks on N rows of V logits
+    (lstm_penalty), with an output buffer on the current device."""
+
+    def __init__(self, N, V, dtype=F32, device="cuda"):
+        self.N, self.V, self.dtype, self.device = N, V, dtype, device
+        self.shape = PenaltyShape(N, V, V, V, 0, 0, 0, 0, 0, int(dtype), I64)
+        self._ref = ctypes.byref(self.shape)
+        self._dev = _device_index(device)
+        self.tdtype = torch_dtype(dtype)
+        self.out = None
+
+    def forward(self, logits, history=None, length=None, repetition=None, presence=None, frequency=None, bias=None,
+                mask=None, out=None, stream=None):
+        """logits [N, V] changed by what its row says: history [N, L] of int32 or int64 ids (any strides >= 0: time-major
+        ids as ids.t()), the first length [N] (int32) of them counting; repetition, presence, frequency fp32 [N]; bias
+        fp32 [V] or [N, V]; mask int32 [N, >= ceil(V / 32)], bit v % 32 of word v / 32 zero = not allowed.  `out`: where
+        to (logits itself, say); None: the operator's own buffer."""
+        N, V, s = self.N, self.V, self.shape
+        if logits.dtype != self.tdtype or logits.shape != (N, V) or (V > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits: [{N}, {V}] of {self.tdtype}, rows contiguous")
+        s.ld = _row_stride("logits", logits, V)
+        if out is None:
+            if self.out is None:
+                self.out = _buffer((N, V), self.tdtype, self.device, stream)
+            out = self.out
+        elif out.dtype != self.tdtype or out.shape != (N, V) or (V > 1 and out.stride(1) != 1):
+            raise ValueError(f"out: [{N}, {V}] of {self.tdtype}, rows contiguous")
+        s.ld_out = _row_stride("out", out, V)
+        some = repetition is not None or presence is not None or frequency is not None
+        if some and history is None:
+            raise ValueError("history: the tokens that the penalties are for")
+        s.L = 0
+        if history is not None:
+            if history.dim() != 2 or history.shape[0] != N or history.dtype not in _ID_TYPES:
+                raise ValueError(f"history: [{N}, L] of int32 or int64")
+            s.L, s.history_n, s.history_t = history.shape[1], history.stride(0), history.stride(1)
+            s.id_type = _ID_TYPES[history.dtype]
+        if length is not None and (length.dtype != torch.int32 or length.shape != (N,) or not length.is_contiguous()):
+            raise ValueError(f"length: int32 [{N}], contiguous")
+        for name, x in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+            if x is not None and (x.dtype != torch.float32 or x.shape != (N,) or not x.is_contiguous()):
+                raise ValueError(f"{name}: float32 [{N}], contiguous")
+        if bias is not None:
+            if bias.dtype != torch.float32 or bias.shape not in ((V,), (N, V)) or (V > 1 and bias.stride(-1) != 1):
+                raise ValueError(f"bias: float32 [{V}] or [{N}, {V}], rows contiguous")
+            s.ld_bias = 0 if bias.dim() == 1 or N == 1 or bias.stride(0) == 0 else _row_stride("bias", bias, V)
+        words = (V + 31) // 32
+        if mask is not None:
+            if mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[0] != N or mask.shape[1] < words or \
+                    (words > 1 and mask.stride(1) != 1):
+                raise ValueError(f"mask: int32 [{N}, {words}], rows contiguous")
+            s.ld_mask = _row_stride("mask", mask, words)
+        _on_device(self._dev, logits, history, length, repetition, presence, frequency, bias, mask, out)
+        rc = _lib.lstm_penalty(self._ref, _ptr(logits), _ptr(history), _ptr(length), _ptr(repetition), _ptr(presence),
+                               _ptr(frequency), _ptr(bias), _ptr(mask), _ptr(out), _stream_on(self._dev, stream))
+        if rc != OK:
+            raise LstmError(rc, "lstm_penalty")
+        return out
+
+
+class AdamW:
+    """AdamW steps over `params` (contiguous tensors of one storage type on the
+    current device, which do not overlap), all of them in one launch
+    (lstm_adamw_*).  bits: 32 or 8, of the states m and v; 16-bit parameters
+    have an fp32 copy, `master`, unless master=False.  weight_decay: one number
+    or one for each parameter.  clip: the norm that the gradients are held to
+    (math.inf: none); it, or loss_scale (gradients are divided by it), puts the
+    number of the step on the device, leaves out steps whose gradients are not
+    finite, and is what a step captured into a graph needs.
+
+    The states of all tensors lie in one buffer each (m, v, master; 8 bits: of
+    torch.float8_e4m3fn, with m_scale and v_scale), tensor i's at
+    places[i]..., a multiple of ADAMW_BLOCK values.  lr may be changed between
+    steps."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, clip=None,
+                 loss_scale=None, master=None, device="cuda"):
+        self.params = list(params)
+        kinds = {p.dtype for p in self.params}
+        if len(kinds) != 1 or next(iter(kinds)) not in _STORAGE:
+            raise ValueError("params: tensors of one type, float32, bfloat16 or float16")
+        if bits not in (8, 32):
+            raise ValueError("bits: 8 or 32")
+        self.tdtype = kinds.pop()
+        self.lr, self.betas, self.eps, self.bits, self.device = lr, betas, eps, bits, device
+        self._dev = _device_index(device)
+        n = len(self.params)
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
+        if len(decay) != n:
+            raise ValueError(f"weight_decay: one number, or {n}")
+        if any(not p.is_contiguous() for p in self.params):
+            raise ValueError("params: contiguous tensors")
+        _on_device(self._dev, *self.params)
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in self.params if p.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("params: tensors that do not overlap (one was given twice?)")
+        self.places, end = [], 0
+        for p in self.params:
+            self.places.append(end)
+            end += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+        state = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        self.m, self.v = (torch.zeros(end, dtype=state, device=device) for _ in range(2))
+        self.m_scale = self.v_scale = self.master = None
+        if bits == 8:
+            self.m_scale, self.v_scale = (torch.zeros(end // ADAMW_BLOCK, dtype=torch.float32, device=device) for _ in range(2))
+        if self.tdtype != torch.float32 and master is not False:
+            self.master = torch.zeros(end, dtype=torch.float32, device=device)
+            for p, at in zip(self.params, self.places):
+                self.master[at : at + p.numel()].copy_(p.reshape(-1))
+        self._table = (AdamwTensor * n)()
+        each = self.m.element_size()
+        for t, p, at, w in zip(self._table, self.params, self.places, decay):
+            t.n, t.weight_decay = p.numel(), w
+            if t.n == 0:
+                continue
+            t.param = p.data_ptr()
+            t.m, t.v = self.m.data_ptr() + at * each, self.v.data_ptr() + at * each
+            if bits == 8:
+                t.m_scale, t.v_scale = (x.data_ptr() + at // ADAMW_BLOCK * 4 for x in (self.m_scale, self.v_scale))
+            if self.master is not None:
+                t.master = self.master.data_ptr() + at * 4
+        self.shape = AdamwShape(lr, betas[0], betas[1], eps, 0, _STORAGE[self.tdtype], bits)
+        self._ref = ctypes.byref(self.shape)
+        self.clip = self.loss_scale = self.control = self.workspace = None
+        if clip is not None or loss_scale is not None:
+            self.clip = math.inf if clip is None else float(clip)
+            self.loss_scale = 1.0 if loss_scale is None else float(loss_scale)
+            size = ctypes.c_size_t(0)
+            rc = _lib.lstm_adamw_query(self._ref, self._table, n, ctypes.byref(size))
+            if rc != OK:
+                raise LstmError(rc, "lstm_adamw_query")
+            self.workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
+            self.control = torch.zeros(ctypes.sizeof(AdamwControl) // 8, dtype=torch.int64, device=device)
+
+    def set_step(self, t):
+        """t steps have been taken (0 at the start)."""
+        self.shape.step = int(t)
+        if self.control is not None:
+            self.control[0] = int(t)
+
+    @property
+    def norm(self):
+        """The last step's gradient norm, a view of device memory (with clip or loss_scale)."""
+        return None if self.control is None else self.control.view(torch.float32)[3]
+
+    def step(self, grads, stream=None):
+        """One step by the gradients, one for each parameter (contiguous, of its shape and type)."""
+        params, table, dev, td = self.params, self._table, self._dev, self.tdtype
+        if len(grads) != len(params):
+            raise ValueError(f"grads: {len(params)} tensors")
+        for p, g, t in zip(params, grads, table):
+            if g.shape != p.shape or g.dtype != td or not g.is_contiguous() or g.get_device() != dev:
+                raise ValueError(f"grads: {list(p.shape)} of {td} on cuda:{dev}, contiguous")
+            t.grad = g.data_ptr()
+        s, st = self.shape, _stream_on(dev, stream)
+        s.lr, s.beta1, s.beta2, s.eps = self.lr, self.betas[0], self.betas[1], self.eps
+        control = None
+        if self.control is not None:
+            control = self.control.data_ptr()
+            rc = _lib.lstm_adamw_norm(self._ref, table, len(params), self.clip, 1.0 / self.loss_scale,
+                                      _ptr(self.workspace), self.workspace.numel(), control, st)
+            if rc != OK:
+                raise LstmError(rc, "lstm_adamw_norm")
+        elif torch.cuda.is_current_stream_capturing():
+            raise ValueError("a step in a graph needs clip (math.inf: none): its number has to be on the device")
+        else:
+            s.step += 1
+        rc = _lib.lstm_adamw_step(self._ref, table, len(params), control, st)
+        if rc != OK:
+            if control is None:
+                s.step -= 1
+            raise LstmError(rc, "lstm_adamw_step")
