@@ -83,8 +83,18 @@ __device__ __forceinline__ float log2_decay(const float* log_decay, int h) {
 // (1 where there is none, or it is not finite): operands in fp16 are scaled by
 // it, so that sums beyond 65504 and values among its denormals keep their bits.
 __device__ __forceinline__ float lift_of(float most) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+  auto from = [&](auto ctl) {
+    const uint32_t v = __float_as_uint(most);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, decltype(ctl)::value, 0xf, 0xf, false));
+  };
+  using std::integral_constant;
+  most = fmaxf(most, from(integral_constant<int, 0xB1>{}));   // quad_perm 1,0,3,2
+  most = fmaxf(most, from(integral_constant<int, 0x4E>{}));   // quad_perm 2,3,0,1
+  most = fmaxf(most, from(integral_constant<int, 0x124>{}));  // row_ror:4
+  most = fmaxf(most, from(integral_constant<int, 0x128>{}));  // row_ror:8
+  const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(most), __float_as_uint(most), false, false);
+  most = fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
+  most = fmaxf(most, other_half(most));
   const uint32_t e = __float_as_uint(most) >> 23;  // exponent (most >= 0)
   const uint32_t r = e == 0 || e == 255 ? 127u : 127u + 13u + 127u - e;
   return __uint_as_float(__builtin_amdgcn_readfirstlane((r < 1 ? 1u : r > 253 ? 253u : r) << 23));
@@ -95,8 +105,9 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Loads 32 rows of a tensor (row r at p + r st) into a tile at an LDS address
-// with NW waves: rows at or past `rows` and values past D become zeros.  DMA:
+// Loads a tensor's rows 0 .. `rows` - 1 (row r at p + r st) into rows `shift` ..
+// of a tile of 32 at an LDS address with NW waves; the tile's other rows and
+// values past D become zeros.  DMA:
 // straight into LDS (rows of whole 16-byte chunks, st >= D, 32 st below 2^31
 // bytes); else chunk by chunk through registers.
 template <typename T, int DP, int NW, bool DMA>
@@ -115,37 +126,47 @@ struct Rows32 {
       off[j] = c * 16 < D * (int)sizeof(T) ? (uint32_t)(r * (int)st * (int)sizeof(T) + c * 16) : kNoRow;
     }
   }
-  __device__ __forceinline__ void load(const T* p, int rows, uint32_t lds) const {
+  __device__ __forceinline__ void load(const T* p, int rows, int shift, uint32_t lds) const {
     if constexpr (DMA) {
       const int bytes = rows > 0 ? (int)(((rows - 1) * (int)st + D) * (int)sizeof(T)) : 0;
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) lds_dma16_at<false>(r, lds + (j * NW + w) * 1024, off[j], 0);
+      // (a row before the first: an offset below 0, past the descriptor's end)
+      for (int j = 0; j < kLoads; ++j)
+        lds_dma16_at<false>(r, lds + (j * NW + w) * 1024, off[j] - (uint32_t)(shift * (int)st * (int)sizeof(T)), 0);
     } else {
       typedef __attribute__((address_space(3))) u32x4_t lds_vec_t;
       for (int j = 0; j < kLoads; ++j) {
         const int i = (j * NW + w) * 64 + lane, r = i / TL::C, c = (i % TL::C) ^ TL::swizzle(r);
         u32x4_t v = {0, 0, 0, 0};
-        if (r < rows) v = load_chunk<T>(p + r * st, c * vec_of<T>(), D, whole != 0);
+        if (r >= shift && r - shift < rows) v = load_chunk<T>(p + (r - shift) * st, c * vec_of<T>(), D, whole != 0);
         *(lds_vec_t*)(uintptr_t)(lds + i * 16) = v;
       }
     }
   }
 };
 
-template <typename T, int DP, int NW> constexpr int lin_stage_bytes() {
-  return 2 * Tile<T, DP>::kBytes32 + Tile<T, 32 * NW>::kBytes32;
+constexpr int kAheadRows = 6, kAheadCols = 4;  // fragments read ahead of their products
+// What a launch does: the run (kOne: one head of keys a state, kSum: several),
+// or the segments' own sums alone, without rows a and outputs.
+enum { kOne = 0, kSum = 1, kState = 2 };
+template <typename T, int DP, int NW, int KIND> constexpr int lin_stage_bytes() {
+  return (KIND == kState ? 1 : 2) * Tile<T, DP>::kBytes32 + Tile<T, 32 * NW>::kBytes32;
 }
 // Stages of LDS: three where two work-groups of them fit a compute unit or
 // nothing is gained by fewer.
-template <typename T, int DP, int NW> constexpr int lin_stages() { return 3 * lin_stage_bytes<T, DP, NW>() <= 150 * 1024 ? 3 : 2; }
+template <typename T, int DP, int NW, int KIND> constexpr int lin_stages() {
+  return 3 * lin_stage_bytes<T, DP, NW, KIND>() <= 150 * 1024 ? 3 : 2;
+}
 
-template <typename T, int DP, int NW, bool DMA>
+template <typename T, int DP, int NW, bool DMA, int KIND>
 __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn_kernel(LinArgs args) {
   using TK = StateTile<T, DP>;
   using TV = Tile<T, 32 * NW>;
   constexpr bool kHalf = std::is_same<T, f16_t>::value;
-  constexpr int NST = lin_stages<T, DP, NW>(), kStage = lin_stage_bytes<T, DP, NW>();
+  constexpr int NST = lin_stages<T, DP, NW, KIND>(), kStage = lin_stage_bytes<T, DP, NW, KIND>();
+  constexpr bool state_only = KIND == kState;
+  constexpr int kAtK = state_only ? 0 : TK::kBytes32, kAtV = kAtK + TK::kBytes32;  // of a stage
   constexpr int NDT = DP / 32, PB = TK::PB, EB = vec_of<T>();
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -156,7 +177,6 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   while (which + 1 < args.runs && u >= args.run[which + 1].group0) ++which;
   const LinRun& x = args.run[which];
   u -= x.group0;
-  const bool state_only = args.state_only != 0;
   const int heads = state_only ? args.Hs : x.Ha;
   const int dvb = (int)(u % x.dv_blocks);
   u /= x.dv_blocks;
@@ -175,7 +195,7 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   int64_t r1 = r0 + args.seg_rows < end ? r0 + args.seg_rows : end;
   if (r1 < r0) r1 = r0;
   const int n_chunks = (int)((r1 - r0 + 31) >> 5);
-  const int rev = x.rev, gb = x.gb;
+  const int rev = x.rev, gb = KIND == kOne ? 1 : x.gb;
   const float ld2 = log2_decay(args.log_decay, hs);
   const int dv0 = dvb * 32 * NW, cols = x.DV - dv0;  // (cols > 0)
 
@@ -187,37 +207,36 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   const T* a0 = (const T*)x.a + b * x.as.b + h * x.as.h;
   const T* k0 = (const T*)x.k + b * x.ks.b + (int64_t)hs * gb * x.ks.h;
   const T* v0 = (const T*)x.v + b * x.vs.b + (int64_t)hs * gb * x.vs.h + dv0;
-  constexpr int kLoads = decltype(la)::kLoads + decltype(lk)::kLoads + decltype(lv)::kLoads;
+  constexpr int kLoads = (state_only ? 0 : decltype(la)::kLoads) + decltype(lk)::kLoads + decltype(lv)::kLoads;
 
   // the state this wave carries: tile dt, register i
-  const int my_dv = dv0 + 32 * w + (lane & 31);
+  const int64_t head = (int64_t)b * args.Hs + hs, state_size = (int64_t)x.DK * x.DV;
   f32x16_t S[NDT];
   {
-    const float* in = nullptr;
-    int64_t s_dk = x.s_dk, s_dv = x.s_dv;
+    const float* in = x.s_in ? x.s_in + head * state_size : nullptr;
+    int s_dk = (int)x.s_dk, s_dv = (int)x.s_dv;
     float by = x.in_by;
-    const int64_t head = (int64_t)b * args.Hs + hs;
     if (args.segs > 1) {
-      if (!state_only) {
-        in = x.seg + (head * args.segs + order) * ((int64_t)x.DK * x.DV);
-        s_dk = x.DV; s_dv = 1;
-        by = 1.f;
-      }
-    } else if (x.s_in) {
-      in = x.s_in + head * ((int64_t)x.DK * x.DV);
+      in = state_only ? nullptr : x.seg + (head * args.segs + order) * state_size;
+      s_dk = x.DV; s_dv = 1;
+      by = 1.f;
     }
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)in, 0, in ? (int)state_size * 4 : 0, 0x00020000);
+    const int dv = dv0 + 32 * w + (lane & 31);
 #pragma unroll
     for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int d = 32 * dt + TK::state_row(i, lane);
-        S[dt][i] = in && d < x.DK && my_dv < x.DV ? in[d * s_dk + my_dv * s_dv] * by : 0.f;
+        const uint32_t at = d < x.DK && dv < x.DV ? (uint32_t)(d * s_dk + dv * s_dv) * 4 : kNoRow;
+        S[dt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0)) * by;
       }
   }
   float lift = 1.f;  // fp16: S holds the state times this power of two
 
-  // weights of a whole chunk: of P (row j = reg_row, column i = lane), of V in
-  // the state's sum
+  // Weights of P (row j = reg_row, column i = lane) and of V in the state's sum.
+  // They count from the chunk's end forwards in time and from its beginning
+  // backwards, so a chunk of fewer than 32 steps lies at that end of its tiles.
   const int ri = lane & 31;
   float wp[16], wv[PB][EB];
 #pragma unroll
@@ -225,17 +244,13 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
     const int j = reg_row(i, lane), e = rev ? j - ri : ri - j;
     wp[i] = e < 0 ? 0.f : power(ld2, e);
   }
-  auto value_weights = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
-    for (int pb = 0; pb < PB; ++pb)
+  for (int pb = 0; pb < PB; ++pb)
 #pragma unroll
-      for (int e = 0; e < EB; ++e) {
-        const int j = frag_row<T>(pb, e, lane), to = rev ? j + 1 : n - 1 - j;
-        wv[pb][e] = power(ld2, to < 0 ? 0 : to);
-      }
-  };
-  value_weights(32);
-
+    for (int e = 0; e < EB; ++e) {
+      const int j = frag_row<T>(pb, e, lane);
+      wv[pb][e] = power(ld2, rev ? j + 1 : 31 - j);
+    }
   // the state of this work-group reaches an output in fp32
   const bool state_out = x.s_out != nullptr && (state_only || h % x.ga == 0);
   f32x16_t O = zero16();
@@ -247,9 +262,10 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
     const uint32_t at = lds0 + slot * kStage;
     const int64_t row0 = r0 + 32 * (int64_t)(rev ? n_chunks - 1 - lc : lc);
     const int rows = (int)(r1 - row0 < 32 ? r1 - row0 : 32);
-    if (!state_only) la.load(a0 + row0 * x.as.t, rows, at);
-    lk.load(k0 + lg * x.ks.h + row0 * x.ks.t, rows, at + TK::kBytes32);
-    lv.load(v0 + lg * x.vs.h + row0 * x.vs.t, rows, at + 2 * TK::kBytes32);
+    const int shift = rev ? 0 : 32 - rows;
+    if constexpr (!state_only) la.load(a0 + row0 * x.as.t, rows, shift, at);
+    lk.load(k0 + lg * x.ks.h + row0 * x.ks.t, rows, shift, at + kAtK);
+    lv.load(v0 + lg * x.vs.h + row0 * x.vs.t, rows, shift, at + kAtV);
     if (++lg == gb) {
       lg = 0;
       ++lc;
@@ -264,7 +280,9 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   const float scale = args.scale;
   // O of the chunk whose rows begin at row0, times scale
   auto store = [&](int64_t row0) __attribute__((always_inline)) {
-    const int64_t row = row0 + ri;
+    const int shift = rev || r1 - row0 >= 32 ? 0 : 32 - (int)(r1 - row0);
+    const int64_t row = row0 + ri - shift;
+    const bool there = ri >= shift && row < r1;
     T* p = out + row * x.os.t;
     if ((x.whole & kWholeO) && out_cols >= 32) {
       if constexpr (sizeof(T) == 2) {
@@ -279,15 +297,15 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
           const auto s0 = __builtin_amdgcn_permlane32_swap(lo[0], hi[0], false, false);
           const auto s1 = __builtin_amdgcn_permlane32_swap(lo[1], hi[1], false, false);
           const u32x4_t q = {s0[0], s1[0], s0[1], s1[1]};
-          if (row < r1) *(u32x4_t*)(p + 16 * i + 8 * (lane >> 5)) = q;
+          if (there) *(u32x4_t*)(p + 16 * i + 8 * (lane >> 5)) = q;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (row < r1)
+          if (there)
             *(f32x4_t*)(p + reg_row(4 * i, lane)) = f32x4_t{O[4 * i] * scale, O[4 * i + 1] * scale, O[4 * i + 2] * scale, O[4 * i + 3] * scale};
       }
-    } else if (row < r1) {
+    } else if (there) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int d = reg_row(i, lane);
@@ -300,27 +318,26 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   for (int it = 0; it < iters; ++it) {
     // this iteration's rows have come; those of the next (NST = 3) may be on their way
     if (NST == 2 || it + 1 == iters) stage_barrier<0>();
-    else if (state_only) stage_barrier<kLoads - decltype(la)::kLoads>();
     else stage_barrier<kLoads>();
-    if (it > 0 && g == 0 && !state_only) {  // the chunk before
+    if (!state_only && it > 0 && g == 0) {  // the chunk before
       const int64_t row0 = r0 + 32 * (int64_t)(rev ? n_chunks - c : c - 1);
       store(row0);
     }
     if (it + NST - 1 < iters) load((it + NST - 1) % NST);
+    const int ln = tile_lane<true>(lane);  // (fragment addresses kept over the iterations would take the registers)
     const char* at = lds + (it % NST) * kStage;
-    const char *ta = at, *tk = at + TK::kBytes32, *tv = at + 2 * TK::kBytes32;
+    const char *ta = at, *tk = at + kAtK, *tv = at + kAtV;
     const int64_t row0 = r0 + 32 * (int64_t)(rev ? n_chunks - 1 - c : c);
     const int n = (int)(r1 - row0 < 32 ? r1 - row0 : 32);
-    if (n < 32) value_weights(n);  // (one chunk of a segment)
 
-    u32x4_t vf[PB];
-#pragma unroll
-    for (int pb = 0; pb < PB; ++pb) vf[pb] = TV::col_frag(tv, TK::KR * pb, w, lane);
-
-    if (!state_only) {
+    if constexpr (!state_only) {
       f32x16_t P = zero16();
       float undo = 1.f;
-      if (g == 0) {
+      // rows of a and k in turn, k-block by k-block
+      u32x4_t af;
+      Ahead<2 * TK::KB, kAheadRows> rows;
+      auto read_rows = [&](int f) __attribute__((always_inline)) { return TK::row_frag(f & 1 ? tk : ta, 0, f >> 1, ln); };
+      if (KIND == kOne || g == 0) {
         float by = 1.f;
         if constexpr (kHalf) {
           float most = 0.f;
@@ -332,10 +349,14 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
           undo = 1.f / (by * lift);
         }
         O = zero16();
-#pragma unroll
-        for (int kb = 0; kb < TK::KB; ++kb) {
-          const u32x4_t af = TK::row_frag(ta, 0, kb, lane), kf = TK::row_frag(tk, 0, kb, lane);
-          constexpr int kPer = 32 / (sizeof(T) == 2 ? 16 : 8);  // k-blocks of a tile of the state
+        constexpr int kPer = sizeof(T) == 2 ? 2 : 4;  // k-blocks of a tile of the state
+        rows.start(read_rows);
+        rows.run(read_rows, [&](int f, u32x4_t q) __attribute__((always_inline)) {
+          const int kb = f >> 1;
+          if (!(f & 1)) {
+            af = q;
+            return;
+          }
           u32x4_t sf;
           if constexpr (kHalf) {
             f32x16_t s;
@@ -345,17 +366,19 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
           } else {
             sf = TK::reg_frag(S[kb / kPer], kb % kPer);
           }
-          P = Mm<T>::mac(kf, af, P);
+          P = Mm<T>::mac(q, af, P);
           O = Mm<T>::mac(sf, af, O);
-        }
-        const int e = rev ? n - 1 - ri : ri + 1;
+        });
+        const int e = rev ? n - 1 - ri : ri + 1 - (32 - n);
         const float f = power(ld2, e < 0 ? 0 : e) * undo;
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[i] *= f;
       } else {
-#pragma unroll
-        for (int kb = 0; kb < TK::KB; ++kb)
-          P = Mm<T>::mac(TK::row_frag(tk, 0, kb, lane), TK::row_frag(ta, 0, kb, lane), P);
+        rows.start(read_rows);
+        rows.run(read_rows, [&](int f, u32x4_t q) __attribute__((always_inline)) {
+          if (f & 1) P = Mm<T>::mac(q, af, P);
+          else af = q;
+        });
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) P[i] *= wp[i];
@@ -372,7 +395,7 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
         }
       }
 #pragma unroll
-      for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(vf[pb], TK::reg_frag(P, pb), O);
+      for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(TV::col_frag(tv, TK::KR * pb, w, ln), TK::reg_frag(P, pb), O);
       if constexpr (kHalf) {
         const float un = 1.f / by;
 #pragma unroll
@@ -385,11 +408,11 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
     float f[PB][EB];
 #pragma unroll
     for (int pb = 0; pb < PB; ++pb) {
-      unpack<T>(vf[pb], f[pb]);
+      unpack<T>(TV::col_frag(tv, TK::KR * pb, w, ln), f[pb]);
 #pragma unroll
       for (int e = 0; e < EB; ++e) f[pb][e] *= wv[pb][e];
     }
-    float keep = g == 0 ? power(ld2, n) : 1.f;
+    float keep = KIND == kOne || g == 0 ? power(ld2, n) : 1.f;
     if constexpr (kHalf) {
       float most = 0.f;
 #pragma unroll
@@ -408,42 +431,30 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
     for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) S[dt][i] *= keep;
+    constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
+    u32x4_t vw[PB][kParts];
 #pragma unroll
     for (int pb = 0; pb < PB; ++pb) {
-      if constexpr (sizeof(T) == 4) {
-        const u32x4_t vw = pack<T>(f[pb]);
+      vw[pb][0] = pack<T>(f[pb]);
 #pragma unroll
-        for (int dt = 0; dt < NDT; ++dt) S[dt] = Mm<T>::mac(TK::col_frag_state(tk, TK::KR * pb, dt, lane), vw, S[dt]);
-      } else {
-        // what the first number has rounded away, and what that has
-        auto rest = [&](u32x4_t q) __attribute__((always_inline)) {
-          float r[EB];
-          unpack<T>(q, r);
+      for (int i = 1; i < kParts; ++i) {  // what the number before has rounded away
+        float r[EB];
+        unpack<T>(vw[pb][i - 1], r);
 #pragma unroll
-          for (int e = 0; e < EB; ++e) f[pb][e] -= r[e];
-          return pack<T>(f[pb]);
-        };
-        const u32x4_t hi = pack<T>(f[pb]), lo = rest(hi);
-        if (!kHalf && state_out) {
-          const u32x4_t last = rest(lo);
-#pragma unroll
-          for (int dt = 0; dt < NDT; ++dt) {
-            const u32x4_t kf = TK::col_frag_state(tk, TK::KR * pb, dt, lane);
-            S[dt] = Mm<T>::mac(kf, hi, S[dt]);
-            S[dt] = Mm<T>::mac(kf, lo, S[dt]);
-            S[dt] = Mm<T>::mac(kf, last, S[dt]);
-          }
-        } else {
-#pragma unroll
-          for (int dt = 0; dt < NDT; ++dt) {
-            const u32x4_t kf = TK::col_frag_state(tk, TK::KR * pb, dt, lane);
-            S[dt] = Mm<T>::mac(kf, hi, S[dt]);
-            S[dt] = Mm<T>::mac(kf, lo, S[dt]);
-          }
-        }
+        for (int e = 0; e < EB; ++e) f[pb][e] -= r[e];
+        vw[pb][i] = pack<T>(f[pb]);
       }
     }
-    if (n < 32) value_weights(32);
+    Ahead<PB * NDT, kAheadCols> kcols;
+    auto read_cols = [&](int i) __attribute__((always_inline)) { return TK::col_frag_state(tk, TK::KR * (i / NDT), i % NDT, ln); };
+    kcols.start(read_cols);
+    kcols.run(read_cols, [&](int i, u32x4_t kf) __attribute__((always_inline)) {
+      f32x16_t& s = S[i % NDT];
+      s = Mm<T>::mac(kf, vw[i / NDT][0], s);
+      if constexpr (kParts > 1) s = Mm<T>::mac(kf, vw[i / NDT][1], s);
+      if constexpr (kParts > 2)
+        if (state_out) s = Mm<T>::mac(kf, vw[i / NDT][2], s);
+    });
     if (++g == gb) {
       g = 0;
       ++c;
@@ -460,40 +471,49 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   }
   // the state after the run, or the segment's own sum
   float* to = nullptr;
-  int64_t s_dk = x.s_dk, s_dv = x.s_dv;
+  int s_dk = (int)x.s_dk, s_dv = (int)x.s_dv;
   float by = x.out_by;
-  const int64_t head = (int64_t)b * args.Hs + hs;
   if (state_only) {
-    to = x.seg + (head * args.segs + order) * ((int64_t)x.DK * x.DV);
+    to = x.seg + (head * args.segs + order) * state_size;
     s_dk = x.DV; s_dv = 1;
     by = 1.f;
   } else if (state_out && order == args.segs - 1) {
-    to = x.s_out + head * ((int64_t)x.DK * x.DV);
+    to = x.s_out + head * state_size;
   }
   if (to) {
     if constexpr (kHalf) by /= lift;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)to, 0, (int)state_size * 4, 0x00020000);
+    const int ln = tile_lane<true>(lane), dv = dv0 + 32 * w + (ln & 31);
 #pragma unroll
     for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int d = 32 * dt + TK::state_row(i, lane);
-        if (d < x.DK && my_dv < x.DV) to[d * s_dk + my_dv * s_dv] = S[dt][i] * by;
+        const int d = 32 * dt + TK::state_row(i, ln);
+        const uint32_t at = d < x.DK && dv < x.DV ? (uint32_t)(d * s_dk + dv * s_dv) * 4 : kNoRow;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[dt][i] * by), r, at, 0, 0);
       }
   }
 }
 
-template <typename T, int DP, int NW, bool DMA>
+template <typename T, int DP, int NW, bool DMA, int KIND>
 static hipError_t linattn_launch(const LinArgs& a, unsigned groups, hipStream_t s) {
-  const size_t bytes = (size_t)lin_stages<T, DP, NW>() * lin_stage_bytes<T, DP, NW>();
-  const hipError_t e = allow_lds<linattn_kernel<T, DP, NW, DMA>>(bytes);
+  const size_t bytes = (size_t)lin_stages<T, DP, NW, KIND>() * lin_stage_bytes<T, DP, NW, KIND>();
+  const hipError_t e = allow_lds<linattn_kernel<T, DP, NW, DMA, KIND>>(bytes);
   if (e != hipSuccess) return e;
   Timed timed(10, s);
-  linattn_kernel<T, DP, NW, DMA><<<dim3(groups), 64 * NW, bytes, s>>>(a);
+  linattn_kernel<T, DP, NW, DMA, KIND><<<dim3(groups), 64 * NW, bytes, s>>>(a);
   return hipGetLastError();
+}
+template <typename T, int DP, int NW, bool DMA>
+static hipError_t linattn_kind(const LinArgs& a, unsigned groups, hipStream_t s) {
+  if (a.state_only) return linattn_launch<T, DP, NW, DMA, kState>(a, groups, s);
+  int gb = 1;
+  for (int i = 0; i < a.runs; ++i) gb = a.run[i].gb > gb ? a.run[i].gb : gb;
+  return gb > 1 ? linattn_launch<T, DP, NW, DMA, kSum>(a, groups, s) : linattn_launch<T, DP, NW, DMA, kOne>(a, groups, s);
 }
 template <typename T, int DP, int NW>
 static hipError_t linattn_loads(const LinArgs& a, int dma, unsigned groups, hipStream_t s) {
-  return dma ? linattn_launch<T, DP, NW, true>(a, groups, s) : linattn_launch<T, DP, NW, false>(a, groups, s);
+  return dma ? linattn_kind<T, DP, NW, true>(a, groups, s) : linattn_kind<T, DP, NW, false>(a, groups, s);
 }
 template <typename T>
 static hipError_t linattn_of(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s) {
