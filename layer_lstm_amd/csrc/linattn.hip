@@ -7,27 +7,82 @@
 
 namespace lstm {
 
+// The instance for rows of DK and DV values: `few` work-groups take the one of
+// shorter iterations (two waves for 32 columns), which takes more work in all.
+static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
+  LinTile t;
+  t.dp = DK <= 64 ? 64 : DK <= 128 ? 128 : 256;
+  const bool f32 = dtype == LSTM_F32;
+  if (t.dp == 64) t = {64, 2, f32 || few ? 2 : 1};
+  else if (t.dp == 128) t = f32 || few || DV <= 64 ? LinTile{128, 2, 2} : LinTile{128, 4, 1};
+  else t = LinTile{256, f32 || DV <= 64 ? 2 : 4, 2};
+  return t;
+}
+
+// How a call's runs are cut into work-groups.  The heads alone, where they fill
+// the device: an iteration of a work-group is a chunk, and one work-group after
+// the other reads its sequence once.  Else first by columns (two work-groups a
+// head of more than 64), then the time axis into segments of four chunks at
+// least, whose own sums a launch before has to find (k and v read twice).
+// (8 sequences, 16 heads of 128, 4096 steps, bf16, forward, us: 128 work-groups
+// 226, two a head 180, four segments 202; 2 sequences, 4 heads: 202, 172, 16
+// segments of two a head 37, of one 43.)  Where the segments have many chunks to
+// go, whole heads (32768 steps, 32/8 heads, fp16: 235 and 372).  Heads that share
+// a state take one work-group (one update of the state for all of them) unless
+// that leaves compute units idle (8 sequences, 6/3 heads of 80, 191 steps, fp32:
+// 56 us, heads apart 32; 32 sequences, 32/8 heads, 1024 steps, fp16: 206, apart 260).
+static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int64_t (*sizes)[3], LinCall* c) {
+  const int64_t sets = s.B * s.Hk, chunks = (s.T + 31) / 32, most = chunks / 4 > 1 ? chunks / 4 : 1;
+  auto groups = [&](bool few) {
+    int64_t n = 0;
+    for (int i = 0; i < runs; ++i) {
+      const int64_t DK = sizes[i][0], DV = sizes[i][1], ga = sizes[i][2];
+      c->tile[i] = linattn_tile(DK, DV, s.dtype, few);
+      const int64_t blocks = (DV + 32 * c->tile[i].nw - 1) / (32 * c->tile[i].nw);
+      c->many[i] = ga > 1 && sets * blocks * most >= cus;
+      n += sets * blocks * (c->many[i] ? 1 : ga);
+    }
+    return n;
+  };
+  int64_t n = groups(false), segs = 1;
+  const int64_t full = c->tile[0].dp == 64 ? 2 * (int64_t)cus : cus;  // (work-groups of 64-value rows are half as large)
+  if (n > 0 && n < full) {
+    const bool long_runs = n * chunks > 16 * (int64_t)cus;
+    const int64_t fine = groups(true);
+    if (fine >= (c->tile[0].dp == 64 ? cus : full)) {
+      n = fine;
+    } else if (long_runs && c->tile[0].dp != 64) {
+      n = groups(false);
+      segs = (c->tile[0].dp == 256 ? 3 * full / 2 : 2 * full) / n;
+    } else {
+      n = fine;
+      segs = (runs > 1 ? 3 * full / 2 : full) / n;  // (the three runs of a backward do not end together)
+    }
+    if (segs > most) segs = most;
+    if (segs < 1) segs = 1;
+  }
+  c->seg_rows = (chunks + segs - 1) / segs * 32;
+  if (c->seg_rows == 0) c->seg_rows = 32;
+  c->segs = s.T > 0 ? (int)((s.T + c->seg_rows - 1) / c->seg_rows) : 1;
+}
+
 void make_linattn_plan(const lstm_linattn_shape& s, int cus, LinPlan* p) {
   p->dtype = s.dtype;
   p->cus = cus;
   p->step = s.T <= LSTM_LINATTN_STEP;
-  // Segments where the heads alone leave compute units idle: two work-groups a
-  // unit, of four chunks at least.
-  const int64_t heads = s.B * s.Hq * ((s.Dv + 127) / 128), chunks = (s.T + 31) / 32;
-  int64_t segs = 1;
-  if (heads > 0 && heads < cus) segs = 2 * (int64_t)cus / heads;
-  if (segs > chunks / 4) segs = chunks / 4;
-  if (segs < 1) segs = 1;
-  p->seg_rows = (chunks + segs - 1) / segs * 32;
-  if (p->seg_rows == 0) p->seg_rows = 32;
-  p->segs = s.T > 0 ? (int)((s.T + p->seg_rows - 1) / p->seg_rows) : 1;
-  p->seg_bytes = p->segs > 1 ? align256_seq((size_t)s.B * s.Hk * p->segs * s.D * s.Dv * 4) : 0;
-  p->total_fwd = p->step ? 0 : p->seg_bytes;
+  const int64_t G = s.Hk > 0 ? s.Hq / s.Hk : 1;
+  const int64_t fwd[1][3] = {{s.D, s.Dv, G}}, bwd[3][3] = {{s.Dv, s.D, G}, {s.Dv, s.D, 1}, {s.D, s.Dv, 1}};
+  plan_call(s, cus, 1, fwd, &p->fwd);
+  plan_call(s, cus, 3, bwd, &p->bwd);
+  const size_t states = (size_t)s.B * s.Hk * s.D * s.Dv * 4;
+  p->total_fwd = p->step || p->fwd.segs == 1 ? 0 : align256_seq(states * p->fwd.segs);
+  p->seg_bytes = p->bwd.segs == 1 ? 0 : align256_seq(states * p->bwd.segs);
   p->total_bwd = 3 * p->seg_bytes;
 }
 
 // The states at the segments' starts from the segments' own sums, in place:
-// a thread an element, in the order of the run's time.
+// a thread an element, in the order of the run's time, eight segments' sums
+// read ahead.
 __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
   const int which = blockIdx.z;
   const LinRun& x = args.run[which];
@@ -45,49 +100,60 @@ __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
   const int d = e / x.DV, c = e - d * x.DV;
   float S = x.s_in ? x.s_in[head * n + d * x.s_dk + c * x.s_dv] * x.in_by : 0.f;
   float* at = x.seg + head * args.segs * n + e;
-  for (int o = 0; o < args.segs; ++o) {
-    const int64_t seg = x.rev ? args.segs - 1 - o : o, r0 = seg * args.seg_rows;
-    int64_t rows = end - r0;
-    rows = rows < 0 ? 0 : rows < args.seg_rows ? rows : args.seg_rows;
-    const float own = o + 1 < args.segs ? at[(int64_t)o * n] : 0.f;
-    at[(int64_t)o * n] = S;
-    S = (rows == 0 ? S : S * __builtin_amdgcn_exp2f(ld2 * (float)rows)) + own;
+  constexpr int kAhead = 8;
+  for (int o0 = 0; o0 < args.segs; o0 += kAhead) {
+    float own[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) own[j] = o0 + j + 1 < args.segs ? at[(int64_t)(o0 + j) * n] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int o = o0 + j;
+      if (o < args.segs) {
+        const int64_t seg = x.rev ? args.segs - 1 - o : o, r0 = seg * args.seg_rows;
+        int64_t rows = end - r0;
+        rows = rows < 0 ? 0 : rows < args.seg_rows ? rows : args.seg_rows;
+        at[(int64_t)o * n] = S;
+        S = (rows == 0 ? S : S * __builtin_amdgcn_exp2f(ld2 * (float)rows)) + own[j];
+      }
+    }
   }
 }
 
-static int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-
-static hipError_t launch_runs(int dtype, const LinArgs& a, int dp, int nw, int dma, int64_t groups, hipStream_t s) {
+static hipError_t launch_runs(int dtype, const LinArgs& a, const LinTile& t, int many, int dma, int64_t groups, hipStream_t s) {
   if (groups == 0) return hipSuccess;
-  if (dtype == LSTM_F32) return launch_linattn_f32(a, dp, nw, dma, (unsigned)groups, s);
-  if (dtype == LSTM_BF16) return launch_linattn_bf16(a, dp, nw, dma, (unsigned)groups, s);
-  return launch_linattn_f16(a, dp, nw, dma, (unsigned)groups, s);
+  if (dtype == LSTM_F32) return launch_linattn_f32(a, t, many, dma, (unsigned)groups, s);
+  if (dtype == LSTM_BF16) return launch_linattn_bf16(a, t, many, dma, (unsigned)groups, s);
+  return launch_linattn_f16(a, t, many, dma, (unsigned)groups, s);
 }
 
-hipError_t launch_linattn(const LinPlan& p, LinArgs a, const int* dma, hipStream_t s) {
-  a.segs = p.segs;
-  a.seg_rows = p.seg_rows;
-  // runs of one kernel share a launch
-  for (int pass = p.segs > 1 ? 0 : 1; pass < 2; ++pass) {
+hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const int* dma, hipStream_t s) {
+  a.segs = c.segs;
+  a.seg_rows = c.seg_rows;
+  // runs of one instance and kind share a launch
+  for (int pass = a.segs > 1 ? 0 : 1; pass < 2; ++pass) {
+    auto alike = [&](int i, int j) {
+      return c.tile[i].dp == c.tile[j].dp && c.tile[i].nw == c.tile[j].nw && c.tile[i].ks == c.tile[j].ks && dma[i] == dma[j] &&
+             (pass == 0 || (c.many[i] == c.many[j] && (a.run[i].gb > 1) == (a.run[j].gb > 1)));
+    };
     bool done[3] = {false, false, false};
     for (int i = 0; i < a.runs; ++i) {
       if (done[i]) continue;
       LinArgs l = a;
       l.runs = 0;
       l.state_only = pass == 0;
-      l.segs_of_launch = pass == 0 ? p.segs - 1 : p.segs;
-      const int dp = padded(a.run[i].DK), nw = a.run[i].DV <= 64 ? 2 : 4;
+      l.segs_of_launch = pass == 0 ? a.segs - 1 : a.segs;
       int64_t groups = 0;
       for (int j = i; j < a.runs; ++j) {
-        if (done[j] || padded(a.run[j].DK) != dp || (a.run[j].DV <= 64 ? 2 : 4) != nw || dma[j] != dma[i]) continue;
+        if (done[j] || !alike(i, j)) continue;
         done[j] = true;
         LinRun& r = l.run[l.runs++];
         r = a.run[j];
-        r.dv_blocks = (r.DV + 32 * nw - 1) / (32 * nw);
-        r.group0 = groups;
-        groups += (int64_t)a.B * (pass == 0 ? a.Hs : r.Ha) * r.dv_blocks * l.segs_of_launch;
+        r.dv_blocks = (r.DV + 32 * c.tile[j].nw - 1) / (32 * c.tile[j].nw);
+        r.group0 = (uint32_t)groups;
+        const int64_t sets = (int64_t)a.B * a.Hs * l.segs_of_launch;
+        groups += (sets + 7) / 8 * 8 * r.dv_blocks * (pass == 0 || c.many[j] ? 1 : r.ga);
       }
-      const hipError_t e = launch_runs(p.dtype, l, dp, nw, dma[i], groups, s);
+      const hipError_t e = launch_runs(p.dtype, l, c.tile[i], c.many[i], dma[i], groups, s);
       if (e != hipSuccess) return e;
     }
     if (pass == 0 && a.B > 0 && a.Hs > 0) {

@@ -25,38 +25,66 @@
 namespace lstm {
 
 // A work-group walks over the chunks of a (sequence, head of a, block of 32 NW
-// columns of v); each of its NW waves owns 32 of the columns and the state's
-// DK x 32 part of them, in the accumulators of the matrix cores:
+// columns of v).  Its NW KS waves own 32 of the columns and a KS-th of the rows
+// of the state each, DK / KS x 32 in the accumulators of the matrix cores:
 //   P^T = K A^T            rows j down the registers, column i = lane: weighted
 //                          and rounded they are an operand as they stand
 //   O^T = S^T A^T + V^T P^T
 //   S  += K^T (V weighted)
-// Every wave computes P for itself: 8 of its 34 products (rows of 128 16-bit
-// values), which costs less than passing it round with two more barriers.
+// Every wave computes P for itself (over its own d: the waves of the same
+// columns have parts of O, which they add up through LDS; the next chunk's
+// barrier is theirs too).  Passing P round instead would cost two barriers for
+// 8 of a wave's 34 products (rows of 128 16-bit values, KS = 1).
 // The state as the operand of the first product of O^T has its k index down
 // the registers too; in 16 bits the columns of K are read in the order (bits 2
 // and 3 of the index exchanged) that leaves its rows in row_frag's order.
+//
+// Fragment addresses.  Rows are multiples of 128 bytes and tiles of 1 KB, so a
+// fragment's chunk is a lane's first one with bits flipped (the swizzle is an
+// exclusive or) and constants added: three registers hold a lane's part of all.
+typedef __attribute__((address_space(3))) u32x4_t lds_vec_t;
+typedef __attribute__((address_space(3))) uint32_t lds_word_t;
+
 template <typename T, int DP>
 struct StateTile : Tile<T, DP> {
   using TL = Tile<T, DP>;
-  // col_frag whose lanes hold the columns in the state's order
-  __device__ __forceinline__ static u32x4_t col_frag_state(const char* lds, int row0, int dt, int lane) {
+  static_assert(TL::C % 8 == 0, "rows of whole 128 bytes");
+  static constexpr int kRow = TL::C * 16;
+  // Tile::row_frag(row0 = 0, kb): this lane's first chunk, and a fragment from
+  // the tile's address plus it
+  __device__ __forceinline__ static uint32_t row_first(int lane) {
+    return (lane & 31) * kRow + (((lane >> 5) ^ TL::swizzle(lane & 31)) * 16);
+  }
+  __device__ __forceinline__ static u32x4_t row_at(uint32_t at, int kb) {
+    return *(lds_vec_t*)(uintptr_t)((at ^ (32 * (kb & 3))) + 128 * (kb >> 2));
+  }
+  // Tile::col_frag: the same; in 16 bits with `state`, the columns in the
+  // state's order
+  __device__ __forceinline__ static uint32_t col_first(int lane, bool state) {
     if constexpr (sizeof(T) == 2) {
-      u32x4_t out;
-      const int L = lane & 15, r = 4 * (lane >> 5) + (L >> 2), c = ((L & 1) << 1) | ((L >> 1) & 1);
-      const int d = 32 * dt + 16 * ((lane >> 4) & 1) + 4 * c;
-      const char* p = lds + row0 * TL::C * 16 + TL::chunk_at(r, d >> 3) + (d & 7) * 2;
+      const int L = lane & 15, r = 4 * (lane >> 5) + (L >> 2), c = state ? ((L & 1) << 1) | ((L >> 1) & 1) : L & 3;
+      return r * kRow + (((2 * ((lane >> 4) & 1) + (c >> 1)) ^ TL::swizzle(r)) * 16) + (c & 1) * 8;
+    } else {
+      const int r = 4 * (lane >> 5);
+      return r * kRow + ((((lane & 31) >> 2) ^ TL::swizzle(r)) * 16) + (lane & 3) * 4;
+    }
+  }
+  __device__ __forceinline__ static u32x4_t col_at(uint32_t at, int row0, int dt) {
+    u32x4_t out;
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t p = (at ^ (64 * (dt & 1))) + 128 * (dt >> 1) + row0 * kRow;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const s16x4_lds_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t*)(p + h * 8 * TL::C * 16));
-        const uint2 u = __builtin_bit_cast(uint2, v);
+        const uint2 u = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_t*)(uintptr_t)(p + h * 8 * kRow)));
         out[2 * h] = u.x;
         out[2 * h + 1] = u.y;
       }
-      return out;
     } else {
-      return TL::col_frag(lds, row0, dt, lane);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)  // swizzle(r + s) = swizzle(r) with these bits flipped, r a multiple of 4
+        out[s] = *(lds_word_t*)(uintptr_t)((at ^ ((s & 1) * 64 | (s >> 1) * 16)) + (row0 + s) * kRow + 128 * dt);
     }
+    return out;
   }
   // row of the state in register i of a tile
   __device__ __forceinline__ static int state_row(int i, int lane) {
@@ -106,38 +134,42 @@ __device__ __forceinline__ void stage_barrier() {
 }
 
 // Loads a tensor's rows 0 .. `rows` - 1 (row r at p + r st) into rows `shift` ..
-// of a tile of 32 at an LDS address with NW waves; the tile's other rows and
-// values past D become zeros.  DMA:
-// straight into LDS (rows of whole 16-byte chunks, st >= D, 32 st below 2^31
-// bytes); else chunk by chunk through registers.
-template <typename T, int DP, int NW, bool DMA>
+// of a tile of 32 at an LDS address with W waves; the tile's other rows and
+// values past D become zeros.  DMA: straight into LDS (rows of whole 16-byte
+// chunks, st >= D, 64 st below 2^31 bytes); else chunk by chunk through
+// registers.
+template <typename T, int DP, int W, bool DMA>
 struct Rows32 {
   using TL = Tile<T, DP>;
-  static constexpr int kLoads = 32 * TL::C / 64 / NW;  // loads of 1 KB a wave
-  static_assert(32 * TL::C / 64 % NW == 0, "every wave has as many");
+  static constexpr int kLoads = 32 * TL::C / 64 / W;  // loads of 1 KB a wave
+  static_assert(32 * TL::C / 64 % W == 0, "every wave has as many");
   int64_t st;
+  int row_bytes, all_bytes;  // from row to row, of 32 rows
   int D, whole, w, lane;
   uint32_t off[kLoads];  // DMA: byte offset of this lane's chunk of each load
   __device__ __forceinline__ void init(int64_t st_, int D_, int whole_, int w_, int lane_) {
     st = st_; D = D_; whole = whole_; w = w_; lane = lane_;
+    row_bytes = (int)st * (int)sizeof(T);
+    all_bytes = 31 * row_bytes + D * (int)sizeof(T);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
-      const int i = (j * NW + w) * 64 + lane, r = i / TL::C, c = (i % TL::C) ^ TL::swizzle(r);
-      off[j] = c * 16 < D * (int)sizeof(T) ? (uint32_t)(r * (int)st * (int)sizeof(T) + c * 16) : kNoRow;
+      const int i = (j * W + w) * 64 + lane, r = i / TL::C, c = (i % TL::C) ^ TL::swizzle(r);
+      off[j] = c * 16 < D * (int)sizeof(T) ? (uint32_t)(r * row_bytes + c * 16) : kNoRow;
     }
   }
   __device__ __forceinline__ void load(const T* p, int rows, int shift, uint32_t lds) const {
     if constexpr (DMA) {
-      const int bytes = rows > 0 ? (int)(((rows - 1) * (int)st + D) * (int)sizeof(T)) : 0;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000);
+      // (uniform, which the compiler does not see through the loop's selects)
+      const uint64_t at = (uint64_t)p;
+      const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+      const int bytes = __builtin_amdgcn_readfirstlane(all_bytes - (32 - rows) * row_bytes);
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, bytes, 0x00020000);
+      const uint32_t back = (uint32_t)(shift * row_bytes);  // (a row before the first: an offset below 0, past the end)
 #pragma unroll
-      // (a row before the first: an offset below 0, past the descriptor's end)
-      for (int j = 0; j < kLoads; ++j)
-        lds_dma16_at<false>(r, lds + (j * NW + w) * 1024, off[j] - (uint32_t)(shift * (int)st * (int)sizeof(T)), 0);
+      for (int j = 0; j < kLoads; ++j) lds_dma16_at<false>(r, lds + (j * W + w) * 1024, off[j] - back, 0);
     } else {
-      typedef __attribute__((address_space(3))) u32x4_t lds_vec_t;
       for (int j = 0; j < kLoads; ++j) {
-        const int i = (j * NW + w) * 64 + lane, r = i / TL::C, c = (i % TL::C) ^ TL::swizzle(r);
+        const int i = (j * W + w) * 64 + lane, r = i / TL::C, c = (i % TL::C) ^ TL::swizzle(r);
         u32x4_t v = {0, 0, 0, 0};
         if (r >= shift && r - shift < rows) v = load_chunk<T>(p + (r - shift) * st, c * vec_of<T>(), D, whole != 0);
         *(lds_vec_t*)(uintptr_t)(lds + i * 16) = v;
@@ -147,45 +179,56 @@ struct Rows32 {
 };
 
 constexpr int kAheadRows = 6, kAheadCols = 4;  // fragments read ahead of their products
-// What a launch does: the run (kOne: one head of keys a state, kSum: several),
-// or the segments' own sums alone, without rows a and outputs.
-enum { kOne = 0, kSum = 1, kState = 2 };
-template <typename T, int DP, int NW, int KIND> constexpr int lin_stage_bytes() {
-  return (KIND == kState ? 1 : 2) * Tile<T, DP>::kBytes32 + Tile<T, 32 * NW>::kBytes32;
-}
-// Stages of LDS: three where two work-groups of them fit a compute unit or
-// nothing is gained by fewer.
-template <typename T, int DP, int NW, int KIND> constexpr int lin_stages() {
-  return 3 * lin_stage_bytes<T, DP, NW, KIND>() <= 150 * 1024 ? 3 : 2;
-}
+// What a launch does: runs of one head of a and of k a work-group (kOne), of
+// several heads of k and v, whose products add up (kSum), of several heads of a,
+// which share a chunk's k, v and the state's update (kMany); or the segments' own sums
+// alone, without rows a and outputs (kState).
+enum { kOne = 0, kSum = 1, kMany = 2, kState = 3 };
+// LDS: stages of an iteration's tiles -- a, k and v; in kMany a alone, and two
+// pairs of k and v.  KS = 2: half of each wave's part of O, for the other wave
+// of its columns, twice.
+template <typename T, int DP, int NW, int KS, int KIND>
+struct LinLds {
+  static constexpr int kA = KIND == kState ? 0 : Tile<T, DP>::kBytes32;
+  static constexpr int kKV = Tile<T, DP>::kBytes32 + Tile<T, 32 * NW>::kBytes32;
+  static constexpr int kStage = KIND == kMany ? kA : kA + kKV;
+  static constexpr int kPass = KS == 2 && KIND != kState ? 2 * NW * KS * 2048 : 0;
+  static constexpr int kPairs = KIND == kMany ? 2 * kKV : 0;
+  // three stages where they fit a compute unit
+  static constexpr int kStages = 3 * kStage + kPairs + kPass <= 160 * 1024 ? 3 : 2;
+  static constexpr int kAtPairs = kStages * kStage, kAtPass = kAtPairs + kPairs, kBytes = kAtPass + kPass;
+  static_assert(kBytes <= 160 * 1024, "a compute unit's LDS");
+};
 
-template <typename T, int DP, int NW, bool DMA, int KIND>
-__global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn_kernel(LinArgs args) {
+template <typename T, int DP, int NW, int KS, bool DMA, int KIND>
+__global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 2) linattn_kernel(LinArgs args) {
   using TK = StateTile<T, DP>;
-  using TV = Tile<T, 32 * NW>;
-  constexpr bool kHalf = std::is_same<T, f16_t>::value;
-  constexpr int NST = lin_stages<T, DP, NW, KIND>(), kStage = lin_stage_bytes<T, DP, NW, KIND>();
-  constexpr bool state_only = KIND == kState;
-  constexpr int kAtK = state_only ? 0 : TK::kBytes32, kAtV = kAtK + TK::kBytes32;  // of a stage
-  constexpr int NDT = DP / 32, PB = TK::PB, EB = vec_of<T>();
+  using TV = StateTile<T, 32 * NW>;
+  using LL = LinLds<T, DP, NW, KS, KIND>;
+  constexpr bool kHalf = std::is_same<T, f16_t>::value, state_only = KIND == kState, kSplit = KS == 2 && !state_only;
+  constexpr int NST = LL::kStages;
+  constexpr int NDT = DP / 32 / KS, KB = TK::KB / KS, PB = TK::PB, EB = vec_of<T>();
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wave % NW, part = wave / NW;  // columns, rows of the state
 
-  // which run, and which (sequence, head, columns, segment) of it
-  int64_t u = blockIdx.x;
+  // Which run, and which (sequence, head, columns, segment) of it: the work-
+  // groups that read the same k and v (columns of a head, heads of a that share
+  // a state) are dealt to one XCD (work-groups go to the XCDs round robin).
+  uint32_t u = blockIdx.x;
   int which = 0;
   while (which + 1 < args.runs && u >= args.run[which + 1].group0) ++which;
   const LinRun& x = args.run[which];
   u -= x.group0;
-  const int heads = state_only ? args.Hs : x.Ha;
-  const int dvb = (int)(u % x.dv_blocks);
-  u /= x.dv_blocks;
-  const int h = (int)(u % heads);
-  u /= heads;
-  const int order = (int)(u % args.segs_of_launch);  // in the order of the run's time
-  const int b = (int)(u / args.segs_of_launch);
-  const int hs = state_only ? h : h / x.ga;
-  const int seg = x.rev ? args.segs - 1 - order : order;
+  const uint32_t share = x.dv_blocks * (KIND == kOne ? x.ga : 1), slot = (u >> 3) / share, member = (u >> 3) - slot * share;
+  const int dvb = (int)(member % x.dv_blocks), ha = (int)(member / x.dv_blocks);  // (ha: 0 but in kOne)
+  uint32_t set = slot * 8 + (u & 7);
+  if (set >= (uint32_t)args.B * args.Hs * args.segs_of_launch) return;
+  const int hs = (int)(set % args.Hs);
+  set /= args.Hs;
+  const int order = (int)(set % args.segs_of_launch);  // in the order of the run's time
+  const int b = (int)(set / args.segs_of_launch);
+  const int rev = x.rev, seg = rev ? args.segs - 1 - order : order;
   int64_t end = args.T;
   if (args.len) {
     const int64_t l = args.len[b];
@@ -194,20 +237,10 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
   const int64_t r0 = (int64_t)seg * args.seg_rows;
   int64_t r1 = r0 + args.seg_rows < end ? r0 + args.seg_rows : end;
   if (r1 < r0) r1 = r0;
-  const int n_chunks = (int)((r1 - r0 + 31) >> 5);
-  const int rev = x.rev, gb = KIND == kOne ? 1 : x.gb;
+  const int steps = (int)(r1 - r0), n_chunks = (steps + 31) >> 5;
+  const int heads = KIND == kSum || state_only ? x.gb : KIND == kMany ? x.ga : 1;  // iterations of a chunk
   const float ld2 = log2_decay(args.log_decay, hs);
   const int dv0 = dvb * 32 * NW, cols = x.DV - dv0;  // (cols > 0)
-
-  Rows32<T, DP, NW, DMA> la, lk;
-  Rows32<T, 32 * NW, NW, DMA> lv;
-  la.init(x.as.t, x.DK, x.whole & kWholeQ, w, lane);
-  lk.init(x.ks.t, x.DK, x.whole & kWholeK, w, lane);
-  lv.init(x.vs.t, cols < 32 * NW ? cols : 32 * NW, x.whole & kWholeV, w, lane);
-  const T* a0 = (const T*)x.a + b * x.as.b + h * x.as.h;
-  const T* k0 = (const T*)x.k + b * x.ks.b + (int64_t)hs * gb * x.ks.h;
-  const T* v0 = (const T*)x.v + b * x.vs.b + (int64_t)hs * gb * x.vs.h + dv0;
-  constexpr int kLoads = (state_only ? 0 : decltype(la)::kLoads) + decltype(lk)::kLoads + decltype(lv)::kLoads;
 
   // the state this wave carries: tile dt, register i
   const int64_t head = (int64_t)b * args.Hs + hs, state_size = (int64_t)x.DK * x.DV;
@@ -227,22 +260,24 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
     for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int d = 32 * dt + TK::state_row(i, lane);
+        const int d = 32 * (part * NDT + dt) + TK::state_row(i, lane);
         const uint32_t at = d < x.DK && dv < x.DV ? (uint32_t)(d * s_dk + dv * s_dv) * 4 : kNoRow;
         S[dt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0)) * by;
       }
   }
   float lift = 1.f;  // fp16: S holds the state times this power of two
 
-  // Weights of P (row j = reg_row, column i = lane) and of V in the state's sum.
-  // They count from the chunk's end forwards in time and from its beginning
-  // backwards, so a chunk of fewer than 32 steps lies at that end of its tiles.
+  // Weights of P (row j = reg_row, column i = lane; times scale) and of V in the
+  // state's sum.  They count from the chunk's end forwards in time and from its
+  // beginning backwards, so a chunk of fewer than 32 steps lies at that end of
+  // its tiles.
   const int ri = lane & 31;
+  const float scale = args.scale;
   float wp[16], wv[PB][EB];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int j = reg_row(i, lane), e = rev ? j - ri : ri - j;
-    wp[i] = e < 0 ? 0.f : power(ld2, e);
+    wp[i] = e < 0 ? 0.f : power(ld2, e) * scale;
   }
 #pragma unroll
   for (int pb = 0; pb < PB; ++pb)
@@ -251,105 +286,209 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
       const int j = frag_row<T>(pb, e, lane);
       wv[pb][e] = power(ld2, rev ? j + 1 : 31 - j);
     }
+  const float keep32 = power(ld2, 32);
+  // forwards every row's power is the chunk's full one but in the last chunk
+  const float since32 = power(ld2, rev ? 31 - ri : ri + 1) * scale;
   // the state of this work-group reaches an output in fp32
-  const bool state_out = x.s_out != nullptr && (state_only || h % x.ga == 0);
-  f32x16_t O = zero16();
-  const int iters = n_chunks * gb;
-  // iteration it: chunk it / gb (in the order of time), head it % gb of the keys
-  int lc = 0, lg = 0;  // of the next load
+  const bool state_out = x.s_out != nullptr && ha == 0;
+  // (this wave's rows of the state: k-blocks from part KB of a, tiles from part NDT of k)
+  static_assert(KB % 4 == 0 || KB == 2, "");
+  const uint32_t row_first = KB % 4 == 0 ? TK::row_first(lane) + 128 * (part * KB / 4) : TK::row_first(lane) ^ (64 * part);
+  uint32_t col_first = TK::col_first(lane, true);
+  if constexpr (sizeof(T) == 4) col_first += 128 * part * NDT;
+  else if constexpr (NDT % 2 == 0) col_first += 64 * part * NDT;
+  else col_first ^= 64 * part;
+  const uint32_t v_first = (TV::col_first(lane, false) + (sizeof(T) == 2 ? (w >> 1) * 128 : w * 128)) ^
+                           (sizeof(T) == 2 ? (w & 1) * 64 : 0);  // columns 32 w ..
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_t*)lds;
-  auto load = [&](int slot) __attribute__((always_inline)) {
-    const uint32_t at = lds0 + slot * kStage;
-    const int64_t row0 = r0 + 32 * (int64_t)(rev ? n_chunks - 1 - lc : lc);
-    const int rows = (int)(r1 - row0 < 32 ? r1 - row0 : 32);
-    const int shift = rev ? 0 : 32 - rows;
-    if constexpr (!state_only) la.load(a0 + row0 * x.as.t, rows, shift, at);
-    lk.load(k0 + lg * x.ks.h + row0 * x.ks.t, rows, shift, at + kAtK);
-    lv.load(v0 + lg * x.vs.h + row0 * x.vs.t, rows, shift, at + kAtV);
-    if (++lg == gb) {
+
+  // ---- loads: iteration it is chunk it / heads (in the order of time), head it % heads ----
+  Rows32<T, DP, NW * KS, DMA> la, lk;
+  Rows32<T, 32 * NW, NW * KS, DMA> lv;
+  la.init(x.as.t, x.DK, x.whole & kWholeQ, wave, lane);
+  lk.init(x.ks.t, x.DK, x.whole & kWholeK, wave, lane);
+  lv.init(x.vs.t, cols < 32 * NW ? cols : 32 * NW, x.whole & kWholeV, wave, lane);
+  const int64_t first_row = rev && n_chunks > 0 ? r0 + 32 * (int64_t)(n_chunks - 1) : r0, next = rev ? -32 : 32;
+  const T* a0 = (const T*)x.a + b * x.as.b + ((int64_t)hs * x.ga + ha) * x.as.h + first_row * x.as.t;
+  const T* k0 = (const T*)x.k + b * x.ks.b + (int64_t)hs * x.gb * x.ks.h + first_row * x.ks.t;
+  const T* v0 = (const T*)x.v + b * x.vs.b + (int64_t)hs * x.gb * x.vs.h + first_row * x.vs.t + dv0;
+  const int64_t a_head = KIND == kMany ? x.as.h : 0, k_head = KIND == kSum || state_only ? x.ks.h : 0,
+                v_head = KIND == kSum || state_only ? x.vs.h : 0;
+  // (32 rows of a tile that a descriptor reaches are below 2^30 bytes)
+  typedef typename std::conditional<DMA, int, int64_t>::type step_t;
+  const step_t a_next = (step_t)(next * x.as.t), k_next = (step_t)(next * x.ks.t), v_next = (step_t)(next * x.vs.t);
+  // A chunk's heads are taken from another one on in neighbouring work-groups:
+  // side by side in memory, all work-groups at the same one would keep to a part
+  // of the memory channels (32 heads of 128 in fp16, 4 a state, 32768 steps:
+  // 283 us at the same one, 235 so)
+  const int rot = heads > 1 ? (int)((uint32_t)(order + hs) % (uint32_t)heads) : 0;
+  constexpr int kLoadsA = state_only ? 0 : decltype(la)::kLoads, kLoadsKV = decltype(lk)::kLoads + decltype(lv)::kLoads;
+  int left = steps, lg = 0, lh = rot;  // of the next load: steps not loaded yet, heads of the chunk loaded, head
+  uint32_t l_at = lds0, l_kv = lds0 + LL::kAtPairs;
+  // steps of a chunk with `left` to go (backwards the last one, of fewer, is the first)
+  auto chunk_steps = [&](int left) __attribute__((always_inline)) { return rev ? ((left - 1) & 31) + 1 : left < 32 ? left : 32; };
+  auto load = [&]() __attribute__((always_inline)) {
+    const int rows = chunk_steps(left), shift = rev ? 0 : 32 - rows;
+    if constexpr (!state_only) la.load(KIND == kMany ? a0 + lh * a_head : a0, rows, shift, l_at);
+    if (KIND != kMany || lg == 0) {
+      const uint32_t kv = KIND == kMany ? l_kv : l_at + LL::kA;
+      const bool sum = KIND == kSum || state_only;
+      lk.load(sum ? k0 + lh * k_head : k0, rows, shift, kv);
+      lv.load(sum ? v0 + lh * v_head : v0, rows, shift, kv + TK::kBytes32);
+      if constexpr (KIND == kMany) l_kv = l_kv == lds0 + LL::kAtPairs ? l_kv + LL::kKV : lds0 + LL::kAtPairs;
+    }
+    l_at = l_at == lds0 + (NST - 1) * LL::kStage ? lds0 : l_at + LL::kStage;
+    if (KIND != kOne) lh = lh + 1 == heads ? 0 : lh + 1;
+    if (KIND == kOne || ++lg == heads) {
       lg = 0;
-      ++lc;
+      left -= rows;
+      a0 += a_next;
+      k0 += k_next;
+      v0 += v_next;
     }
   };
-#pragma unroll
-  for (int i = 0; i < NST - 1; ++i)
-    if (i < iters) load(i);
 
-  T* out = (T*)x.out + b * x.os.b + h * x.os.h + dv0 + 32 * w;
-  const int out_cols = cols - 32 * w;  // (may be below 0: no columns)
-  const float scale = args.scale;
-  // O of the chunk whose rows begin at row0, times scale
-  auto store = [&](int64_t row0) __attribute__((always_inline)) {
-    const int shift = rev || r1 - row0 >= 32 ? 0 : 32 - (int)(r1 - row0);
-    const int64_t row = row0 + ri - shift;
-    const bool there = ri >= shift && row < r1;
-    T* p = out + row * x.os.t;
-    if ((x.whole & kWholeO) && out_cols >= 32) {
+  // ---- stores ----
+  constexpr int kKeep = kSplit ? 8 : 16;  // registers of O that this wave stores
+  float keep_o[kKeep];
+  T* out = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha) * x.os.h + dv0 + 32 * w + (kSplit ? 16 * part : 0) +
+           (first_row + ri) * x.os.t;
+  const int64_t o_row = x.os.t, o_next = next * o_row;
+  int sh = rot, sg = 0;  // of the next store: head, heads of the chunk stored
+  const int out_cols = cols - 32 * w - (kSplit ? 16 * part : 0);  // (may be below 0: no columns)
+  const bool whole_o = (x.whole & kWholeO) && out_cols >= 2 * kKeep;
+  uint32_t pass = lds0 + LL::kAtPass;
+  // O of the iteration before, a chunk of n steps, to where `out` stands
+  auto store = [&](int n) __attribute__((always_inline)) {
+    const bool there = rev ? ri < n : ri >= 32 - n;
+    T* p = n < 32 && !rev ? out - (32 - n) * o_row : out;
+    if constexpr (KIND == kMany) p += sh * x.os.h;
+    if constexpr (kSplit) {
+      const uint32_t at = pass + (w + NW * (1 - part)) * 2048 + lane * 16;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float y[4];
+        unpack<float>(*(lds_vec_t*)(uintptr_t)(at + i * 1024), y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) keep_o[4 * i + j] += y[j];
+      }
+      pass = pass == lds0 + LL::kAtPass ? pass + NW * KS * 2048 : lds0 + LL::kAtPass;
+    }
+    if (whole_o) {
       if constexpr (sizeof(T) == 2) {
+        u32x4_t q[kKeep / 8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t lo[2], hi[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            lo[c] = pack2<T>(O[8 * i + 2 * c] * scale, O[8 * i + 2 * c + 1] * scale);
-            hi[c] = pack2<T>(O[8 * i + 4 + 2 * c] * scale, O[8 * i + 4 + 2 * c + 1] * scale);
-          }
-          const auto s0 = __builtin_amdgcn_permlane32_swap(lo[0], hi[0], false, false);
-          const auto s1 = __builtin_amdgcn_permlane32_swap(lo[1], hi[1], false, false);
-          const u32x4_t q = {s0[0], s1[0], s0[1], s1[1]};
-          if (there) *(u32x4_t*)(p + 16 * i + 8 * (lane >> 5)) = q;
+        for (int i = 0; i < kKeep / 8; ++i) {
+          const float* o = keep_o + 8 * i;
+          const auto s0 = __builtin_amdgcn_permlane32_swap(pack2<T>(o[0], o[1]), pack2<T>(o[4], o[5]), false, false);
+          const auto s1 = __builtin_amdgcn_permlane32_swap(pack2<T>(o[2], o[3]), pack2<T>(o[6], o[7]), false, false);
+          q[i] = u32x4_t{s0[0], s1[0], s0[1], s1[1]};
         }
-      } else {
+        if (there) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (there)
-            *(f32x4_t*)(p + reg_row(4 * i, lane)) = f32x4_t{O[4 * i] * scale, O[4 * i + 1] * scale, O[4 * i + 2] * scale, O[4 * i + 3] * scale};
+          for (int i = 0; i < kKeep / 8; ++i) *(u32x4_t*)(p + 16 * i + 8 * (lane >> 5)) = q[i];
+        }
+      } else if (there) {
+#pragma unroll
+        for (int i = 0; i < kKeep / 4; ++i) *(u32x4_t*)(p + reg_row(4 * i, lane)) = pack<float>(keep_o + 4 * i);
       }
     } else if (there) {
+#pragma unroll 1
+      for (int i = 0; i < kKeep; ++i) {
+        float o = 0.f;  // (registers cannot be indexed: a loop keeps this rare path small)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+        for (int j = 0; j < kKeep; ++j) o = j == i ? keep_o[j] : o;
         const int d = reg_row(i, lane);
-        if (d < out_cols) p[d] = Elem<T>::from_f(as_f32(O[i] * scale));
+        if (d < out_cols) p[d] = Elem<T>::from_f(o);
       }
+    }
+    if constexpr (KIND == kMany) sh = sh + 1 == heads ? 0 : sh + 1;
+    if (KIND != kMany || ++sg == heads) {
+      sg = 0;
+      out += o_next;
+    }
+  };
+  // O is complete: what this wave stores stays, the rest goes to the other
+  // wave of its columns
+  auto hand_over = [&](const f32x16_t& O) __attribute__((always_inline)) {
+    if constexpr (kSplit) {
+      const uint32_t at = pass + wave * 2048 + lane * 16;
+      float give[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        keep_o[i] = part ? O[8 + i] : O[i];
+        give[i] = part ? O[i] : O[8 + i];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) *(lds_vec_t*)(uintptr_t)(at + i * 1024) = pack<float>(give + 4 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) keep_o[i] = O[i];
     }
   };
 
-  int c = 0, g = 0;
-  for (int it = 0; it < iters; ++it) {
-    // this iteration's rows have come; those of the next (NST = 3) may be on their way
-    if (NST == 2 || it + 1 == iters) stage_barrier<0>();
-    else stage_barrier<kLoads>();
-    if (!state_only && it > 0 && g == 0) {  // the chunk before
-      const int64_t row0 = r0 + 32 * (int64_t)(rev ? n_chunks - c : c - 1);
-      store(row0);
+  const int iters = n_chunks * heads;
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i)
+    if (i < iters) load();
+
+  f32x16_t O = zero16();
+  float s_by = 1.f, undo = 1.f;       // fp16: of the state as an operand
+  u32x4_t s_op[KIND == kMany ? KB : 1];
+  // the state as the operand of k-block kb
+  auto state_operand = [&](int kb) __attribute__((always_inline)) {
+    constexpr int kPer = sizeof(T) == 2 ? 2 : 4;  // k-blocks of a tile of the state
+    if constexpr (kHalf) {
+      f32x16_t s;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[8 * (kb % kPer) + i] = S[kb / kPer][8 * (kb % kPer) + i] * s_by;
+      return TK::reg_frag(s, kb % kPer);
+    } else {
+      return TK::reg_frag(S[kb / kPer], kb % kPer);
     }
-    if (it + NST - 1 < iters) load((it + NST - 1) % NST);
-    const int ln = tile_lane<true>(lane);  // (fragment addresses kept over the iterations would take the registers)
-    const char* at = lds + (it % NST) * kStage;
-    const char *ta = at, *tk = at + kAtK, *tv = at + kAtV;
-    const int64_t row0 = r0 + 32 * (int64_t)(rev ? n_chunks - 1 - c : c);
-    const int n = (int)(r1 - row0 < 32 ? r1 - row0 : 32);
+  };
+  int togo = steps, g = 0, n_before = 0;
+  uint32_t u_at = lds0, u_kv = lds0 + LL::kAtPairs;
+  for (int it = 0; it < iters; ++it) {
+    const bool first = KIND == kOne || g == 0, last = KIND == kOne || g == heads - 1;
+    // this iteration's rows have come; those of the next (three stages) may be on their way
+    if (NST == 2 || it + 1 >= iters) stage_barrier<0>();
+    else if (KIND == kMany && !last) stage_barrier<kLoadsA>();
+    else stage_barrier<kLoadsA + kLoadsKV>();
+    if (!state_only && it > 0 && (KIND != kSum || first)) {
+      store(n_before);
+    }
+    if (it + NST - 1 < iters) load();
+    const uint32_t kv = KIND == kMany ? u_kv : u_at + LL::kA;
+    const uint32_t rows_at = u_at + row_first, keys_at = kv + row_first, cols_at = kv + col_first,
+                   v_at = kv + TK::kBytes32 + v_first;
+    const int n = chunk_steps(togo);
 
     if constexpr (!state_only) {
       f32x16_t P = zero16();
-      float undo = 1.f;
       // rows of a and k in turn, k-block by k-block
       u32x4_t af;
-      Ahead<2 * TK::KB, kAheadRows> rows;
-      auto read_rows = [&](int f) __attribute__((always_inline)) { return TK::row_frag(f & 1 ? tk : ta, 0, f >> 1, ln); };
-      if (KIND == kOne || g == 0) {
-        float by = 1.f;
+      Ahead<2 * KB, kAheadRows> rows;
+      auto read_rows = [&](int f) __attribute__((always_inline)) { return TK::row_at(f & 1 ? keys_at : rows_at, f >> 1); };
+      if (KIND != kSum || first) {
         if constexpr (kHalf) {
-          float most = 0.f;
+          if (first) {
+            float most = 0.f;
 #pragma unroll
-          for (int dt = 0; dt < NDT; ++dt)
+            for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(S[dt][i]));
-          by = lift_of(most);
-          undo = 1.f / (by * lift);
+              for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(S[dt][i]));
+            s_by = lift_of(most);
+            undo = 1.f / s_by / lift;
+          }
+        }
+        if constexpr (KIND == kMany) {  // kept over the chunk's heads
+          if (first) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) s_op[kb] = state_operand(kb);
+          }
         }
         O = zero16();
-        constexpr int kPer = sizeof(T) == 2 ? 2 : 4;  // k-blocks of a tile of the state
         rows.start(read_rows);
         rows.run(read_rows, [&](int f, u32x4_t q) __attribute__((always_inline)) {
           const int kb = f >> 1;
@@ -357,20 +496,16 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
             af = q;
             return;
           }
-          u32x4_t sf;
-          if constexpr (kHalf) {
-            f32x16_t s;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[8 * (kb % kPer) + i] = S[kb / kPer][8 * (kb % kPer) + i] * by;
-            sf = TK::reg_frag(s, kb % kPer);
-          } else {
-            sf = TK::reg_frag(S[kb / kPer], kb % kPer);
-          }
+          const u32x4_t sf = KIND == kMany ? s_op[kb] : state_operand(kb);
           P = Mm<T>::mac(q, af, P);
           O = Mm<T>::mac(sf, af, O);
         });
-        const int e = rev ? n - 1 - ri : ri + 1 - (32 - n);
-        const float f = power(ld2, e < 0 ? 0 : e) * undo;
+        float f = since32;
+        if (n < 32) {
+          const int e = rev ? n - 1 - ri : ri + 1 - (32 - n);
+          f = power(ld2, e < 0 ? 0 : e) * scale;
+        }
+        if constexpr (kHalf) f *= undo;
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[i] *= f;
       } else {
@@ -395,79 +530,92 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
         }
       }
 #pragma unroll
-      for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(TV::col_frag(tv, TK::KR * pb, w, ln), TK::reg_frag(P, pb), O);
+      for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(TV::col_at(v_at, TK::KR * pb, 0), TK::reg_frag(P, pb), O);
       if constexpr (kHalf) {
-        const float un = 1.f / by;
+        const float un = __uint_as_float((254u << 23) - __float_as_uint(by));  // 1 / by, a power of two
 #pragma unroll
         for (int i = 0; i < 16; ++i) O[i] *= un;
       }
+      if (KIND != kSum || last) hand_over(O);
     }
 
-    // the state's sum: V weighted, in 16 bits as two numbers (fp16 to 2^-22,
-    // bf16 to 2^-17) and in bf16 as a third where the state is an fp32 output
-    float f[PB][EB];
+    if (KIND != kMany || last) {
+      // the state's sum: V weighted, in 16 bits as two numbers (fp16 to 2^-22,
+      // bf16 to 2^-17) and in bf16 as a third where the state is an fp32 output
+      float f[PB][EB];
 #pragma unroll
-    for (int pb = 0; pb < PB; ++pb) {
-      unpack<T>(TV::col_frag(tv, TK::KR * pb, w, ln), f[pb]);
+      for (int pb = 0; pb < PB; ++pb) {
+        unpack<T>(TV::col_at(v_at, TK::KR * pb, 0), f[pb]);
 #pragma unroll
-      for (int e = 0; e < EB; ++e) f[pb][e] *= wv[pb][e];
-    }
-    float keep = KIND == kOne || g == 0 ? power(ld2, n) : 1.f;
-    if constexpr (kHalf) {
-      float most = 0.f;
-#pragma unroll
-      for (int pb = 0; pb < PB; ++pb)
-#pragma unroll
-        for (int e = 0; e < EB; ++e) most = fmaxf(most, fabsf(f[pb][e]));
-      const float to = lift_of(most);
-      keep *= to / lift;
-      lift = to;
-#pragma unroll
-      for (int pb = 0; pb < PB; ++pb)
-#pragma unroll
-        for (int e = 0; e < EB; ++e) f[pb][e] *= to;
-    }
-#pragma unroll
-    for (int dt = 0; dt < NDT; ++dt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) S[dt][i] *= keep;
-    constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
-    u32x4_t vw[PB][kParts];
-#pragma unroll
-    for (int pb = 0; pb < PB; ++pb) {
-      vw[pb][0] = pack<T>(f[pb]);
-#pragma unroll
-      for (int i = 1; i < kParts; ++i) {  // what the number before has rounded away
-        float r[EB];
-        unpack<T>(vw[pb][i - 1], r);
-#pragma unroll
-        for (int e = 0; e < EB; ++e) f[pb][e] -= r[e];
-        vw[pb][i] = pack<T>(f[pb]);
+        for (int e = 0; e < EB; ++e) f[pb][e] *= wv[pb][e];
       }
+      float keep = (KIND == kSum || state_only) && !first ? 1.f : n < 32 ? power(ld2, n) : keep32;
+      if constexpr (kHalf) {
+        float most = 0.f;
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb)
+#pragma unroll
+          for (int e = 0; e < EB; ++e) most = fmaxf(most, fabsf(f[pb][e]));
+        const float to = lift_of(most);
+        keep *= to / lift;
+        lift = to;
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb)
+#pragma unroll
+          for (int e = 0; e < EB; ++e) f[pb][e] *= to;
+      }
+#pragma unroll
+      for (int dt = 0; dt < NDT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[dt][i] *= keep;
+      constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
+      u32x4_t vw[PB][kParts];
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) {
+        vw[pb][0] = pack<T>(f[pb]);
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) {  // what the number before has rounded away
+          if (i == 2 && !state_out) break;
+          float r[EB];
+          unpack<T>(vw[pb][i - 1], r);
+#pragma unroll
+          for (int e = 0; e < EB; ++e) f[pb][e] -= r[e];
+          vw[pb][i] = pack<T>(f[pb]);
+        }
+      }
+      Ahead<PB * NDT, kAheadCols> kcols;
+      auto read_cols = [&](int i) __attribute__((always_inline)) { return TK::col_at(cols_at, TK::KR * (i / NDT), i % NDT); };
+      kcols.start(read_cols);
+      kcols.run(read_cols, [&](int i, u32x4_t kf) __attribute__((always_inline)) {
+        f32x16_t& s = S[i % NDT];
+        s = Mm<T>::mac(kf, vw[i / NDT][0], s);
+        if constexpr (kParts > 1) s = Mm<T>::mac(kf, vw[i / NDT][1], s);
+        if constexpr (kParts > 2)
+          if (state_out) s = Mm<T>::mac(kf, vw[i / NDT][2], s);
+      });
     }
-    Ahead<PB * NDT, kAheadCols> kcols;
-    auto read_cols = [&](int i) __attribute__((always_inline)) { return TK::col_frag_state(tk, TK::KR * (i / NDT), i % NDT, ln); };
-    kcols.start(read_cols);
-    kcols.run(read_cols, [&](int i, u32x4_t kf) __attribute__((always_inline)) {
-      f32x16_t& s = S[i % NDT];
-      s = Mm<T>::mac(kf, vw[i / NDT][0], s);
-      if constexpr (kParts > 1) s = Mm<T>::mac(kf, vw[i / NDT][1], s);
-      if constexpr (kParts > 2)
-        if (state_out) s = Mm<T>::mac(kf, vw[i / NDT][2], s);
-    });
-    if (++g == gb) {
+    n_before = n;
+    u_at = u_at == lds0 + (NST - 1) * LL::kStage ? lds0 : u_at + LL::kStage;
+    if (last) {
       g = 0;
-      ++c;
+      togo -= n;
+      if constexpr (KIND == kMany) u_kv = u_kv == lds0 + LL::kAtPairs ? u_kv + LL::kKV : lds0 + LL::kAtPairs;
+    } else {
+      ++g;
     }
   }
-  if (!state_only) {
-    if (iters > 0) store(r0 + 32 * (int64_t)(rev ? 0 : n_chunks - 1));
+  if constexpr (!state_only) {
+    if (iters > 0) {
+      if constexpr (kSplit) stage_barrier<0>();
+      store(n_before);
+    }
     // steps past the end
     const int64_t top = r0 + args.seg_rows < args.T ? r0 + args.seg_rows : args.T;
-    for (int64_t row = (r1 > r0 ? r1 : r0) + w; row < top; row += NW) {
-      T* p = (T*)x.out + b * x.os.b + h * x.os.h + dv0 + row * x.os.t;
-      for (int d = lane; d < 32 * NW && d < cols; d += 64) p[d] = Elem<T>::from_f(0.f);
-    }
+    for (int64_t row = r1 + wave; row < top; row += NW * KS)
+      for (int k = 0; k < (KIND == kMany ? x.ga : 1); ++k) {
+        T* p = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha + k) * x.os.h + dv0 + row * x.os.t;
+        for (int d = lane; d < 32 * NW && d < cols; d += 64) p[d] = Elem<T>::from_f(0.f);
+      }
   }
   // the state after the run, or the segment's own sum
   float* to = nullptr;
@@ -488,42 +636,48 @@ __global__ void __launch_bounds__(64 * NW, DP * sizeof(T) > 256 ? 1 : 2) linattn
     for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int d = 32 * dt + TK::state_row(i, ln);
+        const int d = 32 * (part * NDT + dt) + TK::state_row(i, ln);
         const uint32_t at = d < x.DK && dv < x.DV ? (uint32_t)(d * s_dk + dv * s_dv) * 4 : kNoRow;
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[dt][i] * by), r, at, 0, 0);
       }
   }
 }
 
-template <typename T, int DP, int NW, bool DMA, int KIND>
+template <typename T, int DP, int NW, int KS, bool DMA, int KIND>
 static hipError_t linattn_launch(const LinArgs& a, unsigned groups, hipStream_t s) {
-  const size_t bytes = (size_t)lin_stages<T, DP, NW, KIND>() * lin_stage_bytes<T, DP, NW, KIND>();
-  const hipError_t e = allow_lds<linattn_kernel<T, DP, NW, DMA, KIND>>(bytes);
+  constexpr size_t bytes = LinLds<T, DP, NW, KS, KIND>::kBytes;
+  const hipError_t e = allow_lds<linattn_kernel<T, DP, NW, KS, DMA, KIND>>(bytes);
   if (e != hipSuccess) return e;
   Timed timed(10, s);
-  linattn_kernel<T, DP, NW, DMA, KIND><<<dim3(groups), 64 * NW, bytes, s>>>(a);
+  linattn_kernel<T, DP, NW, KS, DMA, KIND><<<dim3(groups), 64 * NW * KS, bytes, s>>>(a);
   return hipGetLastError();
 }
-template <typename T, int DP, int NW, bool DMA>
-static hipError_t linattn_kind(const LinArgs& a, unsigned groups, hipStream_t s) {
-  if (a.state_only) return linattn_launch<T, DP, NW, DMA, kState>(a, groups, s);
-  int gb = 1;
-  for (int i = 0; i < a.runs; ++i) gb = a.run[i].gb > gb ? a.run[i].gb : gb;
-  return gb > 1 ? linattn_launch<T, DP, NW, DMA, kSum>(a, groups, s) : linattn_launch<T, DP, NW, DMA, kOne>(a, groups, s);
+template <typename T, int DP, int NW, int KS, bool DMA>
+static hipError_t linattn_kind(const LinArgs& a, int many, unsigned groups, hipStream_t s) {
+  if (a.state_only) return linattn_launch<T, DP, NW, KS, DMA, kState>(a, groups, s);
+  // (every run of the launch is of one kind)
+  if (a.run[0].gb > 1) return linattn_launch<T, DP, NW, KS, DMA, kSum>(a, groups, s);
+  if (many) return linattn_launch<T, DP, NW, KS, DMA, kMany>(a, groups, s);
+  return linattn_launch<T, DP, NW, KS, DMA, kOne>(a, groups, s);
 }
-template <typename T, int DP, int NW>
-static hipError_t linattn_loads(const LinArgs& a, int dma, unsigned groups, hipStream_t s) {
-  return dma ? linattn_kind<T, DP, NW, true>(a, groups, s) : linattn_kind<T, DP, NW, false>(a, groups, s);
+template <typename T, int DP, int NW, int KS>
+static hipError_t linattn_loads(const LinArgs& a, int many, int dma, unsigned groups, hipStream_t s) {
+  return dma ? linattn_kind<T, DP, NW, KS, true>(a, many, groups, s) : linattn_kind<T, DP, NW, KS, false>(a, many, groups, s);
 }
 template <typename T>
-static hipError_t linattn_of(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s) {
-  switch (dp + nw) {
-    case 64 + 2: return linattn_loads<T, 64, 2>(a, dma, groups, s);
-    case 64 + 4: return linattn_loads<T, 64, 4>(a, dma, groups, s);
-    case 128 + 2: return linattn_loads<T, 128, 2>(a, dma, groups, s);
-    case 128 + 4: return linattn_loads<T, 128, 4>(a, dma, groups, s);
-    case 256 + 2: return linattn_loads<T, 256, 2>(a, dma, groups, s);
-    default: return linattn_loads<T, 256, 4>(a, dma, groups, s);
+static hipError_t linattn_of(const LinArgs& a, const LinTile& t, int many, int dma, unsigned groups, hipStream_t s) {
+  switch (t.dp * 100 + t.nw * 10 + t.ks) {
+    case 64 * 100 + 21: return linattn_loads<T, 64, 2, 1>(a, many, dma, groups, s);
+    case 64 * 100 + 22: return linattn_loads<T, 64, 2, 2>(a, many, dma, groups, s);
+    case 128 * 100 + 22: return linattn_loads<T, 128, 2, 2>(a, many, dma, groups, s);
+    case 256 * 100 + 22: return linattn_loads<T, 256, 2, 2>(a, many, dma, groups, s);
+    default: break;
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (t.dp == 128) return linattn_loads<T, 128, 4, 1>(a, many, dma, groups, s);
+    return linattn_loads<T, 256, 4, 2>(a, many, dma, groups, s);
+  } else {
+    return hipErrorInvalidValue;  // (linattn_tile)
   }
 }
 

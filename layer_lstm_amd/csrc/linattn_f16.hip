@@ -4,7 +4,7 @@
 #include "linattn_common.hpp"
 
 namespace lstm {
-hipError_t launch_linattn_f16(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s) {
-  return linattn_of<f16_t>(a, dp, nw, dma, groups, s);
+hipError_t launch_linattn_f16(const LinArgs& a, const LinTile& t, int many, int dma, unsigned groups, hipStream_t s) {
+  return linattn_of<f16_t>(a, t, many, dma, groups, s);
 }
 }  // namespace lstm

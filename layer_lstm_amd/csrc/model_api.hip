@@ -170,7 +170,7 @@ int lstm_linattn_fwd(const lstm_linattn_shape* shape, const void* q, const void*
   r.in_by = r.out_by = 1.f;
   r.seg = (float*)workspace;
   if (p.step) return status(launch_linattn_step(p, a, (hipStream_t)stream));
-  return status(launch_linattn(p, a, &dma, (hipStream_t)stream));
+  return status(launch_linattn(p, p.fwd, a, &dma, (hipStream_t)stream));
 }
 
 int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const void* q, const void* k, const void* v,
@@ -211,7 +211,7 @@ int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const vo
     r.seg = (float*)((char*)workspace + i * p.seg_bytes);
   }
   a.run[2].s_out = dstate0;
-  return status(launch_linattn(p, a, dma, (hipStream_t)stream));
+  return status(launch_linattn(p, p.bwd, a, dma, (hipStream_t)stream));
 }
 
 int lstm_penalty(const lstm_penalty_shape* shape, const void* logits, const void* history, const void* history_length,

@@ -23,7 +23,7 @@ struct LinRun {
   float* seg;       // [B][Hs][segs][DK][DV] states at the segments' starts
   int whole;        // kWholeQ / K / V / O of a, k, v, out
   int dv_blocks;    // work-groups a head's columns are split over
-  int64_t group0;   // first work-group of the run in its launch
+  uint32_t group0;  // first work-group of the run in its launch, a multiple of 8
 };
 struct LinArgs {
   LinRun run[3];
@@ -37,21 +37,31 @@ struct LinArgs {
   int64_t seg_rows;          // steps of a segment, a multiple of 32
   int state_only;            // the segments' own sums into seg, no outputs
 };
+// An instance of the kernel: the row size it runs with, 32-column tiles and parts
+// of the state's rows of a work-group, a wave each.
+struct LinTile {
+  int dp, nw, ks;
+};
+struct LinCall {        // the forward, or the backward
+  LinTile tile[3];     // of each run
+  int many[3];
+  int segs;            // segments of the time axis
+  int64_t seg_rows;
+};
 struct LinPlan {
   int dtype, cus;
-  int segs;
-  int64_t seg_rows;
+  LinCall fwd, bwd;
   int step;            // forward by the kernel for a few steps
-  size_t seg_bytes;    // of one run's seg
+  size_t seg_bytes;    // of one run's seg of the backward
   size_t total_fwd, total_bwd;
 };
 void make_linattn_plan(const lstm_linattn_shape& s, int cus, LinPlan* p);
 // runs of a call, their seg set; dma[i]: rows of run i are whole aligned chunks
-hipError_t launch_linattn(const LinPlan& p, LinArgs a, const int* dma, hipStream_t s);
+hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const int* dma, hipStream_t s);
 hipError_t launch_linattn_step(const LinPlan& p, const LinArgs& a, hipStream_t s);
-hipError_t launch_linattn_f32(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s);
-hipError_t launch_linattn_bf16(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s);
-hipError_t launch_linattn_f16(const LinArgs& a, int dp, int nw, int dma, unsigned groups, hipStream_t s);
+hipError_t launch_linattn_f32(const LinArgs& a, const LinTile& t, int many, int dma, unsigned groups, hipStream_t s);
+hipError_t launch_linattn_bf16(const LinArgs& a, const LinTile& t, int many, int dma, unsigned groups, hipStream_t s);
+hipError_t launch_linattn_f16(const LinArgs& a, const LinTile& t, int many, int dma, unsigned groups, hipStream_t s);
 
 // ---- penalty.hip ----
 struct PenaltyArgs {
