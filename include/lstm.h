@@ -479,9 +479,8 @@ int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const 
  * times a power of two, so that they neither overflow nor fall among the
  * denormals), and summed, kept and handed over in fp32.  A step that is not
  * finite may also reach the outputs of the 31 steps before it.
- * Any D, Dv in [1, 256]; scale and 1 / scale finite and not 0; T < 2^26, B, Hq <
- * 2^20; rows of whole aligned 16-byte chunks (t stride included) are the fast
- * case. */
+ * Any D, Dv in [1, 256]; scale finite; T < 2^26, B, Hq < 2^20, B Hq < 2^18; rows of
+ * whole aligned 16-byte chunks (t stride included) are the fast case. */
 #define LSTM_LINATTN_STEP 8
 typedef struct {
   int64_t T, B, Hq, Hk, D, Dv;

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
   float ld2 = args.log_decay[hs];
   ld2 = (ld2 > 0.f ? 0.f : ld2) * kLog2e;
   const int d = e / x.DV, c = e - d * x.DV;
-  float S = x.s_in ? x.s_in[head * n + d * x.s_dk + c * x.s_dv] * x.in_by : 0.f;
+  float S = x.s_in ? x.s_in[head * n + d * x.s_dk + c * x.s_dv] : 0.f;
   float* at = x.seg + head * args.segs * n + e;
   constexpr int kAhead = 8;
   for (int o0 = 0; o0 < args.segs; o0 += kAhead) {

@@ -12,12 +12,11 @@
 //   dk_t = R_t v_t            (backwards in time: rows v, keys do, values q, state R^T)
 //   dv_t = R_t^T k_t          (backwards in time: rows k, keys q, values do, state R)
 // so that one kernel is all four: a "run" has rows a, keys k and values v,
-// out_i = scale (inner_i + state part), and a direction of time.  Backwards,
-// the state X that is carried to a chunk has been through its step's decay
-// already (what R_T = dstate stands for):
-//   out_i = scale ( a^(n-1-i) a_i X + sum_{j>=i} a^(j-i) (a_i . k_j) v_j )
-//   X'    = a^n X + sum_j a^(j+1) k_j v_j^T,
-// with X in units of 1 / scale.
+// and a direction of time.  Backwards, the state X that is carried to a chunk has
+// been through its step's decay already (what dstate stands for), and has the
+// scale in it:
+//   out_i = a^(n-1-i) a_i X + scale sum_{j>=i} a^(j-i) (a_i . k_j) v_j
+//   X'    = a^n X + scale sum_j a^(j+1) k_j v_j^T.
 #pragma once
 #include "attend_common.hpp"
 #include "model_internal.hpp"
@@ -248,11 +247,9 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
   {
     const float* in = x.s_in ? x.s_in + head * state_size : nullptr;
     int s_dk = (int)x.s_dk, s_dv = (int)x.s_dv;
-    float by = x.in_by;
     if (args.segs > 1) {
       in = state_only ? nullptr : x.seg + (head * args.segs + order) * state_size;
       s_dk = x.DV; s_dv = 1;
-      by = 1.f;
     }
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)in, 0, in ? (int)state_size * 4 : 0, 0x00020000);
     const int dv = dv0 + 32 * w + (lane & 31);
@@ -262,13 +259,13 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
       for (int i = 0; i < 16; ++i) {
         const int d = 32 * (part * NDT + dt) + TK::state_row(i, lane);
         const uint32_t at = d < x.DK && dv < x.DV ? (uint32_t)(d * s_dk + dv * s_dv) * 4 : kNoRow;
-        S[dt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0)) * by;
+        S[dt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
       }
   }
   float lift = 1.f;  // fp16: S holds the state times this power of two
 
   // Weights of P (row j = reg_row, column i = lane; times scale) and of V in the
-  // state's sum.  They count from the chunk's end forwards in time and from its
+  // state's sum (backwards times scale).  They count from the chunk's end forwards in time and from its
   // beginning backwards, so a chunk of fewer than 32 steps lies at that end of
   // its tiles.
   const int ri = lane & 31;
@@ -284,11 +281,11 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
 #pragma unroll
     for (int e = 0; e < EB; ++e) {
       const int j = frag_row<T>(pb, e, lane);
-      wv[pb][e] = power(ld2, rev ? j + 1 : 31 - j);
+      wv[pb][e] = power(ld2, rev ? j + 1 : 31 - j) * (rev ? scale : 1.f);
     }
   const float keep32 = power(ld2, 32);
   // forwards every row's power is the chunk's full one but in the last chunk
-  const float since32 = power(ld2, rev ? 31 - ri : ri + 1) * scale;
+  const float since32 = power(ld2, rev ? 31 - ri : ri + 1) * (rev ? 1.f : scale);
   // the state of this work-group reaches an output in fp32
   const bool state_out = x.s_out != nullptr && ha == 0;
   // (this wave's rows of the state: k-blocks from part KB of a, tiles from part NDT of k)
@@ -503,7 +500,7 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
         float f = since32;
         if (n < 32) {
           const int e = rev ? n - 1 - ri : ri + 1 - (32 - n);
-          f = power(ld2, e < 0 ? 0 : e) * scale;
+          f = power(ld2, e < 0 ? 0 : e) * (rev ? 1.f : scale);
         }
         if constexpr (kHalf) f *= undo;
 #pragma unroll
@@ -620,16 +617,14 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
   // the state after the run, or the segment's own sum
   float* to = nullptr;
   int s_dk = (int)x.s_dk, s_dv = (int)x.s_dv;
-  float by = x.out_by;
   if (state_only) {
     to = x.seg + (head * args.segs + order) * state_size;
     s_dk = x.DV; s_dv = 1;
-    by = 1.f;
   } else if (state_out && order == args.segs - 1) {
     to = x.s_out + head * state_size;
   }
   if (to) {
-    if constexpr (kHalf) by /= lift;
+    const float by = 1.f / lift;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)to, 0, (int)state_size * 4, 0x00020000);
     const int ln = tile_lane<true>(lane), dv = dv0 + 32 * w + (ln & 31);
 #pragma unroll
@@ -638,7 +633,7 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
       for (int i = 0; i < 16; ++i) {
         const int d = 32 * (part * NDT + dt) + TK::state_row(i, ln);
         const uint32_t at = d < x.DK && dv < x.DV ? (uint32_t)(d * s_dk + dv * s_dv) * 4 : kNoRow;
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[dt][i] * by), r, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(kHalf ? S[dt][i] * by : S[dt][i]), r, at, 0, 0);
       }
   }
 }

@@ -12,7 +12,7 @@ namespace lstm {
 static int linattn_plan(const lstm_linattn_shape* s, bool bwd, LinPlan* p) {
   if (!s) return LSTM_ERR_NULL;
   if (s->T < 0 || s->B < 0 || s->Hq < 0 || s->Hk < 0 || s->D < 1 || s->Dv < 1 || (s->Hk == 0) != (s->Hq == 0) ||
-      (s->Hk > 0 && s->Hq % s->Hk != 0) || !(fabsf(s->scale) <= 3.4e38f) || !(fabsf(1.f / s->scale) <= 3.4e38f) ||
+      (s->Hk > 0 && s->Hq % s->Hk != 0) || !(fabsf(s->scale) <= 3.4e38f) ||
       !strides_ok(s->q) || !strides_ok(s->k) || !strides_ok(s->v) || !strides_ok(s->o) ||
       !disjoint(s->o, s->T, s->B, s->Hq, s->Dv))
     return LSTM_ERR_DIMS;
@@ -167,7 +167,6 @@ int lstm_linattn_fwd(const lstm_linattn_shape* shape, const void* q, const void*
   LinRun& r = a.run[0];
   r.s_in = state; r.s_out = state_out;
   r.s_dk = s.Dv; r.s_dv = 1;
-  r.in_by = r.out_by = 1.f;
   r.seg = (float*)workspace;
   if (p.step) return status(launch_linattn_step(p, a, (hipStream_t)stream));
   return status(launch_linattn(p, p.fwd, a, &dma, (hipStream_t)stream));
@@ -206,8 +205,6 @@ int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const vo
     r.s_in = i == 0 ? state : dstate;
     r.s_dk = i == 2 ? s.Dv : 1;
     r.s_dv = i == 2 ? 1 : s.Dv;
-    r.in_by = i == 0 ? 1.f : 1.f / s.scale;
-    r.out_by = s.scale;
     r.seg = (float*)((char*)workspace + i * p.seg_bytes);
   }
   a.run[2].s_out = dstate0;

@@ -19,7 +19,6 @@ struct LinRun {
   const float* s_in;  // [B][Hs] states before the first step, element (dk, dv) at dk s_dk + dv s_dv; null: zeros
   float* s_out;       // after the last, or null
   int64_t s_dk, s_dv;
-  float in_by, out_by;
   float* seg;       // [B][Hs][segs][DK][DV] states at the segments' starts
   int whole;        // kWholeQ / K / V / O of a, k, v, out
   int dv_blocks;    // work-groups a head's columns are split over

@@ -715,9 +715,10 @@ class LinearAttention:
         self.state = self.dq = self.dk = self.dv = self.dstate = None
 
     def _rows(self, name, s, x, H, D):
-        if x.dtype != self.tdtype or x.shape != (self.T, self.B, H, D) or (D > 1 and x.stride(3) != 1):
+        if x.dtype != self.tdtype or x.shape != (self.T, self.B, H, D) or (D > 1 and x.stride(3) != 1 and x.numel()):
             raise ValueError(f"{name}: {[self.T, self.B, H, D]} of {self.tdtype}, last dimension contiguous")
-        s.t, s.b, s.h = x.stride()[:3]
+        if x.numel():
+            s.t, s.b, s.h = x.stride()[:3]
 
     def _state(self, name, x):
         if x is not None and (x.dtype != torch.float32 or x.shape != (self.B, self.Hk, self.D, self.Dv) or
