@@ -170,30 +170,48 @@ hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const i
 
 // ---------------------------------------------------------------------------
 // A few steps: the state in registers in fp32, read and written once, which is
-// the bound.  A work-group has a (sequence, key head) and 4 CL columns of its
-// state: CL lanes of four columns, the rows dealt to the 256 / CL lane groups.
-template <typename T, int CL, int RPT>
+// the bound.  A work-group has a (sequence, key head) and COLS columns of its
+// state: COLS / 4 lanes of four columns each, the rows dealt to the other lanes.
+constexpr int kStepHeads = 4;  // query heads at a time
+template <typename T, int COLS, int RPT>
 __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
-  constexpr int RG = 256 / CL;  // row groups
-  constexpr int HB = 4;         // query heads at a time
+  constexpr int CL = COLS / 4, RG = 256 / CL, HB = kStepHeads;
+  constexpr int QN = HB * RPT * RG, QL = (QN + 255) / 256;  // values of q staged, and by a lane
   const LinRun& x = args.run[0];
-  __shared__ float qs[HB][256], ks[256], vs[4 * CL];
+  __shared__ float qs[HB][RPT * RG], ks[RPT * RG], vs[COLS];
   __shared__ f32x4_t part[HB][RG][CL];
   const int tid = threadIdx.x, cl = tid % CL, rg = tid / CL;
   const int dvb = (int)(blockIdx.x % (unsigned)x.dv_blocks);
   const int64_t head = blockIdx.x / (unsigned)x.dv_blocks;
   const int b = (int)(head / args.Hs), hs = (int)(head - (int64_t)b * args.Hs);
-  const int dv0 = dvb * 4 * CL, c0 = dv0 + 4 * cl;
+  const int dv0 = dvb * COLS, c0 = dv0 + 4 * cl;
   const bool whole = x.DV % 4 == 0 && ((uintptr_t)x.s_in & 15) == 0 && ((uintptr_t)x.s_out & 15) == 0;
   int end = (int)args.T;
   if (args.len) {
     const int l = args.len[b];
     end = l < 0 ? 0 : l < end ? l : end;
   }
-  const float decay = __builtin_amdgcn_exp2f([&] {
-    const float ld = args.log_decay[hs];
-    return (ld > 0.f ? 0.f : ld) * kLog2e;
-  }());
+  const float ld = args.log_decay[hs], decay = __builtin_amdgcn_exp2f((ld > 0.f ? 0.f : ld) * kLog2e);
+
+  // a step's k, v and first heads of q, read ahead (the first before the state:
+  // loads return in order)
+  float kx = 0.f, vx = 0.f, qx[QL];
+  const int first_heads = x.ga < HB ? x.ga : HB;
+  auto q_at = [&](int t, int g, int d) __attribute__((always_inline)) {
+    return Elem<T>::load((const T*)x.a + t * x.as.t + b * x.as.b + (int64_t)(hs * x.ga + g) * x.as.h + d);
+  };
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    if (t >= end) return;
+    if (tid < x.DK) kx = Elem<T>::load((const T*)x.k + t * x.ks.t + b * x.ks.b + hs * x.ks.h + tid);
+    if (tid < COLS && dv0 + tid < x.DV) vx = Elem<T>::load((const T*)x.v + t * x.vs.t + b * x.vs.b + hs * x.vs.h + dv0 + tid);
+#pragma unroll
+    for (int j = 0; j < QL; ++j) {
+      const int g = (tid + 256 * j) / (RPT * RG), d = (tid + 256 * j) % (RPT * RG);
+      if (g < first_heads && d < x.DK) qx[j] = q_at(t, g, d);
+    }
+  };
+  fetch(0);
+
   f32x4_t S[RPT];
   const float* in = x.s_in ? x.s_in + head * x.DK * x.DV : nullptr;
 #pragma unroll
@@ -214,17 +232,23 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
   for (int t = 0; t < (int)args.T; ++t) {
     const bool real = t < end;
     if (real) {
-      __syncthreads();  // the step before has read k and v
-      if (tid < x.DK) ks[tid] = Elem<T>::load((const T*)x.k + t * x.ks.t + b * x.ks.b + hs * x.ks.h + tid);
-      if (tid < 4 * CL) vs[tid] = dv0 + tid < x.DV ? Elem<T>::load((const T*)x.v + t * x.vs.t + b * x.vs.b + hs * x.vs.h + dv0 + tid) : 0.f;
+      if (t > 0) __syncthreads();  // the step before has been read
+      if (tid < x.DK) ks[tid] = kx;
+      if (tid < COLS) vs[tid] = vx;
+#pragma unroll
+      for (int j = 0; j < QL; ++j)
+        if (tid + 256 * j < QN) (&qs[0][0])[tid + 256 * j] = qx[j];
+      fetch(t + 1);
     }
     for (int g0 = 0; g0 < x.ga; g0 += HB) {
       const int heads = x.ga - g0 < HB ? x.ga - g0 : HB;
       if (real) {
-        if (g0 > 0) __syncthreads();  // the heads before have been read
-        for (int i = tid; i < heads * x.DK; i += 256) {
-          const int g = i / x.DK, d = i - g * x.DK;
-          qs[g][d] = Elem<T>::load((const T*)x.a + t * x.as.t + b * x.as.b + (int64_t)(hs * x.ga + g0 + g) * x.as.h + d);
+        if (g0 > 0) {
+          __syncthreads();  // the heads before have been read
+          for (int i = tid; i < heads * x.DK; i += 256) {
+            const int g = i / x.DK, d = i - g * x.DK;
+            qs[g][d] = q_at(t, g0 + g, d);
+          }
         }
         __syncthreads();
         f32x4_t acc[HB];
@@ -254,12 +278,12 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
           if (g < heads) part[g][rg][cl] = acc[g];
         __syncthreads();
       }
-      for (int i = tid; i < heads * 4 * CL; i += 256) {
-        const int g = i / (4 * CL), c = i - g * 4 * CL;
+      if (tid < heads * COLS) {  // (HB COLS threads at most)
+        const int g = tid / COLS, c = tid % COLS;
         if (dv0 + c < x.DV) {
           float o = 0.f;
           if (real) {
-#pragma unroll 8
+#pragma unroll
             for (int k = 0; k < RG; ++k) o += ((const float*)&part[g][k][0])[c];
           }
           ((T*)x.out)[t * x.os.t + b * x.os.b + (int64_t)(hs * x.ga + g0 + g) * x.os.h + dv0 + c] = Elem<T>::from_f(as_f32(o * args.scale));
@@ -285,25 +309,32 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
   }
 }
 
-template <typename T, int CL>
-static hipError_t step_rows(const LinArgs& a, unsigned groups, hipStream_t s) {
-  constexpr int RG = 256 / CL;
+// Small work-groups, whose reads and writes overlap other ones', but for heads
+// that share a state or columns that are not divided, where a work-group's fixed
+// work counts (32 and 64 columns, us from HBM: 256 sequences, 16 heads of 128 115
+// and 132, 16 sequences 11.9 and 13.6; 256 sequences, 8/2 heads of 80 x 112 17.7 and
+// 13.8; 200 sequences, 3 heads of 37 x 51 9.7 and 7.7).
+template <typename T, int COLS>
+static hipError_t step_launch(const LinArgs& a, unsigned groups, hipStream_t s) {
+  constexpr int R = COLS / 32;  // rows of a lane per 32
   Timed timed(10, s);
-  if (a.run[0].DK <= 64) linattn_step_kernel<T, CL, 64 / RG><<<dim3(groups), 256, 0, s>>>(a);
-  else if (a.run[0].DK <= 128) linattn_step_kernel<T, CL, 128 / RG><<<dim3(groups), 256, 0, s>>>(a);
-  else linattn_step_kernel<T, CL, 256 / RG><<<dim3(groups), 256, 0, s>>>(a);
+  const int DK = a.run[0].DK;
+  if (DK <= 64) linattn_step_kernel<T, COLS, 2 * R><<<dim3(groups), 256, 0, s>>>(a);
+  else if (DK <= 96) linattn_step_kernel<T, COLS, 3 * R><<<dim3(groups), 256, 0, s>>>(a);
+  else if (DK <= 128) linattn_step_kernel<T, COLS, 4 * R><<<dim3(groups), 256, 0, s>>>(a);
+  else linattn_step_kernel<T, COLS, 8 * R><<<dim3(groups), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename T>
 static hipError_t step_of(const LinPlan& p, LinArgs a, hipStream_t s) {
   LinRun& x = a.run[0];
-  // 32 columns a work-group where 128 leave compute units idle
   const int64_t heads = (int64_t)a.B * a.Hs;
-  const bool wide = heads * ((x.DV + 127) / 128) >= 2 * (int64_t)p.cus;
-  x.dv_blocks = wide ? (x.DV + 127) / 128 : (x.DV + 31) / 32;
+  const bool wide = (x.ga > 1 || x.DV <= 64) && heads * ((x.DV + 63) / 64) >= 2 * (int64_t)p.cus;
+  const int cols = wide ? 64 : 32;
+  x.dv_blocks = (x.DV + cols - 1) / cols;
   const int64_t groups = heads * x.dv_blocks;
   if (groups == 0) return hipSuccess;
-  return wide ? step_rows<T, 32>(a, (unsigned)groups, s) : step_rows<T, 8>(a, (unsigned)groups, s);
+  return wide ? step_launch<T, 64>(a, (unsigned)groups, s) : step_launch<T, 32>(a, (unsigned)groups, s);
 }
 
 hipError_t launch_linattn_step(const LinPlan& p, const LinArgs& a, hipStream_t s) {

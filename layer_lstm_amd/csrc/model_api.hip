@@ -217,7 +217,7 @@ int lstm_penalty(const lstm_penalty_shape* shape, const void* logits, const void
   PenaltyArgs a;
   const int rc = penalty_plan(shape, &a);
   if (rc != LSTM_OK) return rc;
-  if ((bias && a.ldb != 0 && a.ldb < a.V) || (mask && a.ldm < (a.V + 31) / 32) || (out == logits && a.ld != a.ldo))
+  if ((bias && a.ldb != 0 && a.ldb < a.V) || (mask && a.ldm < (a.V + 31) / 32) || (out && out == logits && a.ld != a.ldo))
     return LSTM_ERR_DIMS;
   const bool counts = a.L > 0 && (repetition || presence || frequency);
   if (a.N > 0 && a.V > 0 && (!logits || !out || (counts && !history))) return LSTM_ERR_NULL;

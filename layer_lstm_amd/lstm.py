@@ -702,6 +702,9 @@ class LinearAttention:
         q, k, v, o = rows
         self.shape = LinattnShape(T, B, Hq, Hk, D, Dv, q, k, v, o, o, q, k, v,
                                   float(max(D, 1) ** -0.5 if scale is None else scale), int(dtype))
+        # shapes of q, k, v, dout and the states, and the strides of those last seen
+        self._shapes = [torch.Size(i) for i in ((T, B, Hq, D), (T, B, Hk, D), (T, B, Hk, Dv), (T, B, Hq, Dv), (B, Hk, D, Dv))]
+        self._at = [None] * 4
         nf, nb = ctypes.c_size_t(0), ctypes.c_size_t(0)
         rc = _lib.lstm_linattn_query(ctypes.byref(self.shape), ctypes.byref(nf), ctypes.byref(nb))
         if rc != OK:
@@ -714,31 +717,37 @@ class LinearAttention:
         self.o = torch.empty((T, B, Hq, Dv), dtype=self.tdtype, device=device)
         self.state = self.dq = self.dk = self.dv = self.dstate = None
 
-    def _rows(self, name, s, x, H, D):
-        if x.dtype != self.tdtype or x.shape != (self.T, self.B, H, D) or (D > 1 and x.stride(3) != 1 and x.numel()):
-            raise ValueError(f"{name}: {[self.T, self.B, H, D]} of {self.tdtype}, last dimension contiguous")
-        if x.numel():
-            s.t, s.b, s.h = x.stride()[:3]
+    def _rows(self, name, i, x):
+        shape, at = self._shapes[i], x.stride()
+        if x.dtype is not self.tdtype or x.shape != shape or (at[3] != 1 and shape[3] > 1 and x.numel()):
+            raise ValueError(f"{name}: {list(shape)} of {self.tdtype}, last dimension contiguous")
+        if at != self._at[i]:
+            self._at[i] = at
+            if x.numel():
+                s = getattr(self.shape, name)
+                s.t, s.b, s.h = at[:3]
 
     def _state(self, name, x):
-        if x is not None and (x.dtype != torch.float32 or x.shape != (self.B, self.Hk, self.D, self.Dv) or
-                              not x.is_contiguous()):
-            raise ValueError(f"{name}: float32 {[self.B, self.Hk, self.D, self.Dv]}, contiguous")
+        if x.dtype is not torch.float32 or x.shape != self._shapes[4] or not x.is_contiguous():
+            raise ValueError(f"{name}: float32 {list(self._shapes[4])}, contiguous")
 
     def _inputs(self, q, k, v, log_decay, state, length):
-        self._rows("q", self.shape.q, q, self.Hq, self.D)
-        self._rows("k", self.shape.k, k, self.Hk, self.D)
-        self._rows("v", self.shape.v, v, self.Hk, self.Dv)
-        if log_decay.dtype != torch.float32 or log_decay.shape != (self.Hk,) or not log_decay.is_contiguous():
+        self._rows("q", 0, q)
+        self._rows("k", 1, k)
+        self._rows("v", 2, v)
+        if log_decay.dtype is not torch.float32 or log_decay.dim() != 1 or log_decay.shape[0] != self.Hk or \
+                not log_decay.is_contiguous():
             raise ValueError(f"log_decay: float32 [{self.Hk}], contiguous")
-        self._state("state", state)
-        if length is not None and (length.dtype != torch.int32 or length.shape != (self.B,) or not length.is_contiguous()):
+        if state is not None:
+            self._state("state", state)
+        if length is not None and (length.dtype is not torch.int32 or length.shape != (self.B,) or not length.is_contiguous()):
             raise ValueError(f"length: int32 [{self.B}], contiguous")
         _on_device(self._dev, q, k, v, log_decay, state, length)
 
     def _forward(self, q, k, v, log_decay, state, length, out, stream):
-        rc = _lib.lstm_linattn_fwd(self._ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(length), _ptr(state),
-                                   _ptr(self.workspace), self._fwd_bytes, _ptr(self.o), _ptr(out),
+        rc = _lib.lstm_linattn_fwd(self._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                   None if length is None else length.data_ptr(), None if state is None else state.data_ptr(),
+                                   self.workspace.data_ptr(), self._fwd_bytes, self.o.data_ptr(), out.data_ptr(),
                                    _stream_on(self._dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_linattn_fwd")
@@ -765,8 +774,9 @@ class LinearAttention:
     def backward(self, dout, q, k, v, log_decay, state=None, length=None, dstate=None, stream=None):
         """dq, dk, dv and the gradient of `state`; dstate: the gradient of the state after the last step."""
         self._inputs(q, k, v, log_decay, state, length)
-        self._rows("dout", self.shape.dout, dout, self.Hq, self.Dv)
-        self._state("dstate", dstate)
+        self._rows("dout", 3, dout)
+        if dstate is not None:
+            self._state("dstate", dstate)
         _on_device(self._dev, dout, dstate)
         if self.dq is None:
             if self._bwd_bytes > self.workspace.numel():
@@ -792,6 +802,7 @@ class Penalty:
 
     def __init__(self, N, V, dtype=F32, device="cuda"):
         self.N, self.V, self.dtype, self.device = N, V, dtype, device
+        self._n, self._rows = torch.Size((N,)), torch.Size((N, V))
         self.shape = PenaltyShape(N, V, V, V, 0, 0, 0, 0, 0, int(dtype), I64)
         self._ref = ctypes.byref(self.shape)
         self._dev = _device_index(device)
@@ -804,47 +815,58 @@ class Penalty:
         ids as ids.t()), the first length [N] (int32) of them counting; repetition, presence, frequency fp32 [N]; bias
         fp32 [V] or [N, V]; mask int32 [N, >= ceil(V / 32)], bit v % 32 of word v / 32 zero = not allowed.  `out`: where
         to (logits itself, say); None: the operator's own buffer."""
-        N, V, s = self.N, self.V, self.shape
-        if logits.dtype != self.tdtype or logits.shape != (N, V) or (V > 1 and logits.stride(1) != 1):
-            raise ValueError(f"logits: [{N}, {V}] of {self.tdtype}, rows contiguous")
+        N, V, s, td, dev = self.N, self.V, self.shape, self.tdtype, self._dev
+        if logits.dtype is not td or logits.shape != self._rows or (V > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits: [{N}, {V}] of {td}, rows contiguous")
         s.ld = _row_stride("logits", logits, V)
         if out is None:
             if self.out is None:
-                self.out = _buffer((N, V), self.tdtype, self.device, stream)
-            out = self.out
-        elif out.dtype != self.tdtype or out.shape != (N, V) or (V > 1 and out.stride(1) != 1):
-            raise ValueError(f"out: [{N}, {V}] of {self.tdtype}, rows contiguous")
-        s.ld_out = _row_stride("out", out, V)
-        some = repetition is not None or presence is not None or frequency is not None
-        if some and history is None:
-            raise ValueError("history: the tokens that the penalties are for")
+                self.out = _buffer((N, V), td, self.device, stream)
+            out, s.ld_out = self.out, V
+        else:
+            if out.dtype is not td or out.shape != self._rows or (V > 1 and out.stride(1) != 1):
+                raise ValueError(f"out: [{N}, {V}] of {td}, rows contiguous")
+            s.ld_out = _row_stride("out", out, V)
+        row = self._row
+        rep, pre, fre = row("repetition", repetition), row("presence", presence), row("frequency", frequency)
         s.L = 0
         if history is not None:
             if history.dim() != 2 or history.shape[0] != N or history.dtype not in _ID_TYPES:
                 raise ValueError(f"history: [{N}, L] of int32 or int64")
-            s.L, s.history_n, s.history_t = history.shape[1], history.stride(0), history.stride(1)
+            s.L = history.shape[1]
+            s.history_n, s.history_t = history.stride()
             s.id_type = _ID_TYPES[history.dtype]
-        if length is not None and (length.dtype != torch.int32 or length.shape != (N,) or not length.is_contiguous()):
+        elif rep or pre or fre:
+            raise ValueError("history: the tokens that the penalties are for")
+        if length is not None and (length.dtype is not torch.int32 or length.shape != self._n or not length.is_contiguous()):
             raise ValueError(f"length: int32 [{N}], contiguous")
-        for name, x in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-            if x is not None and (x.dtype != torch.float32 or x.shape != (N,) or not x.is_contiguous()):
-                raise ValueError(f"{name}: float32 [{N}], contiguous")
         if bias is not None:
-            if bias.dtype != torch.float32 or bias.shape not in ((V,), (N, V)) or (V > 1 and bias.stride(-1) != 1):
+            if bias.dtype is not torch.float32 or bias.shape not in ((V,), self._rows) or (V > 1 and bias.stride(-1) != 1):
                 raise ValueError(f"bias: float32 [{V}] or [{N}, {V}], rows contiguous")
             s.ld_bias = 0 if bias.dim() == 1 or N == 1 or bias.stride(0) == 0 else _row_stride("bias", bias, V)
-        words = (V + 31) // 32
         if mask is not None:
-            if mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[0] != N or mask.shape[1] < words or \
+            words = (V + 31) // 32
+            if mask.dtype is not torch.int32 or mask.dim() != 2 or mask.shape[0] != N or mask.shape[1] < words or \
                     (words > 1 and mask.stride(1) != 1):
                 raise ValueError(f"mask: int32 [{N}, {words}], rows contiguous")
             s.ld_mask = _row_stride("mask", mask, words)
-        _on_device(self._dev, logits, history, length, repetition, presence, frequency, bias, mask, out)
-        rc = _lib.lstm_penalty(self._ref, _ptr(logits), _ptr(history), _ptr(length), _ptr(repetition), _ptr(presence),
-                               _ptr(frequency), _ptr(bias), _ptr(mask), _ptr(out), _stream_on(self._dev, stream))
+        _on_device(dev, logits, history, length, bias, mask, out)
+        rc = _lib.lstm_penalty(self._ref, logits.data_ptr(), None if history is None else history.data_ptr(),
+                               None if length is None else length.data_ptr(), rep, pre, fre,
+                               None if bias is None else bias.data_ptr(), None if mask is None else mask.data_ptr(),
+                               out.data_ptr(), _stream_on(dev, stream))
         if rc != OK:
             raise LstmError(rc, "lstm_penalty")
         return out
+
+    def _row(self, name, x):
+        if x is None:
+            return None
+        if x.dtype is not torch.float32 or x.shape != self._n or not x.is_contiguous():
+            raise ValueError(f"{name}: float32 [{self.N}], contiguous")
+        if x.get_device() != self._dev:
+            _on_device(self._dev, x)
+        return x.data_ptr()
 
 
 class AdamW:
@@ -908,6 +930,7 @@ class AdamW:
                 t.m_scale, t.v_scale = (x.data_ptr() + at // ADAMW_BLOCK * 4 for x in (self.m_scale, self.v_scale))
             if self.master is not None:
                 t.master = self.master.data_ptr() + at * 4
+        self._entries = list(zip([p.shape for p in self.params], self._table))
         self.shape = AdamwShape(lr, betas[0], betas[1], eps, 0, _STORAGE[self.tdtype], bits)
         self._ref = ctypes.byref(self.shape)
         self.clip = self.loss_scale = self.control = self.workspace = None
@@ -934,19 +957,19 @@ class AdamW:
 
     def step(self, grads, stream=None):
         """One step by the gradients, one for each parameter (contiguous, of its shape and type)."""
-        params, table, dev, td = self.params, self._table, self._dev, self.tdtype
-        if len(grads) != len(params):
-            raise ValueError(f"grads: {len(params)} tensors")
-        for p, g, t in zip(params, grads, table):
-            if g.shape != p.shape or g.dtype != td or not g.is_contiguous() or g.get_device() != dev:
-                raise ValueError(f"grads: {list(p.shape)} of {td} on cuda:{dev}, contiguous")
-            t.grad = g.data_ptr()
+        n, table, dev, td = len(self.params), self._table, self._dev, self.tdtype
+        if len(grads) != n:
+            raise ValueError(f"grads: {n} tensors")
+        for g, (shape, entry) in zip(grads, self._entries):
+            if g.shape != shape or g.dtype is not td or not g.is_contiguous() or g.get_device() != dev:
+                raise ValueError(f"grads: {list(shape)} of {td} on cuda:{dev}, contiguous")
+            entry.grad = g.data_ptr()
         s, st = self.shape, _stream_on(dev, stream)
         s.lr, s.beta1, s.beta2, s.eps = self.lr, self.betas[0], self.betas[1], self.eps
         control = None
         if self.control is not None:
             control = self.control.data_ptr()
-            rc = _lib.lstm_adamw_norm(self._ref, table, len(params), self.clip, 1.0 / self.loss_scale,
+            rc = _lib.lstm_adamw_norm(self._ref, table, n, self.clip, 1.0 / self.loss_scale,
                                       _ptr(self.workspace), self.workspace.numel(), control, st)
             if rc != OK:
                 raise LstmError(rc, "lstm_adamw_norm")
@@ -954,7 +977,7 @@ class AdamW:
             raise ValueError("a step in a graph needs clip (math.inf: none): its number has to be on the device")
         else:
             s.step += 1
-        rc = _lib.lstm_adamw_step(self._ref, table, len(params), control, st)
+        rc = _lib.lstm_adamw_step(self._ref, table, n, control, st)
         if rc != OK:
             if control is None:
                 s.step -= 1
