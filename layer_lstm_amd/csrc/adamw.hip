@@ -113,8 +113,8 @@ __device__ __forceinline__ uint2 to_8bit(const float* x, float* scale) {
   for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(x[j]));
   most = block_max(most);
   const bool some = most > kLeast;
-  *scale = some ? most / kMost8 : 0.f;
-  const float inv = some ? kMost8 / most : 0.f;
+  *scale = some ? most * (1.f / kMost8) : 0.f;
+  const float inv = some ? (1.f / most) * kMost8 : 0.f;
   float y[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {

@@ -193,8 +193,10 @@ struct LinLds {
   static constexpr int kStage = KIND == kMany ? kA : kA + kKV;
   static constexpr int kPass = KS == 2 && KIND != kState ? 2 * NW * KS * 2048 : 0;
   static constexpr int kPairs = KIND == kMany ? 2 * kKV : 0;
-  // three stages where they fit a compute unit
-  static constexpr int kStages = 3 * kStage + kPairs + kPass <= 160 * 1024 ? 3 : 2;
+  // three stages where they fit a compute unit; two of small tiles, for more
+  // work-groups (64 sequences, 16 heads of 64, 256 steps, bf16: forward 29.5 us,
+  // backward 70, with three 31.5 and 78)
+  static constexpr int kStages = (KIND != kMany && kStage <= 12 * 1024) || 3 * kStage + kPairs + kPass > 160 * 1024 ? 2 : 3;
   static constexpr int kAtPairs = kStages * kStage, kAtPass = kAtPairs + kPairs, kBytes = kAtPass + kPass;
   static_assert(kBytes <= 160 * 1024, "a compute unit's LDS");
 };
