@@ -469,7 +469,7 @@ int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const 
  * length (int32 [B], NULL = all steps; clamped to [0, T]): a step past a
  * sequence's end holds the state and has o = 0 and no gradient; its rows of q,
  * k, v and dout are not used, they may hold anything.  state_out may be state
- * where T <= LSTM_LINATTN_STEP; otherwise they do not overlap.
+ * where T <= LSTM_LINATTN_STEP; otherwise no output overlaps an input.
  * Gradients: with R_t = a R_{t+1} + scale q_t dout_t^T and a R_T standing for
  * dstate (NULL: zeros), the gradient of state_out,
  *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate0 = a R_0
@@ -517,8 +517,8 @@ int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const vo
  * repetition (> 0; 1 is none), presence, frequency: fp32 [N], NULL = none;
  * with none of the three the history is not read.  bias: fp32, NULL = none;
  * ld_bias 0 or >= V.  mask: 32-bit words, NULL = all allowed, ld_mask >=
- * ceil(V / 32).  out may be logits itself (ld = ld_out).  N < 2^24, V < 2^30,
- * N V < 2^37, L < 2^31. */
+ * ceil(V / 32).  out may be logits itself (ld = ld_out), else they do not
+ * overlap.  N < 2^24, V < 2^30, N V < 2^37, L < 2^31. */
 typedef struct {
   int64_t N, V;
   int64_t ld, ld_out;

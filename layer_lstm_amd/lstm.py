@@ -715,7 +715,7 @@ class LinearAttention:
         self._fwd_bytes, self._bwd_bytes = nf.value, nb.value
         self.workspace = torch.empty(self._fwd_bytes, dtype=torch.uint8, device=device)
         self.o = torch.empty((T, B, Hq, Dv), dtype=self.tdtype, device=device)
-        self.state = self.dq = self.dk = self.dv = self.dstate = None
+        self.state = self.dq = self.dk = self.dv = self.dstate = self.bwd_workspace = None
 
     def _rows(self, name, i, x):
         shape, at = self._shapes[i], x.stride()
@@ -778,9 +778,10 @@ class LinearAttention:
         if dstate is not None:
             self._state("dstate", dstate)
         _on_device(self._dev, dout, dstate)
+        if self.bwd_workspace is None:  # beside the forward's, which a captured forward goes on using
+            self.bwd_workspace = self.workspace if self.workspace.numel() >= self._bwd_bytes else \
+                _buffer((self._bwd_bytes,), torch.uint8, self.device, stream)
         if self.dq is None:
-            if self._bwd_bytes > self.workspace.numel():
-                self.workspace = _buffer((self._bwd_bytes,), torch.uint8, self.device, stream)
             self.dq = _buffer((self.T, self.B, self.Hq, self.D), self.tdtype, self.device, stream)
             self.dk = _buffer((self.T, self.B, self.Hk, self.D), self.tdtype, self.device, stream)
             self.dv = _buffer((self.T, self.B, self.Hk, self.Dv), self.tdtype, self.device, stream)
@@ -788,7 +789,7 @@ class LinearAttention:
         if dstate is not None and dstate.numel() and dstate.data_ptr() == self.dstate.data_ptr():
             raise ValueError("dstate: not the buffer that the gradient of the state before is written to")
         rc = _lib.lstm_linattn_bwd(self._ref, _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(length),
-                                   _ptr(state), _ptr(dstate), _ptr(self.workspace), self.workspace.numel(),
+                                   _ptr(state), _ptr(dstate), _ptr(self.bwd_workspace), self.bwd_workspace.numel(),
                                    _ptr(self.dq), _ptr(self.dk), _ptr(self.dv), _ptr(self.dstate),
                                    _stream_on(self._dev, stream))
         if rc != OK:
@@ -882,7 +883,8 @@ class AdamW:
     The states of all tensors lie in one buffer each (m, v, master; 8 bits: of
     torch.float8_e4m3fn, with m_scale and v_scale), tensor i's at
     places[i]..., a multiple of ADAMW_BLOCK values.  lr may be changed between
-    steps."""
+    steps (a captured step keeps the one it was captured with); the parameters
+    stay where they are in memory."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, clip=None,
                  loss_scale=None, master=None, device="cuda"):
@@ -930,7 +932,7 @@ class AdamW:
                 t.m_scale, t.v_scale = (x.data_ptr() + at // ADAMW_BLOCK * 4 for x in (self.m_scale, self.v_scale))
             if self.master is not None:
                 t.master = self.master.data_ptr() + at * 4
-        self._entries = list(zip([p.shape for p in self.params], self._table))
+        self._entries = [(p, p.shape, p.data_ptr(), t) for p, t in zip(self.params, self._table)]
         self.shape = AdamwShape(lr, betas[0], betas[1], eps, 0, _STORAGE[self.tdtype], bits)
         self._ref = ctypes.byref(self.shape)
         self.clip = self.loss_scale = self.control = self.workspace = None
@@ -960,7 +962,9 @@ class AdamW:
         n, table, dev, td = len(self.params), self._table, self._dev, self.tdtype
         if len(grads) != n:
             raise ValueError(f"grads: {n} tensors")
-        for g, (shape, entry) in zip(grads, self._entries):
+        for g, (p, shape, at, entry) in zip(grads, self._entries):
+            if p.data_ptr() != at:
+                raise ValueError("params: their memory is no longer the one that this optimiser was made for")
             if g.shape != shape or g.dtype is not td or not g.is_contiguous() or g.get_device() != dev:
                 raise ValueError(f"grads: {list(shape)} of {td} on cuda:{dev}, contiguous")
             entry.grad = g.data_ptr()

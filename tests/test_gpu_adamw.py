@@ -243,6 +243,17 @@ def test_another_stream(lstm):
     assert all(torch.equal(x, y) for x, y in zip(pa, pb))
 
 
+def test_a_parameter_that_moved_is_refused(lstm):
+    params, grads = make("f32", [40, 8])
+    opt = lstm.AdamW(params, **OPT)
+    opt.step(grads)
+    held = params[1].clone()
+    params[1].data = held
+    with pytest.raises(ValueError, match="memory"):
+        opt.step(grads)
+    assert opt.shape.step == 1
+
+
 def test_refusals(lstm):
     params, grads = make("f32", [40, 8])
     opt = lstm.AdamW(params, **OPT)

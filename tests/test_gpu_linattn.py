@@ -267,6 +267,32 @@ def test_same_bits_other_streams_and_graphs(lstm):
             assert all(torch.equal(a, b) for a, b in zip(want, got)), k
 
 
+def test_a_captured_forward_keeps_its_workspace(lstm):
+    """The first backward, after the capture, makes buffers: none of them the one that the replays write to."""
+    T, B, H, D = 4000, 1, 1, 64
+    c, _ = make("bf16", T, B, H, H, D, D, ragged=False)
+    args = [c[n] for n in ("q", "k", "v", "log_decay", "state")]
+    m = lstm.LinearAttention(T, B, H, H, D, D, lstm.BF16)
+    assert 0 < m._fwd_bytes < m._bwd_bytes
+    want = [i.clone() for i in m.forward(*args)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.forward(*args)
+    space = m.workspace.data_ptr()
+    m.backward(c["do"], *args, dstate=c["dstate"])
+    torch.cuda.synchronize()
+    assert m.workspace.data_ptr() == space and m.bwd_workspace.data_ptr() != space
+    other = [torch.full((m._fwd_bytes,), 1, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        m.o.fill_(7), m.state.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(m.o, want[0]) and torch.equal(m.state, want[1])
+    assert all(int(i.min()) == 1 == int(i.max()) for i in other)
+
+
 def test_empty_calls(lstm):
     for T, B, H in ((0, 2, 2), (3, 0, 2), (3, 2, 0), (40, 0, 2), (40, 2, 0)):
         c, _ = make("f32", T, B, H, H, 8, 8, ragged=False)
