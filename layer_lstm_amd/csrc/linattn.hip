@@ -8,12 +8,15 @@
 namespace lstm {
 
 // The instance for rows of DK and DV values: `few` work-groups take the one of
-// shorter iterations (two waves for 32 columns), which takes more work in all.
+// shorter iterations (two waves for 32 columns; fp32, bound by a wave's chain of
+// matrix instructions, four, and the same instance for all runs, which then are
+// one launch), which takes more work in all.
 static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
   LinTile t;
   t.dp = DK <= 64 ? 64 : DK <= 128 ? 128 : 256;
   const bool f32 = dtype == LSTM_F32;
-  if (t.dp == 64) t = {64, 2, f32 || few ? 2 : 1};
+  if (f32 && few && t.dp <= 128) t = {128, 1, 4};
+  else if (t.dp == 64) t = {64, 2, f32 || few ? 2 : 1};
   else if (t.dp == 128) t = f32 || few || DV <= 64 ? LinTile{128, 2, 2} : LinTile{128, 4, 1};
   else t = LinTile{256, f32 || DV <= 64 ? 2 : 4, 2};
   return t;
@@ -31,32 +34,43 @@ static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
 // a state take one work-group (one update of the state for all of them) unless
 // that leaves compute units idle (8 sequences, 6/3 heads of 80, 191 steps, fp32:
 // 56 us, heads apart 32; 32 sequences, 32/8 heads, 1024 steps, fp16: 206, apart 260).
+// fp32's instance for few work-groups has a compute unit to itself: it is taken
+// where all of them have one, and no run is long (forward and backward of the
+// fp32 case above 115 us, so 53).
 static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int64_t (*sizes)[3], LinCall* c) {
   const int64_t sets = s.B * s.Hk, chunks = (s.T + 31) / 32, most = chunks / 4 > 1 ? chunks / 4 : 1;
+  bool fits = true;  // the device has a compute unit for all work-groups, or for the next when the short ones end
   auto groups = [&](bool few) {
-    int64_t n = 0;
+    int64_t n = 0, iterations = 0, longest = 1;
     for (int i = 0; i < runs; ++i) {
       const int64_t DK = sizes[i][0], DV = sizes[i][1], ga = sizes[i][2];
       c->tile[i] = linattn_tile(DK, DV, s.dtype, few);
       const int64_t blocks = (DV + 32 * c->tile[i].nw - 1) / (32 * c->tile[i].nw);
       c->many[i] = ga > 1 && sets * blocks * most >= cus;
-      n += sets * blocks * (c->many[i] ? 1 : ga);
+      const int64_t mine = sets * blocks * (c->many[i] ? 1 : ga), heads = i > 0 ? sizes[0][2] : c->many[i] ? ga : 1;
+      n += mine;
+      iterations += mine * heads;
+      if (heads > longest) longest = heads;
     }
+    fits = iterations <= cus * longest;
     return n;
   };
   int64_t n = groups(false), segs = 1;
-  const int64_t full = c->tile[0].dp == 64 ? 2 * (int64_t)cus : cus;  // (work-groups of 64-value rows are half as large)
+  const bool small = c->tile[0].dp == 64;  // (work-groups of 64-value rows are half as large)
+  const int64_t full = small ? 2 * (int64_t)cus : cus;
   if (n > 0 && n < full) {
     const bool long_runs = n * chunks > 16 * (int64_t)cus;
-    const int64_t fine = groups(true);
-    if (fine >= (c->tile[0].dp == 64 ? cus : full)) {
+    int64_t fine = groups(true);
+    if (s.dtype == LSTM_F32 && (long_runs || !fits)) fine = groups(false);
+    if (fine >= (small ? cus : full)) {
       n = fine;
-    } else if (long_runs && c->tile[0].dp != 64) {
+    } else if (long_runs && !small) {
       n = groups(false);
       segs = (c->tile[0].dp == 256 ? 3 * full / 2 : 2 * full) / n;
     } else {
       n = fine;
-      segs = (runs > 1 ? 3 * full / 2 : full) / n;  // (the three runs of a backward do not end together)
+      const int64_t fill = c->tile[0].nw == 1 ? cus : full;
+      segs = (runs > 1 ? 3 * fill / 2 : fill) / n;  // (the three runs of a backward do not end together)
     }
     if (segs > most) segs = most;
     if (segs < 1) segs = 1;
@@ -100,6 +114,11 @@ __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
   const int d = e / x.DV, c = e - d * x.DV;
   float S = x.s_in ? x.s_in[head * n + d * x.s_dk + c * x.s_dv] : 0.f;
   float* at = x.seg + head * args.segs * n + e;
+  // decays of whole segments, of the one in which the sequence ends, of those past it
+  const int whole = (int)(end / args.seg_rows);
+  const float by_whole = __builtin_amdgcn_exp2f(ld2 * (float)args.seg_rows);
+  const int rest = (int)(end - whole * args.seg_rows);
+  const float by_rest = rest == 0 ? 1.f : __builtin_amdgcn_exp2f(ld2 * (float)rest);
   constexpr int kAhead = 8;
   for (int o0 = 0; o0 < args.segs; o0 += kAhead) {
     float own[kAhead];
@@ -107,13 +126,10 @@ __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
     for (int j = 0; j < kAhead; ++j) own[j] = o0 + j + 1 < args.segs ? at[(int64_t)(o0 + j) * n] : 0.f;
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int o = o0 + j;
+      const int o = o0 + j, seg = x.rev ? args.segs - 1 - o : o;
       if (o < args.segs) {
-        const int64_t seg = x.rev ? args.segs - 1 - o : o, r0 = seg * args.seg_rows;
-        int64_t rows = end - r0;
-        rows = rows < 0 ? 0 : rows < args.seg_rows ? rows : args.seg_rows;
         at[(int64_t)o * n] = S;
-        S = (rows == 0 ? S : S * __builtin_amdgcn_exp2f(ld2 * (float)rows)) + own[j];
+        S = S * (seg < whole ? by_whole : seg == whole ? by_rest : 1.f) + own[j];
       }
     }
   }
@@ -129,11 +145,11 @@ static hipError_t launch_runs(int dtype, const LinArgs& a, const LinTile& t, int
 hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const int* dma, hipStream_t s) {
   a.segs = c.segs;
   a.seg_rows = c.seg_rows;
-  // runs of one instance and kind share a launch
+  // runs of one instance share a launch, those that share the state.s update apart
   for (int pass = a.segs > 1 ? 0 : 1; pass < 2; ++pass) {
     auto alike = [&](int i, int j) {
       return c.tile[i].dp == c.tile[j].dp && c.tile[i].nw == c.tile[j].nw && c.tile[i].ks == c.tile[j].ks && dma[i] == dma[j] &&
-             (pass == 0 || (c.many[i] == c.many[j] && (a.run[i].gb > 1) == (a.run[j].gb > 1)));
+             (pass == 0 || c.many[i] == c.many[j]);
     };
     bool done[3] = {false, false, false};
     for (int i = 0; i < a.runs; ++i) {
@@ -143,8 +159,9 @@ hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const i
       l.state_only = pass == 0;
       l.segs_of_launch = pass == 0 ? a.segs - 1 : a.segs;
       int64_t groups = 0;
-      for (int j = i; j < a.runs; ++j) {
-        if (done[j] || !alike(i, j)) continue;
+      for (int k = 0; k < 2 * a.runs; ++k) {  // those of summed heads first: they take longest
+        const int j = k % a.runs;
+        if (done[j] || !alike(i, j) || (a.run[j].gb > 1) != (k < a.runs)) continue;
         done[j] = true;
         LinRun& r = l.run[l.runs++];
         r = a.run[j];

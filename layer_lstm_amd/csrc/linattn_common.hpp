@@ -140,14 +140,15 @@ __device__ __forceinline__ void stage_barrier() {
 template <typename T, int DP, int W, bool DMA>
 struct Rows32 {
   using TL = Tile<T, DP>;
-  static constexpr int kLoads = 32 * TL::C / 64 / W;  // loads of 1 KB a wave
-  static_assert(32 * TL::C / 64 % W == 0, "every wave has as many");
+  static constexpr int kAll = 32 * TL::C / 64, kLoads = kAll < W ? 1 : kAll / W;  // loads of 1 KB, of a wave
+  // (every wave has as many: where there are fewer than waves, some are made twice)
+  static_assert(kAll < W ? W % kAll == 0 : kAll % W == 0, "");
   int64_t st;
   int row_bytes, all_bytes;  // from row to row, of 32 rows
   int D, whole, w, lane;
   uint32_t off[kLoads];  // DMA: byte offset of this lane's chunk of each load
   __device__ __forceinline__ void init(int64_t st_, int D_, int whole_, int w_, int lane_) {
-    st = st_; D = D_; whole = whole_; w = w_; lane = lane_;
+    st = st_; D = D_; whole = whole_; w = w_ % kAll; lane = lane_;
     row_bytes = (int)st * (int)sizeof(T);
     all_bytes = 31 * row_bytes + D * (int)sizeof(T);
 #pragma unroll
@@ -156,14 +157,15 @@ struct Rows32 {
       off[j] = c * 16 < D * (int)sizeof(T) ? (uint32_t)(r * row_bytes + c * 16) : kNoRow;
     }
   }
+  template <bool FULL>
   __device__ __forceinline__ void load(const T* p, int rows, int shift, uint32_t lds) const {
     if constexpr (DMA) {
       // (uniform, which the compiler does not see through the loop's selects)
       const uint64_t at = (uint64_t)p;
       const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at), hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-      const int bytes = __builtin_amdgcn_readfirstlane(all_bytes - (32 - rows) * row_bytes);
+      const int bytes = FULL ? all_bytes : __builtin_amdgcn_readfirstlane(all_bytes - (32 - rows) * row_bytes);
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, bytes, 0x00020000);
-      const uint32_t back = (uint32_t)(shift * row_bytes);  // (a row before the first: an offset below 0, past the end)
+      const uint32_t back = FULL ? 0u : (uint32_t)(shift * row_bytes);  // (a row before the first: an offset below 0, past the end)
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) lds_dma16_at<false>(r, lds + (j * W + w) * 1024, off[j] - back, 0);
     } else {
@@ -184,14 +186,14 @@ constexpr int kAheadRows = 6, kAheadCols = 4;  // fragments read ahead of their 
 // alone, without rows a and outputs (kState).
 enum { kOne = 0, kSum = 1, kMany = 2, kState = 3 };
 // LDS: stages of an iteration's tiles -- a, k and v; in kMany a alone, and two
-// pairs of k and v.  KS = 2: half of each wave's part of O, for the other wave
-// of its columns, twice.
+// pairs of k and v.  KS > 1: what each wave hands to the other waves of its
+// columns, a KS-th of its part of O each, twice.
 template <typename T, int DP, int NW, int KS, int KIND>
 struct LinLds {
   static constexpr int kA = KIND == kState ? 0 : Tile<T, DP>::kBytes32;
   static constexpr int kKV = Tile<T, DP>::kBytes32 + Tile<T, 32 * NW>::kBytes32;
   static constexpr int kStage = KIND == kMany ? kA : kA + kKV;
-  static constexpr int kPass = KS == 2 && KIND != kState ? 2 * NW * KS * 2048 : 0;
+  static constexpr int kPass = KS > 1 && KIND != kState ? 2 * NW * KS * (KS - 1) * (4096 / KS) : 0;
   static constexpr int kPairs = KIND == kMany ? 2 * kKV : 0;
   // three stages where they fit a compute unit; two of small tiles, for more
   // work-groups (64 sequences, 16 heads of 64, 256 steps, bf16: forward 29.5 us,
@@ -202,11 +204,12 @@ struct LinLds {
 };
 
 template <typename T, int DP, int NW, int KS, bool DMA, int KIND>
-__global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 2) linattn_kernel(LinArgs args) {
+__global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : DP == 64 && KIND == kOne ? 3 : 2)
+linattn_kernel(LinArgs args) {
   using TK = StateTile<T, DP>;
   using TV = StateTile<T, 32 * NW>;
   using LL = LinLds<T, DP, NW, KS, KIND>;
-  constexpr bool kHalf = std::is_same<T, f16_t>::value, state_only = KIND == kState, kSplit = KS == 2 && !state_only;
+  constexpr bool kHalf = std::is_same<T, f16_t>::value, state_only = KIND == kState, kSplit = KS > 1 && !state_only;
   constexpr int NST = LL::kStages;
   constexpr int NDT = DP / 32 / KS, KB = TK::KB / KS, PB = TK::PB, EB = vec_of<T>();
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -221,8 +224,8 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
   while (which + 1 < args.runs && u >= args.run[which + 1].group0) ++which;
   const LinRun& x = args.run[which];
   u -= x.group0;
-  const uint32_t share = x.dv_blocks * (KIND == kOne ? x.ga : 1), slot = (u >> 3) / share, member = (u >> 3) - slot * share;
-  const int dvb = (int)(member % x.dv_blocks), ha = (int)(member / x.dv_blocks);  // (ha: 0 but in kOne)
+  const uint32_t share = x.dv_blocks * (KIND == kOne || KIND == kSum ? x.ga : 1), slot = (u >> 3) / share, member = (u >> 3) - slot * share;
+  const int dvb = (int)(member % x.dv_blocks), ha = (int)(member / x.dv_blocks);  // (ha: 0 in kMany, kState)
   uint32_t set = slot * 8 + (u & 7);
   if (set >= (uint32_t)args.B * args.Hs * args.segs_of_launch) return;
   const int hs = (int)(set % args.Hs);
@@ -292,11 +295,12 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
   const bool state_out = x.s_out != nullptr && ha == 0;
   // (this wave's rows of the state: k-blocks from part KB of a, tiles from part NDT of k)
   static_assert(KB % 4 == 0 || KB == 2, "");
-  const uint32_t row_first = KB % 4 == 0 ? TK::row_first(lane) + 128 * (part * KB / 4) : TK::row_first(lane) ^ (64 * part);
+  const uint32_t row_first = KB % 4 == 0 ? TK::row_first(lane) + 128 * (part * KB / 4)
+                                         : (TK::row_first(lane) ^ (64 * (part & 1))) + 128 * (part >> 1);
   uint32_t col_first = TK::col_first(lane, true);
   if constexpr (sizeof(T) == 4) col_first += 128 * part * NDT;
   else if constexpr (NDT % 2 == 0) col_first += 64 * part * NDT;
-  else col_first ^= 64 * part;
+  else col_first = (col_first ^ (64 * (part & 1))) + 128 * (part >> 1);
   const uint32_t v_first = (TV::col_first(lane, false) + (sizeof(T) == 2 ? (w >> 1) * 128 : w * 128)) ^
                            (sizeof(T) == 2 ? (w & 1) * 64 : 0);  // columns 32 w ..
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_t*)lds;
@@ -328,14 +332,19 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
   auto chunk_steps = [&](int left) __attribute__((always_inline)) { return rev ? ((left - 1) & 31) + 1 : left < 32 ? left : 32; };
   auto load = [&]() __attribute__((always_inline)) {
     const int rows = chunk_steps(left), shift = rev ? 0 : 32 - rows;
-    if constexpr (!state_only) la.load(KIND == kMany ? a0 + lh * a_head : a0, rows, shift, l_at);
-    if (KIND != kMany || lg == 0) {
-      const uint32_t kv = KIND == kMany ? l_kv : l_at + LL::kA;
-      const bool sum = KIND == kSum || state_only;
-      lk.load(sum ? k0 + lh * k_head : k0, rows, shift, kv);
-      lv.load(sum ? v0 + lh * v_head : v0, rows, shift, kv + TK::kBytes32);
-      if constexpr (KIND == kMany) l_kv = l_kv == lds0 + LL::kAtPairs ? l_kv + LL::kKV : lds0 + LL::kAtPairs;
-    }
+    const uint32_t kv = KIND == kMany ? l_kv : l_at + LL::kA;
+    const bool sum = KIND == kSum || state_only, pair = KIND != kMany || lg == 0;
+    auto each = [&](auto full) __attribute__((always_inline)) {
+      constexpr bool kFull = decltype(full)::value;
+      if constexpr (!state_only) la.template load<kFull>(KIND == kMany ? a0 + lh * a_head : a0, rows, shift, l_at);
+      if (pair) {
+        lk.template load<kFull>(sum ? k0 + lh * k_head : k0, rows, shift, kv);
+        lv.template load<kFull>(sum ? v0 + lh * v_head : v0, rows, shift, kv + TK::kBytes32);
+      }
+    };
+    if (DMA && rows == 32) each(std::true_type{});
+    else each(std::false_type{});
+    if (KIND == kMany && pair) l_kv = l_kv == lds0 + LL::kAtPairs ? l_kv + LL::kKV : lds0 + LL::kAtPairs;
     l_at = l_at == lds0 + (NST - 1) * LL::kStage ? lds0 : l_at + LL::kStage;
     if (KIND != kOne) lh = lh + 1 == heads ? 0 : lh + 1;
     if (KIND == kOne || ++lg == heads) {
@@ -348,13 +357,14 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
   };
 
   // ---- stores ----
-  constexpr int kKeep = kSplit ? 8 : 16;  // registers of O that this wave stores
+  constexpr int kKeep = kSplit ? 16 / KS : 16;  // registers of O that this wave stores
+  constexpr int kGive = 256 * kKeep, kPassed = NW * KS * (KS - 1) * kGive;  // bytes for another wave, of all waves
   float keep_o[kKeep];
-  T* out = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha) * x.os.h + dv0 + 32 * w + (kSplit ? 16 * part : 0) +
+  T* out = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha) * x.os.h + dv0 + 32 * w + (kSplit ? 32 / KS * part : 0) +
            (first_row + ri) * x.os.t;
   const int64_t o_row = x.os.t, o_next = next * o_row;
   int sh = rot, sg = 0;  // of the next store: head, heads of the chunk stored
-  const int out_cols = cols - 32 * w - (kSplit ? 16 * part : 0);  // (may be below 0: no columns)
+  const int out_cols = cols - 32 * w - (kSplit ? 32 / KS * part : 0);  // (may be below 0: no columns)
   const bool whole_o = (x.whole & kWholeO) && out_cols >= 2 * kKeep;
   uint32_t pass = lds0 + LL::kAtPass;
   // O of the iteration before, a chunk of n steps, to where `out` stands
@@ -363,18 +373,20 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
     T* p = n < 32 && !rev ? out - (32 - n) * o_row : out;
     if constexpr (KIND == kMany) p += sh * x.os.h;
     if constexpr (kSplit) {
-      const uint32_t at = pass + (w + NW * (1 - part)) * 2048 + lane * 16;
+      const uint32_t at = pass + wave * (KS - 1) * kGive + lane * 16;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < (KS - 1) * kKeep / 4; ++i) {
         float y[4];
         unpack<float>(*(lds_vec_t*)(uintptr_t)(at + i * 1024), y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) keep_o[4 * i + j] += y[j];
+        for (int j = 0; j < 4; ++j) keep_o[4 * (i % (kKeep / 4)) + j] += y[j];
       }
-      pass = pass == lds0 + LL::kAtPass ? pass + NW * KS * 2048 : lds0 + LL::kAtPass;
+      pass = pass == lds0 + LL::kAtPass ? pass + kPassed : lds0 + LL::kAtPass;
     }
     if (whole_o) {
-      if constexpr (sizeof(T) == 2) {
+      if constexpr (sizeof(T) == 2 && kKeep == 4) {
+        if (there) *(uint2*)(p + 4 * (lane >> 5)) = make_uint2(pack2<T>(keep_o[0], keep_o[1]), pack2<T>(keep_o[2], keep_o[3]));
+      } else if constexpr (sizeof(T) == 2) {
         u32x4_t q[kKeep / 8];
 #pragma unroll
         for (int i = 0; i < kKeep / 8; ++i) {
@@ -408,18 +420,24 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
     }
   };
   // O is complete: what this wave stores stays, the rest goes to the other
-  // wave of its columns
+  // waves of its columns
   auto hand_over = [&](const f32x16_t& O) __attribute__((always_inline)) {
     if constexpr (kSplit) {
-      const uint32_t at = pass + wave * 2048 + lane * 16;
-      float give[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        keep_o[i] = part ? O[8 + i] : O[i];
-        give[i] = part ? O[i] : O[8 + i];
+      for (int p = 0; p < KS; ++p) {
+        if (p == part) {
+#pragma unroll
+          for (int i = 0; i < kKeep; ++i) keep_o[i] = O[kKeep * p + i];
+        } else {
+          // (of KS - 1 places of wave (w, p), the one for its part's distance)
+          const uint32_t at = pass + ((w + NW * p) * (KS - 1) + ((part - p + KS) % KS - 1)) * kGive + lane * 16;
+          float give[kKeep];
+#pragma unroll
+          for (int i = 0; i < kKeep; ++i) give[i] = O[kKeep * p + i];
+#pragma unroll
+          for (int i = 0; i < kKeep / 4; ++i) *(lds_vec_t*)(uintptr_t)(at + i * 1024) = pack<float>(give + 4 * i);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) *(lds_vec_t*)(uintptr_t)(at + i * 1024) = pack<float>(give + 4 * i);
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) keep_o[i] = O[i];
@@ -430,6 +448,13 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i)
     if (i < iters) load();
+  // The state is here: a wait left to its first use would stand in the loop, and
+  // there wait for every chunk's loads (8 sequences, 16 heads of 128, 4096 steps,
+  // bf16, forward: 266 us, so 229).
+#pragma unroll
+  for (int dt = 0; dt < NDT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+v"(S[dt][i]));
 
   f32x16_t O = zero16();
   float s_by = 1.f, undo = 1.f;       // fp16: of the state as an operand
@@ -463,8 +488,58 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
                    v_at = kv + TK::kBytes32 + v_first;
     const int n = chunk_steps(togo);
 
-    if constexpr (!state_only) {
+    // V weighted for the state's sum, in 16 bits as two numbers (fp16 to 2^-22,
+    // bf16 to 2^-17) and in bf16 as a third where the state is an fp32 output;
+    // done between the products of the rows, which it covers
+    constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
+    u32x4_t vf[PB], vw[PB][kParts];
+    float most_v = 0.f, vx[kHalf ? PB : 1][EB];
+    const bool update = KIND != kMany || last;
+    auto split = [&](int pb, float* f) __attribute__((always_inline)) {
+      vw[pb][0] = pack<T>(f);
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) {  // what the number before has rounded away
+        if (i == 2 && !state_out) break;
+        float r[EB];
+        unpack<T>(vw[pb][i - 1], r);
+#pragma unroll
+        for (int e = 0; e < EB; ++e) f[e] -= r[e];
+        vw[pb][i] = pack<T>(f);
+      }
+    };
+    auto weigh = [&](int pb) __attribute__((always_inline)) {
+      if (!update) return;
+      float f[EB];
+      unpack<T>(vf[pb], f);
+#pragma unroll
+      for (int e = 0; e < EB; ++e) f[e] *= wv[pb][e];
+      if constexpr (kHalf) {
+#pragma unroll
+        for (int e = 0; e < EB; ++e) {
+          vx[pb][e] = f[e];
+          most_v = fmaxf(most_v, fabsf(f[e]));
+        }
+      } else {
+        split(pb, f);
+      }
+    };
+    auto read_v = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) vf[pb] = TV::col_at(v_at, TK::KR * pb, 0);
+    };
+
+    if constexpr (state_only) {
+      read_v();
+#pragma unroll
+      for (int pb = 0; pb < PB; ++pb) weigh(pb);
+    } else {
       f32x16_t P = zero16();
+      // fragments of V are weighed after the products of these k-blocks
+      auto weigh_at = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int pb = 0; pb < PB; ++pb)
+          if (kb == ((pb + 1) * KB + PB - 1) / PB - 1) weigh(pb);
+      };
       // rows of a and k in turn, k-block by k-block
       u32x4_t af;
       Ahead<2 * KB, kAheadRows> rows;
@@ -489,6 +564,7 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
         }
         O = zero16();
         rows.start(read_rows);
+        read_v();
         rows.run(read_rows, [&](int f, u32x4_t q) __attribute__((always_inline)) {
           const int kb = f >> 1;
           if (!(f & 1)) {
@@ -498,6 +574,7 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
           const u32x4_t sf = KIND == kMany ? s_op[kb] : state_operand(kb);
           P = Mm<T>::mac(q, af, P);
           O = Mm<T>::mac(sf, af, O);
+          weigh_at(kb);
         });
         float f = since32;
         if (n < 32) {
@@ -509,9 +586,14 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
         for (int i = 0; i < 16; ++i) O[i] *= f;
       } else {
         rows.start(read_rows);
+        read_v();
         rows.run(read_rows, [&](int f, u32x4_t q) __attribute__((always_inline)) {
-          if (f & 1) P = Mm<T>::mac(q, af, P);
-          else af = q;
+          if (!(f & 1)) {
+            af = q;
+            return;
+          }
+          P = Mm<T>::mac(q, af, P);
+          weigh_at(f >> 1);
         });
       }
 #pragma unroll
@@ -529,7 +611,7 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
         }
       }
 #pragma unroll
-      for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(TV::col_at(v_at, TK::KR * pb, 0), TK::reg_frag(P, pb), O);
+      for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(vf[pb], TK::reg_frag(P, pb), O);
       if constexpr (kHalf) {
         const float un = __uint_as_float((254u << 23) - __float_as_uint(by));  // 1 / by, a power of two
 #pragma unroll
@@ -538,50 +620,23 @@ __global__ void __launch_bounds__(64 * NW * KS, DP * sizeof(T) / KS > 256 ? 1 : 
       if (KIND != kSum || last) hand_over(O);
     }
 
-    if (KIND != kMany || last) {
-      // the state's sum: V weighted, in 16 bits as two numbers (fp16 to 2^-22,
-      // bf16 to 2^-17) and in bf16 as a third where the state is an fp32 output
-      float f[PB][EB];
-#pragma unroll
-      for (int pb = 0; pb < PB; ++pb) {
-        unpack<T>(TV::col_at(v_at, TK::KR * pb, 0), f[pb]);
-#pragma unroll
-        for (int e = 0; e < EB; ++e) f[pb][e] *= wv[pb][e];
-      }
+    if (update) {
       float keep = (KIND == kSum || state_only) && !first ? 1.f : n < 32 ? power(ld2, n) : keep32;
       if constexpr (kHalf) {
-        float most = 0.f;
-#pragma unroll
-        for (int pb = 0; pb < PB; ++pb)
-#pragma unroll
-          for (int e = 0; e < EB; ++e) most = fmaxf(most, fabsf(f[pb][e]));
-        const float to = lift_of(most);
+        const float to = lift_of(most_v);
         keep *= to / lift;
         lift = to;
 #pragma unroll
-        for (int pb = 0; pb < PB; ++pb)
+        for (int pb = 0; pb < PB; ++pb) {
 #pragma unroll
-          for (int e = 0; e < EB; ++e) f[pb][e] *= to;
+          for (int e = 0; e < EB; ++e) vx[pb][e] *= to;
+          split(pb, vx[pb]);
+        }
       }
 #pragma unroll
       for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; ++i) S[dt][i] *= keep;
-      constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
-      u32x4_t vw[PB][kParts];
-#pragma unroll
-      for (int pb = 0; pb < PB; ++pb) {
-        vw[pb][0] = pack<T>(f[pb]);
-#pragma unroll
-        for (int i = 1; i < kParts; ++i) {  // what the number before has rounded away
-          if (i == 2 && !state_out) break;
-          float r[EB];
-          unpack<T>(vw[pb][i - 1], r);
-#pragma unroll
-          for (int e = 0; e < EB; ++e) f[pb][e] -= r[e];
-          vw[pb][i] = pack<T>(f[pb]);
-        }
-      }
       Ahead<PB * NDT, kAheadCols> kcols;
       auto read_cols = [&](int i) __attribute__((always_inline)) { return TK::col_at(cols_at, TK::KR * (i / NDT), i % NDT); };
       kcols.start(read_cols);
@@ -652,8 +707,9 @@ static hipError_t linattn_launch(const LinArgs& a, unsigned groups, hipStream_t 
 template <typename T, int DP, int NW, int KS, bool DMA>
 static hipError_t linattn_kind(const LinArgs& a, int many, unsigned groups, hipStream_t s) {
   if (a.state_only) return linattn_launch<T, DP, NW, KS, DMA, kState>(a, groups, s);
-  // (every run of the launch is of one kind)
-  if (a.run[0].gb > 1) return linattn_launch<T, DP, NW, KS, DMA, kSum>(a, groups, s);
+  // (kSum does runs of kOne too)
+  for (int i = 0; i < a.runs; ++i)
+    if (a.run[i].gb > 1) return linattn_launch<T, DP, NW, KS, DMA, kSum>(a, groups, s);
   if (many) return linattn_launch<T, DP, NW, KS, DMA, kMany>(a, groups, s);
   return linattn_launch<T, DP, NW, KS, DMA, kOne>(a, groups, s);
 }
@@ -674,7 +730,7 @@ static hipError_t linattn_of(const LinArgs& a, const LinTile& t, int many, int d
     if (t.dp == 128) return linattn_loads<T, 128, 4, 1>(a, many, dma, groups, s);
     return linattn_loads<T, 256, 4, 2>(a, many, dma, groups, s);
   } else {
-    return hipErrorInvalidValue;  // (linattn_tile)
+    return linattn_loads<T, 128, 1, 4>(a, many, dma, groups, s);
   }
 }
 
