@@ -145,7 +145,7 @@ static hipError_t launch_runs(int dtype, const LinArgs& a, const LinTile& t, int
 hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const int* dma, hipStream_t s) {
   a.segs = c.segs;
   a.seg_rows = c.seg_rows;
-  // runs of one instance share a launch, those that share the state.s update apart
+  // runs of one instance share a launch, those that share the state's update apart
   for (int pass = a.segs > 1 ? 0 : 1; pass < 2; ++pass) {
     auto alike = [&](int i, int j) {
       return c.tile[i].dp == c.tile[j].dp && c.tile[i].nw == c.tile[j].nw && c.tile[i].ks == c.tile[j].ks && dma[i] == dma[j] &&
@@ -158,7 +158,7 @@ hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const i
       l.runs = 0;
       l.state_only = pass == 0;
       l.segs_of_launch = pass == 0 ? a.segs - 1 : a.segs;
-      int64_t groups = 0;
+      l.share = 0;
       for (int k = 0; k < 2 * a.runs; ++k) {  // those of summed heads first: they take longest
         const int j = k % a.runs;
         if (done[j] || !alike(i, j) || (a.run[j].gb > 1) != (k < a.runs)) continue;
@@ -166,10 +166,10 @@ hipError_t launch_linattn(const LinPlan& p, const LinCall& c, LinArgs a, const i
         LinRun& r = l.run[l.runs++];
         r = a.run[j];
         r.dv_blocks = (r.DV + 32 * c.tile[j].nw - 1) / (32 * c.tile[j].nw);
-        r.group0 = (uint32_t)groups;
-        const int64_t sets = (int64_t)a.B * a.Hs * l.segs_of_launch;
-        groups += (sets + 7) / 8 * 8 * r.dv_blocks * (pass == 0 || c.many[j] ? 1 : r.ga);
+        r.member0 = l.share;
+        l.share += r.dv_blocks * (pass == 0 || c.many[j] ? 1 : r.ga);
       }
+      const int64_t groups = ((int64_t)a.B * a.Hs * l.segs_of_launch + 7) / 8 * 8 * l.share;
       const hipError_t e = launch_runs(p.dtype, l, c.tile[i], c.many[i], dma[i], groups, s);
       if (e != hipSuccess) return e;
     }

@@ -216,15 +216,16 @@ linattn_kernel(LinArgs args) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = wave % NW, part = wave / NW;  // columns, rows of the state
 
-  // Which run, and which (sequence, head, columns, segment) of it: the work-
-  // groups that read the same k and v (columns of a head, heads of a that share
-  // a state) are dealt to one XCD (work-groups go to the XCDs round robin).
-  uint32_t u = blockIdx.x;
+  // Which (sequence, head, segment), and which run, columns and head of a of it:
+  // the work-groups that read the same rows (columns of a head, heads of a that
+  // share a state, the three runs of a backward) are dealt to one XCD, one after
+  // the other (work-groups go to the XCDs round robin).
+  const uint32_t u = blockIdx.x, slot = (u >> 3) / args.share;
+  uint32_t member = (u >> 3) - slot * args.share;
   int which = 0;
-  while (which + 1 < args.runs && u >= args.run[which + 1].group0) ++which;
+  while (which + 1 < args.runs && member >= args.run[which + 1].member0) ++which;
   const LinRun& x = args.run[which];
-  u -= x.group0;
-  const uint32_t share = x.dv_blocks * (KIND == kOne || KIND == kSum ? x.ga : 1), slot = (u >> 3) / share, member = (u >> 3) - slot * share;
+  member -= x.member0;
   const int dvb = (int)(member % x.dv_blocks), ha = (int)(member / x.dv_blocks);  // (ha: 0 in kMany, kState)
   uint32_t set = slot * 8 + (u & 7);
   if (set >= (uint32_t)args.B * args.Hs * args.segs_of_launch) return;
@@ -493,6 +494,7 @@ linattn_kernel(LinArgs args) {
     // done between the products of the rows, which it covers
     constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
     u32x4_t vf[PB], vw[PB][kParts];
+    float un = 1.f;  // fp16: O's factor before it is complete
     float most_v = 0.f, vx[kHalf ? PB : 1][EB];
     const bool update = KIND != kMany || last;
     auto split = [&](int pb, float* f) __attribute__((always_inline)) {
@@ -612,12 +614,7 @@ linattn_kernel(LinArgs args) {
       }
 #pragma unroll
       for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(vf[pb], TK::reg_frag(P, pb), O);
-      if constexpr (kHalf) {
-        const float un = __uint_as_float((254u << 23) - __float_as_uint(by));  // 1 / by, a power of two
-#pragma unroll
-        for (int i = 0; i < 16; ++i) O[i] *= un;
-      }
-      if (KIND != kSum || last) hand_over(O);
+      if constexpr (kHalf) un = __uint_as_float((254u << 23) - __float_as_uint(by));  // 1 / by, a power of two
     }
 
     if (update) {
@@ -647,6 +644,14 @@ linattn_kernel(LinArgs args) {
         if constexpr (kParts > 2)
           if (state_out) s = Mm<T>::mac(kf, vw[i / NDT][2], s);
       });
+    }
+    // (last, when the products are done: the state's cover them)
+    if constexpr (!state_only) {
+      if constexpr (kHalf) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[i] *= un;
+      }
+      if (KIND != kSum || last) hand_over(O);
     }
     n_before = n;
     u_at = u_at == lds0 + (NST - 1) * LL::kStage ? lds0 : u_at + LL::kStage;

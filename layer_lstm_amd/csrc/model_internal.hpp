@@ -22,11 +22,12 @@ struct LinRun {
   float* seg;       // [B][Hs][segs][DK][DV] states at the segments' starts
   int whole;        // kWholeQ / K / V / O of a, k, v, out
   int dv_blocks;    // work-groups a head's columns are split over
-  uint32_t group0;  // first work-group of the run in its launch, a multiple of 8
+  uint32_t member0;  // first of its work-groups among a state's
 };
 struct LinArgs {
   LinRun run[3];
   int runs;
+  uint32_t share;  // work-groups of the launch for a state (and segment), of all runs
   int64_t T;
   int B, Hs;
   const float* log_decay;  // [Hs]
