@@ -544,7 +544,8 @@ linattn_kernel(LinArgs args) {
       };
       // rows of a and k in turn, k-block by k-block
       u32x4_t af;
-      Ahead<2 * KB, kAheadRows> rows;
+      // (fewer where the registers are full)
+      Ahead<2 * KB, NDT * sizeof(T) >= 8 && KIND != kOne ? kAheadRows - 2 : kAheadRows> rows;
       auto read_rows = [&](int f) __attribute__((always_inline)) { return TK::row_at(f & 1 ? keys_at : rows_at, f >> 1); };
       if (KIND != kSum || first) {
         if constexpr (kHalf) {
@@ -670,10 +671,18 @@ linattn_kernel(LinArgs args) {
     }
     // steps past the end
     const int64_t top = r0 + args.seg_rows < args.T ? r0 + args.seg_rows : args.T;
-    for (int64_t row = r1 + wave; row < top; row += NW * KS)
+    T* p0 = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha) * x.os.h + dv0;
+    constexpr int kChunks = 32 * NW / EB, kRows = 64 * NW * KS / kChunks;  // of 16 bytes a row, rows at a time
+    const bool chunks = (x.whole & kWholeO) != 0;
+    const int tid = wave * 64 + tile_lane<true>(lane), c = tid % kChunks * EB;
+    for (int64_t row = r1 + tid / kChunks; row < top; row += kRows)
       for (int k = 0; k < (KIND == kMany ? x.ga : 1); ++k) {
-        T* p = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha + k) * x.os.h + dv0 + row * x.os.t;
-        for (int d = lane; d < 32 * NW && d < cols; d += 64) p[d] = Elem<T>::from_f(0.f);
+        T* p = p0 + k * x.os.h + row * x.os.t + c;
+        if (chunks) {
+          if (c < cols) *(u32x4_t*)p = u32x4_t{0, 0, 0, 0};
+        } else {
+          for (int d = 0; d < EB && c + d < cols; ++d) p[d] = Elem<T>::from_f(0.f);
+        }
       }
   }
   // the state after the run, or the segment's own sum
