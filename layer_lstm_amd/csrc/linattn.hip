@@ -28,15 +28,16 @@ static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
 // head of more than 64), then the time axis into segments of four chunks at
 // least, whose own sums a launch before has to find (k and v read twice).
 // (8 sequences, 16 heads of 128, 4096 steps, bf16, forward, us: 128 work-groups
-// 226, two a head 180, four segments 202; 2 sequences, 4 heads: 202, 172, 16
-// segments of two a head 37, of one 43.)  Where the segments have many chunks to
-// go, whole heads (32768 steps, 32/8 heads, fp16: 235 and 372).  Heads that share
-// a state take one work-group (one update of the state for all of them) unless
-// that leaves compute units idle (8 sequences, 6/3 heads of 80, 191 steps, fp32:
-// 56 us, heads apart 32; 32 sequences, 32/8 heads, 1024 steps, fp16: 206, apart 260).
-// fp32's instance for few work-groups has a compute unit to itself: it is taken
-// where all of them have one, and no run is long (forward and backward of the
-// fp32 case above 115 us, so 53).
+// 210, two a head 181, four segments 202; 2 sequences, 4 heads: 204, 159, 16
+// segments of two a head 35, of one 42.)  Where the segments have many chunks to
+// go, whole heads (32768 steps, 32/8 heads, fp16: 223, two a head 284).  Heads
+// that share a state take one work-group (one update of the state for all of
+// them) unless that leaves compute units idle (8 sequences, 6/3 heads of 80, 191
+// steps, fp32: 56 us, heads apart 32; 32 sequences, 32/8 heads, 1024 steps, fp16:
+// 201, apart 255).  fp32's instance for few work-groups has a compute unit to
+// itself: it is taken where all of them have one, and no run is long (forward
+// and backward of the fp32 case above 83 us, so 65; 32 heads of 64, 8192 steps,
+// cut into segments either way 466 and 900).
 static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int64_t (*sizes)[3], LinCall* c) {
   const int64_t sets = s.B * s.Hk, chunks = (s.T + 31) / 32, most = chunks / 4 > 1 ? chunks / 4 : 1;
   bool fits = true;  // the device has a compute unit for all work-groups, or for the next when the short ones end

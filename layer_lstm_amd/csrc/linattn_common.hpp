@@ -34,6 +34,15 @@ namespace lstm {
 // columns have parts of O, which they add up through LDS; the next chunk's
 // barrier is theirs too).  Passing P round instead would cost two barriers for
 // 8 of a wave's 34 products (rows of 128 16-bit values, KS = 1).
+//
+// What bounds it: instruction issue.  A chunk of 32 steps of 128-value bf16 rows
+// is some 300 vector instructions a wave and column tile (weighing and splitting
+// V 80 to 120, scaling and rounding the state 96, P and O 60) beside its 34
+// matrix instructions, which keep the matrix units 24 to 34 % busy, and the
+// memory's traffic is below half the copy's rate forwards (8 sequences, 16 heads
+// of 128, 4096 steps: 185 us, 2.9 TB/s; the same with rows that stay in L2) and
+// 4.2 TB/s backwards (355 us).  fp32 is bound by the chain of its matrix
+// instructions.
 // The state as the operand of the first product of O^T has its k index down
 // the registers too; in 16 bits the columns of K are read in the order (bits 2
 // and 3 of the index exchanged) that leaves its rows in row_frag's order.
@@ -196,8 +205,8 @@ struct LinLds {
   static constexpr int kPass = KS > 1 && KIND != kState ? 2 * NW * KS * (KS - 1) * (4096 / KS) : 0;
   static constexpr int kPairs = KIND == kMany ? 2 * kKV : 0;
   // three stages where they fit a compute unit; two of small tiles, for more
-  // work-groups (64 sequences, 16 heads of 64, 256 steps, bf16: forward 29.5 us,
-  // backward 70, with three 31.5 and 78)
+  // work-groups (64 sequences, 16 heads of 64, 256 steps, bf16: forward 27 us,
+  // backward 54, with three 28 and 64)
   static constexpr int kStages = (KIND != kMany && kStage <= 12 * 1024) || 3 * kStage + kPairs + kPass > 160 * 1024 ? 2 : 3;
   static constexpr int kAtPairs = kStages * kStage, kAtPass = kAtPairs + kPairs, kBytes = kAtPass + kPass;
   static_assert(kBytes <= 160 * 1024, "a compute unit's LDS");
@@ -321,20 +330,15 @@ linattn_kernel(LinArgs args) {
   // (32 rows of a tile that a descriptor reaches are below 2^30 bytes)
   typedef typename std::conditional<DMA, int, int64_t>::type step_t;
   const step_t a_next = (step_t)(next * x.as.t), k_next = (step_t)(next * x.ks.t), v_next = (step_t)(next * x.vs.t);
-  // A chunk's heads are taken from another one on in neighbouring work-groups:
-  // side by side in memory, all work-groups at the same one would keep to a part
-  // of the memory channels (32 heads of 128 in fp16, 4 a state, 32768 steps:
-  // 283 us at the same one, 235 so)
-  const int rot = heads > 1 ? (int)((uint32_t)(order + hs) % (uint32_t)heads) : 0;
   constexpr int kLoadsA = state_only ? 0 : decltype(la)::kLoads, kLoadsKV = decltype(lk)::kLoads + decltype(lv)::kLoads;
-  int left = steps, lg = 0, lh = rot;  // of the next load: steps not loaded yet, heads of the chunk loaded, head
+  int left = steps, lh = 0;  // of the next load: steps not loaded yet, head
   uint32_t l_at = lds0, l_kv = lds0 + LL::kAtPairs;
   // steps of a chunk with `left` to go (backwards the last one, of fewer, is the first)
   auto chunk_steps = [&](int left) __attribute__((always_inline)) { return rev ? ((left - 1) & 31) + 1 : left < 32 ? left : 32; };
   auto load = [&]() __attribute__((always_inline)) {
     const int rows = chunk_steps(left), shift = rev ? 0 : 32 - rows;
     const uint32_t kv = KIND == kMany ? l_kv : l_at + LL::kA;
-    const bool sum = KIND == kSum || state_only, pair = KIND != kMany || lg == 0;
+    const bool sum = KIND == kSum || state_only, pair = KIND != kMany || lh == 0;
     auto each = [&](auto full) __attribute__((always_inline)) {
       constexpr bool kFull = decltype(full)::value;
       if constexpr (!state_only) la.template load<kFull>(KIND == kMany ? a0 + lh * a_head : a0, rows, shift, l_at);
@@ -347,9 +351,8 @@ linattn_kernel(LinArgs args) {
     else each(std::false_type{});
     if (KIND == kMany && pair) l_kv = l_kv == lds0 + LL::kAtPairs ? l_kv + LL::kKV : lds0 + LL::kAtPairs;
     l_at = l_at == lds0 + (NST - 1) * LL::kStage ? lds0 : l_at + LL::kStage;
-    if (KIND != kOne) lh = lh + 1 == heads ? 0 : lh + 1;
-    if (KIND == kOne || ++lg == heads) {
-      lg = 0;
+    if (KIND == kOne || ++lh == heads) {
+      lh = 0;
       left -= rows;
       a0 += a_next;
       k0 += k_next;
@@ -364,7 +367,7 @@ linattn_kernel(LinArgs args) {
   T* out = (T*)x.out + b * x.os.b + ((int64_t)hs * x.ga + ha) * x.os.h + dv0 + 32 * w + (kSplit ? 32 / KS * part : 0) +
            (first_row + ri) * x.os.t;
   const int64_t o_row = x.os.t, o_next = next * o_row;
-  int sh = rot, sg = 0;  // of the next store: head, heads of the chunk stored
+  int sh = 0;  // head of the next store
   const int out_cols = cols - 32 * w - (kSplit ? 32 / KS * part : 0);  // (may be below 0: no columns)
   const bool whole_o = (x.whole & kWholeO) && out_cols >= 2 * kKeep;
   uint32_t pass = lds0 + LL::kAtPass;
@@ -414,9 +417,8 @@ linattn_kernel(LinArgs args) {
         if (d < out_cols) p[d] = Elem<T>::from_f(o);
       }
     }
-    if constexpr (KIND == kMany) sh = sh + 1 == heads ? 0 : sh + 1;
-    if (KIND != kMany || ++sg == heads) {
-      sg = 0;
+    if (KIND != kMany || ++sh == heads) {
+      sh = 0;
       out += o_next;
     }
   };

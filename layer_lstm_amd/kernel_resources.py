@@ -7,7 +7,8 @@ Compiles the kernel sources for gfx950 with the library's flags plus
 temporary folder; liblstm.so is not touched) and prints, for every kernel
 instance whose demangled name contains one of the --match strings (default:
 the instances the four workloads of layer_lstm_amd/synth.py launch; those of
-the sequence-to-sequence operators: --match attend_ embed_ logprob_):
+the sequence-to-sequence operators: --match attend_ embed_ logprob_; linear
+attention, penalties and AdamW: --match linattn_ penalty_ adamw_):
 
   - VGPRs, AGPRs, SGPRs, SGPRs spilled (to VGPR lanes), VGPRs spilled and
     scratch bytes per lane, as the compiler reports them;
@@ -41,7 +42,8 @@ sys.path.insert(0, ROOT)
 from layer_lstm_amd import build as _build  # noqa: E402
 
 SOURCES = ("recurrent.hip", "recurrent_bwd.hip", "recurrent_vec.hip", "gemm.hip", "embed.hip", "logprob.hip",
-           "attend.hip", "attend_bwd_f32.hip", "attend_bwd_bf16.hip", "attend_bwd_f16.hip")
+           "attend.hip", "attend_bwd_f32.hip", "attend_bwd_bf16.hip", "attend_bwd_f16.hip",
+           "linattn.hip", "linattn_f32.hip", "linattn_bf16.hip", "linattn_f16.hip", "penalty.hip", "adamw.hip")
 # kernel instances of the four workloads (rocprofv3 names, profiles/kernels_*.txt)
 DEFAULT_MATCH = (
     "fwd_rec_kernel<unsigned short, 2, 16, 0, 8, 2, false>",   # bf16_T256_B256_I1024_H1024
