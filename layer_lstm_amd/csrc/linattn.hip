@@ -29,7 +29,8 @@ static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
 // least, whose own sums a launch before has to find (k and v read twice).
 // (8 sequences, 16 heads of 128, 4096 steps, bf16, forward, us: 128 work-groups
 // 210, two a head 181, four segments 202; 2 sequences, 4 heads: 204, 159, 16
-// segments of two a head 35, of one 42.)  Where the segments have many chunks to
+// segments of two a head 35, of one 42.)  Two segments cost what they gain (4
+// sequences, 16 heads, 2048 steps: forward 82, in two 84, backward 115 and 152).  Where the segments have many chunks to
 // go, whole heads (32768 steps, 32/8 heads, fp16: 223, two a head 284).  Heads
 // that share a state take one work-group (one update of the state for all of
 // them) unless that leaves compute units idle (8 sequences, 6/3 heads of 80, 191
@@ -60,7 +61,7 @@ static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int6
   const bool small = c->tile[0].dp == 64;  // (work-groups of 64-value rows are half as large)
   const int64_t full = small ? 2 * (int64_t)cus : cus;
   if (n > 0 && n < full) {
-    const bool long_runs = n * chunks > 16 * (int64_t)cus;
+    const bool long_runs = n * chunks >= 16 * (int64_t)cus;
     int64_t fine = groups(true);
     if (s.dtype == LSTM_F32 && (long_runs || !fits)) fine = groups(false);
     if (fine >= (small ? cus : full)) {
@@ -74,7 +75,7 @@ static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int6
       segs = (runs > 1 ? 3 * fill / 2 : fill) / n;  // (the three runs of a backward do not end together)
     }
     if (segs > most) segs = most;
-    if (segs < 1) segs = 1;
+    if (segs < 3) segs = 1;
   }
   c->seg_rows = (chunks + segs - 1) / segs * 32;
   if (c->seg_rows == 0) c->seg_rows = 32;

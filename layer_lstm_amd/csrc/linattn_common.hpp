@@ -722,7 +722,9 @@ static hipError_t linattn_launch(const LinArgs& a, unsigned groups, hipStream_t 
 }
 template <typename T, int DP, int NW, int KS, bool DMA>
 static hipError_t linattn_kind(const LinArgs& a, int many, unsigned groups, hipStream_t s) {
-  if (a.state_only) return linattn_launch<T, DP, NW, KS, DMA, kState>(a, groups, s);
+  if constexpr (DP != 64 || KS > 1) {  // (a time axis is cut where work-groups are few)
+    if (a.state_only) return linattn_launch<T, DP, NW, KS, DMA, kState>(a, groups, s);
+  }
   // (kSum does runs of kOne too)
   for (int i = 0; i < a.runs; ++i)
     if (a.run[i].gb > 1) return linattn_launch<T, DP, NW, KS, DMA, kSum>(a, groups, s);
@@ -736,13 +738,13 @@ static hipError_t linattn_loads(const LinArgs& a, int many, int dma, unsigned gr
 template <typename T>
 static hipError_t linattn_of(const LinArgs& a, const LinTile& t, int many, int dma, unsigned groups, hipStream_t s) {
   switch (t.dp * 100 + t.nw * 10 + t.ks) {
-    case 64 * 100 + 21: return linattn_loads<T, 64, 2, 1>(a, many, dma, groups, s);
     case 64 * 100 + 22: return linattn_loads<T, 64, 2, 2>(a, many, dma, groups, s);
     case 128 * 100 + 22: return linattn_loads<T, 128, 2, 2>(a, many, dma, groups, s);
     case 256 * 100 + 22: return linattn_loads<T, 256, 2, 2>(a, many, dma, groups, s);
     default: break;
   }
   if constexpr (sizeof(T) == 2) {
+    if (t.dp == 64) return linattn_loads<T, 64, 2, 1>(a, many, dma, groups, s);
     if (t.dp == 128) return linattn_loads<T, 128, 4, 1>(a, many, dma, groups, s);
     return linattn_loads<T, 256, 4, 2>(a, many, dma, groups, s);
   } else {

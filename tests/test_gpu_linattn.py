@@ -101,6 +101,21 @@ def test_linear_attention(lstm, dt, T, B, Hq, Hk, D, Dv):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,B,Hq,Hk,D,Dv", [
+    (40, 130, 8, 4, 64, 48), (50, 140, 8, 4, 37, 51),      # small rows, many heads, shared
+    (40, 100, 6, 3, 33, 64), (40, 32, 4, 2, 128, 128),     # fewer than compute units hold; as many, cut by columns
+    (33, 70, 8, 4, 67, 99), (40, 70, 4, 4, 100, 64),
+    (400, 1, 3, 1, 33, 65), (2100, 4, 8, 4, 64, 64),       # segments; of heads that share a state
+    (191, 8, 6, 3, 80, 48), (191, 8, 6, 3, 41, 127),
+])
+def test_every_way_of_cutting_a_call(lstm, dt, T, B, Hq, Hk, D, Dv):
+    print(f"case: linear attention {dt} T={T} B={B} heads {Hq}/{Hk} D={D} Dv={Dv}", flush=True)
+    c, x = make(dt, T, B, Hq, Hk, D, Dv, seed=3)
+    _, o, S, g = run(lstm, dt, c)
+    check(dt, x, 0.37, o, S, g)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_without_states_and_lengths(lstm, dt):
     for T in (1, 50, 260):
         c, x = make(dt, T, 2, 2, 2, 64, 64, state=False, ragged=False)
