@@ -30,7 +30,10 @@ static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
 // (8 sequences, 16 heads of 128, 4096 steps, bf16, forward, us: 128 work-groups
 // 210, two a head 181, four segments 202; 2 sequences, 4 heads: 204, 159, 16
 // segments of two a head 35, of one 42.)  Two segments cost what they gain (4
-// sequences, 16 heads, 2048 steps: forward 82, in two 84, backward 115 and 152).  Where the segments have many chunks to
+// sequences, 16 heads, 2048 steps: forward 82, in two 84, backward 115 and 152),
+// and so do two work-groups a head that are more than the compute units (12
+// sequences, 16 heads, 2048 steps, forward: 121, two a head 133; 8 sequences, 8
+// heads, 1024 steps, fp16, backward: 73 and 88).  Where the segments have many chunks to
 // go, whole heads (32768 steps, 32/8 heads, fp16: 223, two a head 284).  Heads
 // that share a state take one work-group (one update of the state for all of
 // them) unless that leaves compute units idle (8 sequences, 6/3 heads of 80, 191
@@ -64,7 +67,9 @@ static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int6
     const bool long_runs = n * chunks >= 16 * (int64_t)cus;
     int64_t fine = groups(true);
     if (s.dtype == LSTM_F32 && (long_runs || !fits)) fine = groups(false);
-    if (fine >= (small ? cus : full)) {
+    if (fine > full && !small && s.dtype != LSTM_F32) {
+      n = groups(false);
+    } else if (fine >= (small ? cus : full)) {
       n = fine;
     } else if (long_runs && !small) {
       n = groups(false);
