@@ -33,13 +33,13 @@ static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
 // sequences, 16 heads, 2048 steps: forward 82, in two 84, backward 115 and 152),
 // and so do two work-groups a head that are more than the compute units (12
 // sequences, 16 heads, 2048 steps, forward: 121, two a head 133; 8 sequences, 8
-// heads, 1024 steps, fp16, backward: 73 and 88).  Where the segments have many chunks to
-// go, whole heads (32768 steps, 32/8 heads, fp16: 223, two a head 284).  Heads
-// that share a state take one work-group (one update of the state for all of
-// them) unless that leaves compute units idle (8 sequences, 6/3 heads of 80, 191
-// steps, fp32: 56 us, heads apart 32; 32 sequences, 32/8 heads, 1024 steps, fp16:
-// 201, apart 255).  fp32's instance for few work-groups has a compute unit to
-// itself: it is taken where all of them have one, and no run is long (forward
+// heads, 1024 steps, fp16, backward: 73 and 88).  Where the segments have many
+// chunks to go, whole heads (32768 steps, 32/8 heads, fp16: 223, two a head 284).
+// Heads that share a state take one work-group (one update of the state for all
+// of them) unless that leaves compute units idle (8 sequences, 6/3 heads of 80,
+// 191 steps, fp32: 56 us, heads apart 32; 32 sequences, 32/8 heads, 1024 steps,
+// fp16: 201, apart 255).  fp32's instance for few work-groups has a compute unit
+// to itself: it is taken where all of them have one, and no run is long (forward
 // and backward of the fp32 case above 83 us, so 65; 32 heads of 64, 8192 steps,
 // cut into segments either way 466 and 900).
 static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int64_t (*sizes)[3], LinCall* c) {
