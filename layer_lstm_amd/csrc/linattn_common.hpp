@@ -722,9 +722,7 @@ static hipError_t linattn_launch(const LinArgs& a, unsigned groups, hipStream_t 
 }
 template <typename T, int DP, int NW, int KS, bool DMA>
 static hipError_t linattn_kind(const LinArgs& a, int many, unsigned groups, hipStream_t s) {
-  if constexpr (DP != 64 || KS > 1) {  // (a time axis is cut where work-groups are few)
-    if (a.state_only) return linattn_launch<T, DP, NW, KS, DMA, kState>(a, groups, s);
-  }
+  if (a.state_only) return linattn_launch<T, DP, NW, KS, DMA, kState>(a, groups, s);
   // (kSum does runs of kOne too)
   for (int i = 0; i < a.runs; ++i)
     if (a.run[i].gb > 1) return linattn_launch<T, DP, NW, KS, DMA, kSum>(a, groups, s);

@@ -282,6 +282,15 @@ def test_same_bits_other_streams_and_graphs(lstm):
             assert all(torch.equal(a, b) for a, b in zip(want, got)), k
 
 
+@pytest.mark.parametrize("D,Dv", [(64, 128), (128, 64)])
+def test_segments_of_narrow_and_wide_rows(lstm, D, Dv):
+    """A long backward whose runs have different instances, all of them in segments."""
+    c, x = make("bf16", 2100, 4, 4, 4, D, Dv)
+    m, o, S, g = run(lstm, "bf16", c)
+    assert m._bwd_bytes > 0
+    check("bf16", x, 0.37, o, S, g)
+
+
 def test_a_captured_forward_keeps_its_workspace(lstm):
     """The first backward, after the capture, makes buffers: none of them the one that the replays write to."""
     T, B, H, D = 4000, 1, 1, 64
