@@ -17,6 +17,7 @@ namespace lstm {
 // and mask, us: 256 threads 47, slices of 4096 with 256 threads 39, of 16384 with
 // 512 53, so 38).
 constexpr int kPenThreads = 512;
+constexpr int64_t kPenGroups = (((int64_t)1 << 32) - 1) / kPenThreads;  // of a launch, which has fewer than 2^32 threads
 constexpr int kPenAhead = 2;         // 16-byte loads of logits a lane has under way
 constexpr int64_t kPenSlice = 8192;  // logits of a work-group at most
 
@@ -160,8 +161,8 @@ template <typename T>
 static hipError_t penalty_of(const PenaltyArgs& a, hipStream_t s) {
   const bool count = a.L > 0 && (a.repetition || a.presence || a.frequency);
   const int64_t groups = a.N * a.slices;
-  for (int64_t g = 0; g < groups; g += kMaxGroups) {
-    const unsigned n = (unsigned)(groups - g < kMaxGroups ? groups - g : kMaxGroups);
+  for (int64_t g = 0; g < groups; g += kPenGroups) {
+    const unsigned n = (unsigned)(groups - g < kPenGroups ? groups - g : kPenGroups);
     Timed timed(11, s);
     if (count) penalty_kernel<T, true><<<dim3(n), kPenThreads, (size_t)a.slice * 4, s>>>(a, g);
     else penalty_kernel<T, false><<<dim3(n), kPenThreads, 0, s>>>(a, g);
