@@ -919,7 +919,7 @@ class AdamW:
         if self.tdtype != torch.float32 and master is not False:
             self.master = torch.zeros(end, dtype=torch.float32, device=device)
             for p, at in zip(self.params, self.places):
-                self.master[at : at + p.numel()].copy_(p.reshape(-1))
+                self.master[at : at + p.numel()].copy_(p.detach().reshape(-1))
         self._table = (AdamwTensor * n)()
         each = self.m.element_size()
         for t, p, at, w in zip(self._table, self.params, self.places, decay):
