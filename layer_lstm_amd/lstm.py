@@ -486,6 +486,10 @@ def _stream_on(index, stream):
     return _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream)
 
 
+def _settle():
+    torch.cuda.current_stream().synchronize()
+
+
 def _workspace(fn, name, shape, device):
     n = ctypes.c_size_t(0)
     rc = fn(ctypes.byref(shape), ctypes.byref(n))
@@ -882,7 +886,9 @@ class AdamW:
 
     The states of all tensors lie in one buffer each (m, v, master; 8 bits: of
     torch.float8_e4m3fn, with m_scale and v_scale), tensor i's at
-    places[i]..., a multiple of ADAMW_BLOCK values.  lr may be changed between
+    places[i]..., a multiple of ADAMW_BLOCK values.  They are filled when the
+    constructor returns, whatever stream the steps go to; what is written into
+    them later is for the caller to order before a step.  lr may be changed between
     steps (a captured step keeps the one it was captured with); the parameters
     stay where they are in memory."""
 
@@ -945,12 +951,14 @@ class AdamW:
                 raise LstmError(rc, "lstm_adamw_query")
             self.workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
             self.control = torch.zeros(ctypes.sizeof(AdamwControl) // 8, dtype=torch.int64, device=device)
+        _settle()  # the states are filled before a step on any stream reads them
 
-    def set_step(self, t):
-        """t steps have been taken (0 at the start)."""
+    def set_step(self, t, stream=None):
+        """t steps have been taken (0 at the start); `stream`: the one that the next step goes to."""
         self.shape.step = int(t)
         if self.control is not None:
-            self.control[0] = int(t)
+            with torch.cuda.stream(stream):
+                self.control[0] = int(t)
 
     @property
     def norm(self):

@@ -11,6 +11,7 @@ def lstm(monkeypatch):
     zeros = torch.zeros
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(mod, "_on_device", lambda *a: None)
+    monkeypatch.setattr(mod, "_settle", lambda: None)
     monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
     return mod
 
