@@ -486,6 +486,11 @@ def _stream_on(index, stream):
     return _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream)
 
 
+def _capturing(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _settle():
     torch.cuda.current_stream().synchronize()
 
@@ -985,7 +990,7 @@ class AdamW:
                                       _ptr(self.workspace), self.workspace.numel(), control, st)
             if rc != OK:
                 raise LstmError(rc, "lstm_adamw_norm")
-        elif torch.cuda.is_current_stream_capturing():
+        elif _capturing(stream):
             raise ValueError("a step in a graph needs clip (math.inf: none): its number has to be on the device")
         else:
             s.step += 1

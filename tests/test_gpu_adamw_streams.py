@@ -39,3 +39,16 @@ def test_a_step_on_another_stream_comes_after_the_states_filling(lstm, bits):
     for n in ("m", "v", "m_scale", "v_scale"):
         x, y = getattr(opt, n), getattr(want, n)
         assert (x is None and y is None) or torch.equal(x.view(torch.uint8), y.view(torch.uint8)), n
+
+
+def test_a_step_into_another_streams_graph_needs_its_number_on_the_device(lstm):
+    """The stream that is captured is the one the step goes to, not the current one."""
+    p, grad = torch.randn(40, device="cuda"), torch.randn(40, device="cuda")
+    plain = lstm.AdamW([p], **OPT)
+    plain.step([grad])
+    graph, s, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        with torch.cuda.stream(other), pytest.raises(ValueError, match="graph"):
+            plain.step([grad], stream=s)
+    torch.cuda.synchronize()
+    assert plain.shape.step == 1
