@@ -517,8 +517,9 @@ int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const vo
  * repetition (> 0; 1 is none), presence, frequency: fp32 [N], NULL = none;
  * with none of the three the history is not read.  bias: fp32, NULL = none;
  * ld_bias 0 or >= V.  mask: 32-bit words, NULL = all allowed, ld_mask >=
- * ceil(V / 32).  out may be logits itself (ld = ld_out), else they do not
- * overlap.  N < 2^24, V < 2^30, N V < 2^37, L < 2^31. */
+ * ceil(V / 32).  out may be logits itself (ld = ld_out), or other columns of the
+ * same rows; else the memory from the first row to the last of one is not the
+ * other's (LSTM_ERR_DIMS).  N < 2^24, V < 2^30, N V < 2^37, L < 2^31. */
 typedef struct {
   int64_t N, V;
   int64_t ld, ld_out;

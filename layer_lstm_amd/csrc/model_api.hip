@@ -87,6 +87,17 @@ static int penalty_plan(const lstm_penalty_shape* s, PenaltyArgs* a) {
   return LSTM_OK;
 }
 
+// Rows of logits and out that are neither the same nor apart: in memory that is
+// not the other's, or other columns of the same rows.
+static bool penalty_overlap(const PenaltyArgs& a, const void* logits, const void* out, int64_t e) {
+  if (a.N == 0 || a.V == 0 || (logits == out && a.ld == a.ldo)) return false;
+  const int64_t x = (int64_t)(uintptr_t)logits, y = (int64_t)(uintptr_t)out;
+  if (y >= x + ((a.N - 1) * a.ld + a.V) * e || x >= y + ((a.N - 1) * a.ldo + a.V) * e) return false;
+  if (a.ld != a.ldo || a.N == 1) return true;
+  const int64_t row = a.ld * e, d = ((y - x) % row + row) % row;
+  return d < a.V * e || d > row - a.V * e;
+}
+
 // The step's or the norm's arguments; the norm reads grad and n alone.
 static int adamw_plan(const lstm_adamw_shape* s, const lstm_adamw_tensor* t, int64_t count, bool step, bool control,
                       AdamwPlan* p) {
@@ -225,6 +236,7 @@ int lstm_penalty(const lstm_penalty_shape* shape, const void* logits, const void
   if (off_size(logits, e) || off_size(out, e) || off_size(history, a.id64 ? 8 : 4) || off_size(history_length, 4) ||
       off_size(repetition, 4) || off_size(presence, 4) || off_size(frequency, 4) || off_size(bias, 4) || off_size(mask, 4))
     return LSTM_ERR_ALIGN;
+  if (penalty_overlap(a, logits, out, e)) return LSTM_ERR_DIMS;
   a.logits = logits; a.history = history; a.length = (const int32_t*)history_length;
   a.repetition = repetition; a.presence = presence; a.frequency = frequency;
   a.bias = bias; a.mask = mask; a.out = out;

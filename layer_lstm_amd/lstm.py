@@ -824,7 +824,7 @@ class Penalty:
         """logits [N, V] changed by what its row says: history [N, L] of int32 or int64 ids (any strides >= 0: time-major
         ids as ids.t()), the first length [N] (int32) of them counting; repetition, presence, frequency fp32 [N]; bias
         fp32 [V] or [N, V]; mask int32 [N, >= ceil(V / 32)], bit v % 32 of word v / 32 zero = not allowed.  `out`: where
-        to (logits itself, say); None: the operator's own buffer."""
+        to (logits itself or memory that is not theirs); None: the operator's own buffer."""
         N, V, s, td, dev = self.N, self.V, self.shape, self.tdtype, self._dev
         if logits.dtype is not td or logits.shape != self._rows or (V > 1 and logits.stride(1) != 1):
             raise ValueError(f"logits: [{N}, {V}] of {td}, rows contiguous")
