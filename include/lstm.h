@@ -469,7 +469,8 @@ int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const 
  * length (int32 [B], NULL = all steps; clamped to [0, T]): a step past a
  * sequence's end holds the state and has o = 0 and no gradient; its rows of q,
  * k, v and dout are not used, they may hold anything.  state_out may be state
- * where T <= LSTM_LINATTN_STEP; otherwise no output overlaps an input.
+ * where T <= LSTM_LINATTN_STEP; otherwise no output overlaps an input (one that
+ * begins where an input begins is refused).
  * Gradients: with R_t = a R_{t+1} + scale q_t dout_t^T and a R_T standing for
  * dstate (NULL: zeros), the gradient of state_out,
  *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate0 = a R_0

@@ -169,7 +169,7 @@ int lstm_linattn_fwd(const lstm_linattn_shape* shape, const void* q, const void*
       off_size(state, 4) || off_size(state_out, 4) || ((uintptr_t)workspace & 255u))
     return LSTM_ERR_ALIGN;
   if (rows && workspace_bytes < p.total_fwd) return LSTM_ERR_WORKSPACE;
-  if (state && state == state_out && !p.step) return LSTM_ERR_DIMS;
+  if ((state && state == state_out && !p.step) || (rows && (o == q || o == k || o == v))) return LSTM_ERR_DIMS;
   if (!heads) return LSTM_OK;
   LinArgs a = linattn_args(s, log_decay, length);
   int dma;
@@ -202,6 +202,8 @@ int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const vo
     return LSTM_ERR_ALIGN;
   if (rows && workspace_bytes < p.total_bwd) return LSTM_ERR_WORKSPACE;
   if (dstate && dstate == dstate0) return LSTM_ERR_DIMS;
+  for (const void* in : {dout, q, k, v})
+    if (rows && (in == dq || in == dk || in == dv)) return LSTM_ERR_DIMS;
   if (!heads) return LSTM_OK;
   LinArgs a = linattn_args(s, log_decay, length);
   const int64_t G = s.Hq / s.Hk;
