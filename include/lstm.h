@@ -477,8 +477,9 @@ int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const 
  * (dstate0 NULL: not wanted); nothing of the forward call is needed.
  * Rows of 16-bit types are multiplied as they are; q . k (times powers of a),
  * S and R are rounded to the type as operands of the matrix cores (in fp16
- * times a power of two, so that they neither overflow nor fall among the
- * denormals), and summed, kept and handed over in fp32.  A step that is not
+ * times a power of two, each step's q . k and each column of v its own, so that
+ * they neither overflow nor fall among the denormals), and summed, kept and
+ * handed over in fp32.  A step that is not
  * finite may also reach the outputs of the 31 steps before it.
  * Any D, Dv in [1, 256]; scale finite; T < 2^26, B, Hq < 2^20, B Hq < 2^18; rows of
  * whole aligned 16-byte chunks (t stride included) are the fast case. */

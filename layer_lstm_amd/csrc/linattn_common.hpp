@@ -115,10 +115,22 @@ __device__ __forceinline__ float log2_decay(const float* log_decay, int h) {
   return (x > 0.f ? 0.f : x) * kLog2e;
 }
 
-// The power of two that brings the largest of a wave's values to [2^13, 2^14)
-// (1 where there is none, or it is not finite): operands in fp16 are scaled by
-// it, so that sums beyond 65504 and values among its denormals keep their bits.
-__device__ __forceinline__ float lift_of(float most) {
+// fp16: operands are scaled by powers of two, so that sums beyond 65504 and
+// values among its denormals keep their bits.  Columns of V, and with them of the
+// state, and rows of P each have their own (a lane holds one), so that none loses
+// its bits to a larger one beside it; the state as an operand has one for all of
+// a wave's (a column counts from 2^-27 of the largest on, and its outputs are
+// fp16).
+// The power of two that brings x (>= 0) to [2^13, 2^14); 1 where x is 0 or not
+// finite; from 2^lo to 2^hi.
+__device__ __forceinline__ uint32_t lift_bits(float x, int lo, int hi) {
+  const int e = (int)(__float_as_uint(x) >> 23), r = e == 0 || e == 255 ? 127 : 127 + 13 + 127 - e;
+  return (uint32_t)(r < 127 + lo ? 127 + lo : r > 127 + hi ? 127 + hi : r);
+}
+__device__ __forceinline__ float power_of_two(uint32_t bits) { return __uint_as_float(bits << 23); }
+__device__ __forceinline__ float inverse(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
+// The largest of a wave's values.
+__device__ __forceinline__ float wave_max(float most) {
   auto from = [&](auto ctl) {
     const uint32_t v = __float_as_uint(most);
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, decltype(ctl)::value, 0xf, 0xf, false));
@@ -130,10 +142,7 @@ __device__ __forceinline__ float lift_of(float most) {
   most = fmaxf(most, from(integral_constant<int, 0x128>{}));  // row_ror:8
   const auto r16 = __builtin_amdgcn_permlane16_swap(__float_as_uint(most), __float_as_uint(most), false, false);
   most = fmaxf(__uint_as_float(r16[0]), __uint_as_float(r16[1]));
-  most = fmaxf(most, other_half(most));
-  const uint32_t e = __float_as_uint(most) >> 23;  // exponent (most >= 0)
-  const uint32_t r = e == 0 || e == 255 ? 127u : 127u + 13u + 127u - e;
-  return __uint_as_float(__builtin_amdgcn_readfirstlane((r < 1 ? 1u : r > 253 ? 253u : r) << 23));
+  return fmaxf(most, other_half(most));
 }
 
 template <int N>
@@ -277,7 +286,10 @@ linattn_kernel(LinArgs args) {
         S[dt][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
       }
   }
-  float lift = 1.f;  // fp16: S holds the state times this power of two
+  // fp16: S holds this lane's column of the state times a power of two; a bound
+  // of its values, so that they stay below 2^100 with it: the power follows V, and
+  // steps that have nearly died away would raise it past what fp32 holds
+  float lift = 1.f, bound = 0.f;
 
   // Weights of P (row j = reg_row, column i = lane; times scale) and of V in the
   // state's sum (backwards times scale).  They count from the chunk's end forwards in time and from its
@@ -458,9 +470,18 @@ linattn_kernel(LinArgs args) {
   for (int dt = 0; dt < NDT; ++dt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) asm volatile("" : "+v"(S[dt][i]));
+  auto most_of_state = [&]() __attribute__((always_inline)) {
+    float most = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < NDT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(S[dt][i]));
+    return most;
+  };
+  if constexpr (kHalf && !state_only) bound = most_of_state();
 
   f32x16_t O = zero16();
-  float s_by = 1.f, undo = 1.f;       // fp16: of the state as an operand
+  float s_by = 1.f, undo = 1.f;       // fp16: of the state as an operand, and back
   u32x4_t s_op[KIND == kMany ? KB : 1];
   // the state as the operand of k-block kb
   auto state_operand = [&](int kb) __attribute__((always_inline)) {
@@ -496,7 +517,7 @@ linattn_kernel(LinArgs args) {
     // done between the products of the rows, which it covers
     constexpr int kParts = sizeof(T) == 4 ? 1 : kHalf ? 2 : 3;
     u32x4_t vf[PB], vw[PB][kParts];
-    float un = 1.f;  // fp16: O's factor before it is complete
+    float un = 1.f;  // fp16: O's factor (of this lane's row) before it is complete
     float most_v = 0.f, vx[kHalf ? PB : 1][EB];
     const bool update = KIND != kMany || last;
     auto split = [&](int pb, float* f) __attribute__((always_inline)) {
@@ -552,13 +573,11 @@ linattn_kernel(LinArgs args) {
       if (KIND != kSum || first) {
         if constexpr (kHalf) {
           if (first) {
-            float most = 0.f;
-#pragma unroll
-            for (int dt = 0; dt < NDT; ++dt)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(S[dt][i]));
-            s_by = lift_of(most);
-            undo = 1.f / s_by / lift;
+            const float down = inverse(lift), most = most_of_state() * down;
+            // (a column that is not finite gives no number anyway)
+            const float by = power_of_two(__builtin_amdgcn_readfirstlane(lift_bits(wave_max(most < INFINITY ? most : 0.f), -126, 60)));
+            s_by = by * down;
+            undo = inverse(by);
           }
         }
         if constexpr (KIND == kMany) {  // kept over the chunk's heads
@@ -608,7 +627,7 @@ linattn_kernel(LinArgs args) {
         float most = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(P[i]));
-        by = lift_of(most);
+        by = power_of_two(lift_bits(fmaxf(most, other_half(most)), -126, 40));  // (O times it stays in range)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           P[i] *= by;
@@ -617,14 +636,17 @@ linattn_kernel(LinArgs args) {
       }
 #pragma unroll
       for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(vf[pb], TK::reg_frag(P, pb), O);
-      if constexpr (kHalf) un = __uint_as_float((254u << 23) - __float_as_uint(by));  // 1 / by, a power of two
+      if constexpr (kHalf) un = inverse(by);
     }
 
     if (update) {
       float keep = (KIND == kSum || state_only) && !first ? 1.f : n < 32 ? power(ld2, n) : keep32;
       if constexpr (kHalf) {
-        const float to = lift_of(most_v);
-        keep *= to / lift;
+        const float most = fmaxf(most_v, other_half(most_v));
+        bound = bound * keep + most * 0x1p21f;  // (32 steps, keys up to 65504)
+        const int cap = 354 - (int)(__float_as_uint(bound) >> 23), r = (int)lift_bits(most, -36, 90);
+        const float to = power_of_two((uint32_t)(r < cap ? r : cap));  // (of 2^100 / bound, 2^-28 and more)
+        keep *= to * inverse(lift);
         lift = to;
 #pragma unroll
         for (int pb = 0; pb < PB; ++pb) {
@@ -697,7 +719,7 @@ linattn_kernel(LinArgs args) {
     to = x.s_out + head * state_size;
   }
   if (to) {
-    const float by = 1.f / lift;
+    const float by = inverse(lift);
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)to, 0, (int)state_size * 4, 0x00020000);
     const int ln = tile_lane<true>(lane), dv = dv0 + 32 * w + (ln & 31);
 #pragma unroll
