@@ -145,6 +145,48 @@ __device__ __forceinline__ float wave_max(float most) {
   return fmaxf(most, other_half(most));
 }
 
+// The product whose zeros make zero of anything, NaN and infinities too
+// (v_mul_legacy_f32; the intrinsic has no builtin).
+__device__ float mul_zero(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
+
+// sum, or NaN where one of the 16 bytes' values is not finite.
+template <typename T>
+__device__ __forceinline__ float add_zeros(u32x4_t v, float sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t word = v[i];  // (a bit cast of v[i] itself takes the vector's first element)
+    if constexpr (std::is_same<T, bf16_t>::value) {
+      typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+      sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(pair_t, word), __builtin_bit_cast(pair_t, 0u), sum, false);
+    } else if constexpr (std::is_same<T, f16_t>::value) {
+      typedef _Float16 pair_t __attribute__((ext_vector_type(2)));
+      sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(pair_t, word), __builtin_bit_cast(pair_t, 0u), sum, false);
+    } else {
+      sum = __builtin_fmaf(__uint_as_float(word), 0.f, sum);
+    }
+  }
+  return sum;
+}
+// Zeros in place of a fragment's values that are not finite; `edge` moves to the
+// row of each (frag_row) that is before it, or behind it with `rev`.
+template <typename T>
+__device__ __forceinline__ u32x4_t finite_only(u32x4_t v, int pb, int lane, bool rev, int* edge) {
+  constexpr uint32_t kExponent = sizeof(T) == 4 ? 0x7f800000u : std::is_same<T, f16_t>::value ? 0x7c00u : 0x7f80u;
+  constexpr int kEach = 4 / (int)sizeof(T), kBits = 32 / kEach;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < kEach; ++h) {
+      const uint32_t word = v[i];
+      if (((word >> (kBits * h)) & kExponent) == kExponent) {
+        const int row = frag_row<T>(pb, kEach * i + h, lane);
+        *edge = rev ? (row > *edge ? row : *edge) : (row < *edge ? row : *edge);
+        v[i] = kEach == 1 ? 0u : word & (h ? 0xffffu : 0xffff0000u);
+      }
+    }
+  return v;
+}
+
 template <int N>
 __device__ __forceinline__ void stage_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -298,10 +340,13 @@ linattn_kernel(LinArgs args) {
   const int ri = lane & 31;
   const float scale = args.scale;
   float wp[16], wv[PB][EB];
+  // (0 is for the rows that have no part in a step; what underflows is not)
+  const float least = scale != 0.f ? 0x1p-149f : 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int j = reg_row(i, lane), e = rev ? j - ri : ri - j;
-    wp[i] = e < 0 ? 0.f : power(ld2, e) * scale;
+    const float x = power(ld2, e < 0 ? 0 : e) * scale;
+    wp[i] = e < 0 ? 0.f : x == 0.f ? least : x;
   }
 #pragma unroll
   for (int pb = 0; pb < PB; ++pb)
@@ -478,7 +523,15 @@ linattn_kernel(LinArgs args) {
       for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(S[dt][i]));
     return most;
   };
-  if constexpr (kHalf && !state_only) bound = most_of_state();
+  if constexpr (kHalf && !state_only) {
+#pragma unroll
+    for (int dt = 0; dt < NDT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float x = fabsf(S[dt][i]);
+        bound = fmaxf(bound, x < INFINITY ? x : 0.f);
+      }
+  }
 
   f32x16_t O = zero16();
   float s_by = 1.f, undo = 1.f;       // fp16: of the state as an operand, and back
@@ -559,16 +612,22 @@ linattn_kernel(LinArgs args) {
       for (int pb = 0; pb < PB; ++pb) weigh(pb);
     } else {
       f32x16_t P = zero16();
+      float zeros = 0.f;  // NaN where a value of V is not finite
       // fragments of V are weighed after the products of these k-blocks
       auto weigh_at = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
         for (int pb = 0; pb < PB; ++pb)
-          if (kb == ((pb + 1) * KB + PB - 1) / PB - 1) weigh(pb);
+          if (kb == ((pb + 1) * KB + PB - 1) / PB - 1) {
+            weigh(pb);
+            zeros = add_zeros<T>(vf[pb], zeros);
+          }
       };
       // rows of a and k in turn, k-block by k-block
       u32x4_t af;
-      // (fewer where the registers are full)
-      Ahead<2 * KB, NDT * sizeof(T) >= 8 && KIND != kOne ? kAheadRows - 2 : kAheadRows> rows;
+      // (fewer where the registers are full: 64 sequences, 16 heads of 64, 256 steps,
+      // bf16, backward 80 us with six ahead, 66 with four, 64 with three)
+      constexpr int kFewer = DP == 64 && KS == 1 && KIND == kOne ? 3 : NDT * sizeof(T) >= 8 && KIND != kOne ? 2 : 0;
+      Ahead<2 * KB, kAheadRows - kFewer> rows;
       auto read_rows = [&](int f) __attribute__((always_inline)) { return TK::row_at(f & 1 ? keys_at : rows_at, f >> 1); };
       if (KIND != kSum || first) {
         if constexpr (kHalf) {
@@ -620,8 +679,20 @@ linattn_kernel(LinArgs args) {
           weigh_at(f >> 1);
         });
       }
+      // Values of V that are not finite would reach, times zero, the rows that
+      // have no part in their steps: they are taken out, and their columns become
+      // NaN from their step on.  (Forward and backward of 8 sequences, 16 heads of
+      // 128, us: 4096 steps of bf16 168 and 354, with it 173 and 358; 2048 of fp32
+      // 273 and 809, with it 279 and 830.)
+      const bool odd = __any(zeros != 0.f);
+      int edge = rev ? -1 : 32;
+      if (__builtin_expect(odd, 0)) {  // (nothing of it is kept in registers over the chunks)
+        const int ln = tile_lane<true>(lane);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) P[i] *= wp[i];
+        for (int pb = 0; pb < PB; ++pb) vf[pb] = finite_only<T>(vf[pb], pb, ln, rev, &edge);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) P[i] = mul_zero(P[i], wp[i]);
       float by = 1.f;
       if constexpr (kHalf) {
         float most = 0.f;
@@ -636,6 +707,15 @@ linattn_kernel(LinArgs args) {
       }
 #pragma unroll
       for (int pb = 0; pb < PB; ++pb) O = Mm<T>::mac(vf[pb], TK::reg_frag(P, pb), O);
+      if (__builtin_expect(odd, 0)) {
+        const int ln = tile_lane<true>(lane), row = ln & 31, other = __shfl(edge, ln ^ 32);
+        edge = rev ? (other > edge ? other : edge) : (other < edge ? other : edge);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = __shfl(edge, reg_row(i, ln));
+          if (rev ? row <= at : row >= at) O[i] = NAN;
+        }
+      }
       if constexpr (kHalf) un = inverse(by);
     }
 
