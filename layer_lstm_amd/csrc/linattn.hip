@@ -3,6 +3,7 @@
 #include <type_traits>
 
 #include "attend_common.hpp"
+#include "linattn_decay.hpp"
 #include "model_internal.hpp"
 
 namespace lstm {
@@ -116,16 +117,13 @@ __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
     const int64_t l = args.len[b];
     end = l < 0 ? 0 : l < args.T ? l : args.T;
   }
-  float ld2 = args.log_decay[hs];
-  ld2 = (ld2 > 0.f ? 0.f : ld2) * kLog2e;
+  const Decay decay = Decay::of(args.log_decay, hs);
   const int d = e / x.DV, c = e - d * x.DV;
   float S = x.s_in ? x.s_in[head * n + d * x.s_dk + c * x.s_dv] : 0.f;
   float* at = x.seg + head * args.segs * n + e;
   // decays of whole segments, of the one in which the sequence ends, of those past it
   const int whole = (int)(end / args.seg_rows);
-  const float by_whole = __builtin_amdgcn_exp2f(ld2 * (float)args.seg_rows);
-  const int rest = (int)(end - whole * args.seg_rows);
-  const float by_rest = rest == 0 ? 1.f : __builtin_amdgcn_exp2f(ld2 * (float)rest);
+  const Kept by_whole = decay.kept((int)args.seg_rows), by_rest = decay.kept((int)(end - whole * args.seg_rows)), all = {1.f, 0.f};
   constexpr int kAhead = 8;
   for (int o0 = 0; o0 < args.segs; o0 += kAhead) {
     float own[kAhead];
@@ -136,7 +134,7 @@ __global__ void __launch_bounds__(256) linattn_scan_kernel(LinArgs args) {
       const int o = o0 + j, seg = x.rev ? args.segs - 1 - o : o;
       if (o < args.segs) {
         at[(int64_t)o * n] = S;
-        S = S * (seg < whole ? by_whole : seg == whole ? by_rest : 1.f) + own[j];
+        S = (seg < whole ? by_whole : seg == whole ? by_rest : all)(S, own[j]);
       }
     }
   }
@@ -215,7 +213,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
     const int l = args.len[b];
     end = l < 0 ? 0 : l < end ? l : end;
   }
-  const float ld = args.log_decay[hs], decay = __builtin_amdgcn_exp2f((ld > 0.f ? 0.f : ld) * kLog2e);
+  const Decay decay = Decay::of(args.log_decay, hs);
 
   // a step's k, v and first heads of q, read ahead (the first before the state:
   // loads return in order)
@@ -253,6 +251,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
       }
     }
   }
+  const Kept kept = decay.kept(1);
   for (int t = 0; t < (int)args.T; ++t) {
     const bool real = t < end;
     if (real) {
@@ -286,7 +285,7 @@ __global__ void __launch_bounds__(256) linattn_step_kernel(LinArgs args) {
             if (g0 == 0) {
               const float k = ks[d];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) S[r][j] = S[r][j] * decay + k * v[j];
+              for (int j = 0; j < 4; ++j) S[r][j] = kept(S[r][j], k * v[j]);
             }
 #pragma unroll
             for (int g = 0; g < HB; ++g)
