@@ -8,9 +8,9 @@ independent: r of them of at most u32 of the state, in the square mean u32 /
 sqrt(3), over n steps or chunks sqrt(n r / 3) u32.  Tokens: r = 2, bound
 2 sqrt(n) u32 (2.4 times that); chunks of fp32: a product and the matrix cores'
 sums of 32 steps, r = 17, bound 6 sqrt(n) u32 (2.5 times), in segments (their
-sums are of 8 chunks here) for all types.  The terms are positive, so that a decay's error does
-not average out: with one of 2^-25 a time it is n u32 / 4 for memories longer
-than the text."""
+sums are of 8 chunks here) for all types.  The terms are positive, so that a
+decay's error does not average out: with one of 2^-25 a time it is n u32 / 4 for
+memories longer than the text."""
 import math
 
 import numpy as np
