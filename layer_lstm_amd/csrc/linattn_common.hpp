@@ -448,9 +448,8 @@ linattn_kernel(LinArgs args) {
       pass = pass == lds0 + LL::kAtPass ? pass + kPassed : lds0 + LL::kAtPass;
     }
     if (whole_o) {
-      if constexpr (sizeof(T) == 2 && kKeep == 4) {
-        if (there) *(uint2*)(p + 4 * (lane >> 5)) = make_uint2(pack2<T>(keep_o[0], keep_o[1]), pack2<T>(keep_o[2], keep_o[3]));
-      } else if constexpr (sizeof(T) == 2) {
+      if constexpr (sizeof(T) == 2) {
+        static_assert(kKeep % 8 == 0, "whole chunks of 16 bytes (KS = 4 is fp32's)");
         u32x4_t q[kKeep / 8];
 #pragma unroll
         for (int i = 0; i < kKeep / 8; ++i) {

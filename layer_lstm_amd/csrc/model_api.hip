@@ -49,13 +49,13 @@ struct Rows {
   int64_t D;
 };
 // A run's tensors; *dma: all of them are whole aligned chunks that one descriptor reaches.
-static LinRun linattn_run(const Rows& a, const Rows& k, const Rows& v, void* out, const lstm_stride& os, int64_t Ha, int64_t ga,
-                          int64_t gb, int rev, int64_t e, int* dma) {
+static LinRun linattn_run(const Rows& a, const Rows& k, const Rows& v, void* out, const lstm_stride& os, int64_t ga, int64_t gb,
+                          int rev, int64_t e, int* dma) {
   LinRun r = {};
   r.a = a.p; r.k = k.p; r.v = v.p; r.out = out;
   r.as = a.s; r.ks = k.s; r.vs = v.s; r.os = os;
   r.DK = (int)k.D; r.DV = (int)v.D;
-  r.Ha = (int)Ha; r.ga = (int)ga; r.gb = (int)gb;
+  r.ga = (int)ga; r.gb = (int)gb;
   r.rev = rev;
   r.whole = (whole_rows(a.p, a.s, a.D, e) ? kWholeQ : 0) | (whole_rows(k.p, k.s, k.D, e) ? kWholeK : 0) |
             (whole_rows(v.p, v.s, v.D, e) ? kWholeV : 0) | (whole_rows(out, os, v.D, e) ? kWholeO : 0);
@@ -174,7 +174,7 @@ int lstm_linattn_fwd(const lstm_linattn_shape* shape, const void* q, const void*
   LinArgs a = linattn_args(s, log_decay, length);
   int dma;
   a.runs = 1;
-  a.run[0] = linattn_run({q, s.q, s.D}, {k, s.k, s.D}, {v, s.v, s.Dv}, o, s.o, s.Hq, s.Hq / s.Hk, 1, 0, e, &dma);
+  a.run[0] = linattn_run({q, s.q, s.D}, {k, s.k, s.D}, {v, s.v, s.Dv}, o, s.o, s.Hq / s.Hk, 1, 0, e, &dma);
   LinRun& r = a.run[0];
   r.s_in = state; r.s_out = state_out;
   r.s_dk = s.Dv; r.s_dv = 1;
@@ -210,9 +210,9 @@ int lstm_linattn_bwd(const lstm_linattn_shape* shape, const void* dout, const vo
   const Rows rq = {q, s.q, s.D}, rk = {k, s.k, s.D}, rv = {v, s.v, s.Dv}, rg = {dout, s.dout, s.Dv};
   int dma[3];
   a.runs = 3;
-  a.run[0] = linattn_run(rg, rv, rk, dq, s.dq, s.Hq, G, 1, 0, e, &dma[0]);   // state S^T
-  a.run[1] = linattn_run(rv, rg, rq, dk, s.dk, s.Hk, 1, G, 1, e, &dma[1]);   // state R^T
-  a.run[2] = linattn_run(rk, rq, rg, dv, s.dv, s.Hk, 1, G, 1, e, &dma[2]);   // state R
+  a.run[0] = linattn_run(rg, rv, rk, dq, s.dq, G, 1, 0, e, &dma[0]);   // state S^T
+  a.run[1] = linattn_run(rv, rg, rq, dk, s.dk, 1, G, 1, e, &dma[1]);   // state R^T
+  a.run[2] = linattn_run(rk, rq, rg, dv, s.dv, 1, G, 1, e, &dma[2]);   // state R
   for (int i = 0; i < 3; ++i) {
     LinRun& r = a.run[i];
     r.s_in = i == 0 ? state : dstate;

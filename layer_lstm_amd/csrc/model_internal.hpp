@@ -13,7 +13,6 @@ struct LinRun {
   void* out;
   lstm_stride as, ks, vs, os;
   int DK, DV;
-  int Ha;           // heads of a and out
   int ga, gb;       // heads of a, of k and v, that share a state (one of them 1)
   int rev;          // backwards in time
   const float* s_in;  // [B][Hs] states before the first step, element (dk, dv) at dk s_dk + dv s_dv; null: zeros
