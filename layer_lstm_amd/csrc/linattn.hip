@@ -43,6 +43,22 @@ static LinTile linattn_tile(int64_t DK, int64_t DV, int dtype, bool few) {
 // to itself: it is taken where all of them have one, and no run is long (forward
 // and backward of the fp32 case above 83 us, so 65; 32 heads of 64, 8192 steps,
 // cut into segments either way 466 and 900).
+//   The numbers (bf16, heads of 128, forward and backward, us, where no other is
+// named): work-groups of 64-value rows fill the device with two a compute unit (16
+// sequences, 16 heads of 64, 1024 steps: 40 and 62, with one 47 and 62; 8
+// sequences, 2048 steps: 57 and 93, with one 70 and 108).  Runs are long from 16
+// chunks a compute unit on (2 sequences, 8 heads, 4096 steps: forwards, with 8, 51
+// as they are, 57 as long ones; backwards, with 24, 80 as long ones and 101; 8192
+// steps, with 16 and 48, 75 and 130, 84 and 179 as short ones).  A segment has four
+// chunks at least (1 sequence, 8 heads, 512 steps: 23 and 29, two 21 and 33, eight
+// 26 and 26; fp32 of 64 values 27 and 29, two 21 and 33, eight 49 and 50).  Segments
+// make two work-groups a compute unit (1 sequence, 16 heads, 16384 steps: 109 and
+// 250, one 122 and 292, three 121 and 261), forwards one where rows of 256 values
+// fill it and where runs are short (1 sequence, 8 heads of 256, 8192 steps: 103,
+// two 126; backwards, whose three runs do not end together, 260 and 240; fp32, 4096
+// steps, 572 and 972; 1 sequence, 8 heads, 2048 steps, backwards: 42, one 46, fp32
+// 110 and 181; 4 sequences, 16 heads of 64, 2048 steps, backwards: 67, three for
+// two compute units 64, which 64-value rows take).
 static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int64_t (*sizes)[3], LinCall* c) {
   const int64_t sets = s.B * s.Hk, chunks = (s.T + 31) / 32, most = chunks / 4 > 1 ? chunks / 4 : 1;
   bool fits = true;  // the device has a compute unit for all work-groups, or for the next when the short ones end
@@ -74,11 +90,11 @@ static void plan_call(const lstm_linattn_shape& s, int cus, int runs, const int6
       n = fine;
     } else if (long_runs && !small) {
       n = groups(false);
-      segs = (c->tile[0].dp == 256 ? 3 * full / 2 : 2 * full) / n;
+      segs = (runs == 1 && c->tile[0].dp == 256 ? full : 2 * full) / n;
     } else {
       n = fine;
       const int64_t fill = c->tile[0].nw == 1 ? cus : full;
-      segs = (runs > 1 ? 3 * fill / 2 : fill) / n;  // (the three runs of a backward do not end together)
+      segs = (runs == 1 ? fill : small ? 3 * fill / 2 : 2 * fill) / n;
     }
     if (segs > most) segs = most;
     if (segs < 3) segs = 1;
