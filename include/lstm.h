@@ -479,8 +479,9 @@ int lstm_logprob_bwd(const lstm_logprob_shape* shape, const void* logits, const 
  * S and R are rounded to the type as operands of the matrix cores (in fp16
  * times a power of two, each step's q . k and each column of v its own, so that
  * they do not overflow, and none above 2^-27 of the largest with the same power
- * falls among the denormals), and summed, kept and handed over in fp32.  What depends on a value that is not finite is not
- * finite (an infinity may be NaN); nothing else is.
+ * falls among the denormals), and summed, kept and handed over in fp32.  What
+ * depends on a value that is not finite is not finite (an infinity may be NaN);
+ * nothing else is.
  * Any D, Dv in [1, 256]; scale finite; T < 2^26, B, Hq < 2^20, B Hq < 2^18; rows of
  * whole aligned 16-byte chunks (t stride included) are the fast case. */
 #define LSTM_LINATTN_STEP 8
