@@ -491,8 +491,8 @@ def _capturing(stream):
         return torch.cuda.is_current_stream_capturing()
 
 
-def _settle():
-    torch.cuda.current_stream().synchronize()
+def _settle(index):
+    torch.cuda.current_stream(index).synchronize()
 
 
 def _workspace(fn, name, shape, device):
@@ -956,7 +956,7 @@ class AdamW:
                 raise LstmError(rc, "lstm_adamw_query")
             self.workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
             self.control = torch.zeros(ctypes.sizeof(AdamwControl) // 8, dtype=torch.int64, device=device)
-        _settle()  # the states are filled before a step on any stream reads them
+        _settle(self._dev)  # the states are filled before a step on any stream reads them
 
     def set_step(self, t, stream=None):
         """t steps have been taken (0 at the start); `stream`: the one that the next step goes to."""

@@ -5,13 +5,19 @@ torch = pytest.importorskip("torch")
 
 
 @pytest.fixture
-def lstm(monkeypatch):
+def settled():
+    """The devices whose current stream was waited for."""
+    return []
+
+
+@pytest.fixture
+def lstm(monkeypatch, settled):
     """The binding with buffers in host memory and cuda:0 the current device."""
     from layer_lstm_amd import lstm as mod
     zeros = torch.zeros
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(mod, "_on_device", lambda *a: None)
-    monkeypatch.setattr(mod, "_settle", lambda: None)
+    monkeypatch.setattr(mod, "_settle", settled.append)
     monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
     return mod
 
@@ -25,3 +31,9 @@ def test_the_copy_is_no_part_of_a_graph(lstm):
         assert torch.equal(opt.master[at : at + p.numel()], p.detach().float().reshape(-1))
     opt.master.copy_(torch.ones_like(opt.master))
     opt.master.numpy()
+
+
+def test_the_filling_that_is_waited_for_is_that_of_the_states_device(lstm, settled):
+    lstm.AdamW([torch.zeros(4)], device="cuda:1")
+    lstm.AdamW([torch.zeros(4)])
+    assert settled == [1, 0]
